@@ -21,7 +21,8 @@
  *     alignments the kernels do not handle). Launch failures return
  *     NVFP4MOE_EHIP. Faults inside kernels surface at the caller's next sync.
  *   - Inputs must be finite (no NaN/Inf); this is a precondition, not checked.
- *   - Device pointers must be 16-byte aligned.
+ *   - Device pointers must be 16-byte aligned (routing and gradient clipping:
+ *     see there).
  *   - Group offsets (`offsets`, `padded_offsets`) live on the device: they are
  *     produced by moe_permute and never copied to the host, so grids are sized
  *     for the capacity (`m_cap`, `P`) and kernels read the real extents.
@@ -45,8 +46,10 @@
  *     block rather than a column slice of a [K, E*N] matrix;
  *   - entry points beyond the seven of the path: the all-MXFP8 forward, the
  *     routed FFN's combine and intermediate quantizer, the 16x16-tile and
- *     NVFP4-backward variants, the one-pass dual dY quantizer and
- *     moe_permute_noalloc.
+ *     NVFP4-backward variants, the one-pass dual dY quantizer,
+ *     moe_permute_noalloc, and what trains around the layer: the router's
+ *     selection with its statistics and backward, the balance loss, and the
+ *     global gradient norm with clipping.
  *
  * Formats (NVFP4 and MXFP8 as named on "Inkling 2 Small uses four-bit
  * training ..." (ai-primer), section "Block scales and per-token activations"):
@@ -94,6 +97,9 @@ enum nvfp4moe_orientation { NVFP4MOE_ROWWISE = 0, NVFP4MOE_COLWISE_GROUPED = 1 }
 
 /* Output layout of the NVFP4 backward's transposes (nvfp4_requant_sr). */
 enum nvfp4moe_layout { NVFP4MOE_LAYOUT_TRANSPOSED = 0, NVFP4MOE_LAYOUT_PER_GROUP = 1 };
+
+/* Scores of the router (moe_route). */
+enum nvfp4moe_score { NVFP4MOE_SCORE_SOFTMAX = 0, NVFP4MOE_SCORE_SIGMOID = 1 };
 
 /* Version of this ABI (NVFP4MOE_ABI_VERSION). */
 NVFP4MOE_API int nvfp4moe_abi_version(void);
@@ -499,6 +505,102 @@ NVFP4MOE_API int moe_bwd_wgrad_nvfp4(const uint8_t* dyT_codes, const uint8_t* dy
                         const uint8_t* xT_scales, const float* xT_outer,
                         const int64_t* padded_offsets, int G, int64_t P, int64_t N, int64_t K,
                         float* dw, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Routing and gradient clipping: what trains around the expert layer. The
+ * pages give the routing's size only ("Thinking Machines' Inkling 2 Small
+ * Trains a 594B Model in 68 Hours" (hermes-ai), section "594B weights, 17B at
+ * work": 8 of 384 experts); the formulas are the ones written here. Pointers of
+ * these calls need the alignment of their elements only (workspaces 16 bytes).
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of device workspace moe_route needs for its statistics (none without). */
+NVFP4MOE_API size_t nvfp4moe_route_workspace_size(int64_t T, int E);
+
+/*
+ * The router's selection: k experts and their gates for each token, and the
+ * per-expert statistics of the balance loss from the same pass.
+ *
+ * logits [T, E] float32 or bfloat16. A logit of -inf closes its expert for
+ * that token (others must be finite: NaN is never selected, and what a row
+ * holding NaN or +inf gives for gates and statistics is not defined; ids stay
+ * in range). score: NVFP4MOE_SCORE_SOFTMAX, s_e = exp(x_e) / sum_i exp(x_i);
+ * NVFP4MOE_SCORE_SIGMOID, s_e = 1 / (1 + exp(-x_e)).
+ * bias [E] float32 or NULL (SIGMOID only, EUNSUPPORTED otherwise): used for
+ * the choice alone; -inf closes the expert for every token's choice.
+ * token_mask [T] bytes or NULL: 0 marks padding, a token with no experts.
+ * topk_ids [T, k] int32: the k open experts of largest x_e, or with a bias of
+ * largest s_e + bias_e (computed in 64 bits), in descending order, the lower
+ * index first among equals; slots past the last open expert hold -1.
+ * gate [T, k] float32: scale * s_j, with renorm != 0 scale * s_j / (sum of the
+ * selected s; gates 0 where that sum is 0); 0 in slots of -1.
+ * counts [E + 1] int64, prob_sum [E] float32 (both or neither NULL):
+ * counts[e] = selected pairs of expert e, counts[E] = tokens with at least one
+ * expert; prob_sum[e] = sum over those tokens of s_te (SIGMOID: of
+ * s_te / sum_i s_ti). Both are overwritten, and the same inputs give the same
+ * bits. Sums over ranks may replace them before the calls below.
+ * workspace: nvfp4moe_route_workspace_size() bytes when counts is given.
+ * Requires E <= 1024, k <= 64, k <= E, T * k < 2^31. T may be 0.
+ */
+NVFP4MOE_API int moe_route(const void* logits, int logits_dtype, int64_t T, int E, int k, int score,
+              int renorm, float scale, const float* bias, const uint8_t* token_mask,
+              int32_t* topk_ids, float* gate, int64_t* counts, float* prob_sum, void* workspace,
+              size_t workspace_bytes, void* stream);
+
+/*
+ * The balance loss of moe_route's statistics:
+ *   loss[0] = alpha * E * sum_e counts[e] / (N k) * prob_sum[e] / N, N = counts[E]
+ * (alpha for a uniform load; 0 when N is 0), sums in 64 bits. Its gradient is
+ * part of moe_route_bwd, the counts being constants of it.
+ */
+NVFP4MOE_API int moe_balance_loss(const int64_t* counts, const float* prob_sum, int E, int k, float alpha,
+                     float* loss, void* stream);
+
+/*
+ * Backward of moe_route and moe_balance_loss to the logits.
+ *
+ * logits, E, k, score, renorm, scale as given to moe_route; topk_ids as it
+ * wrote them (an index outside [0, E) is an empty slot; one expert twice in a
+ * row counts twice); dgate [T, k] float32, the gates' gradient (empty slots
+ * are not read), or NULL for none. counts [E + 1] or NULL for no balance loss;
+ * dloss: device pointer to the loss's gradient, NULL for 1.
+ * dlogits [T, E], of the logits' type: sum of both gradients, rounded once;
+ * 0 for tokens without an expert and for closed experts. dlogits may be
+ * logits. Same size limits as moe_route.
+ */
+NVFP4MOE_API int moe_route_bwd(const void* logits, int logits_dtype, int64_t T, int E, int k, int score,
+                  int renorm, float scale, const int32_t* topk_ids, const float* dgate,
+                  const int64_t* counts, float alpha, const float* dloss, void* dlogits,
+                  void* stream);
+
+/* Bytes of device workspace moe_grad_sumsq needs for a list of n tensors. */
+NVFP4MOE_API size_t nvfp4moe_grad_workspace_size(int n);
+
+/*
+ * Sum of the squares of every element of a list of gradients, in 64 bits.
+ *
+ * grads, dtypes, numels: HOST arrays of n entries, read during the call:
+ * device pointers (aligned to their element, not necessarily to 16 bytes),
+ * NVFP4MOE_F32 or NVFP4MOE_BF16, element counts (0 allowed).
+ * sumsq (device): the sum; 0 for an empty list. The same list gives the same
+ * bits. Values of several devices may be added before moe_grad_clip.
+ * Requires n <= 2^20 and at most 2^44 elements in all.
+ */
+NVFP4MOE_API int moe_grad_sumsq(const void* const* grads, const int* dtypes, const int64_t* numels, int n,
+                   double* sumsq, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients clipped by their global norm, sqrt(*sumsq):
+ *   outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6)),
+ * a float32 product rounded to the tensor's type; a norm of infinity gives a
+ * factor of 0, NaN a factor of NaN. norm (device float32) gets the norm before clipping,
+ * unless NULL. outs[i] is grads[i] (in place; left as it is when the factor is
+ * 1) or apart from every gradient; outputs must not overlap one another.
+ * Host arrays, types and limits as moe_grad_sumsq; max_norm >= 0.
+ */
+NVFP4MOE_API int moe_grad_clip(const void* const* grads, void* const* outs, const int* dtypes,
+                  const int64_t* numels, int n, const double* sumsq, float max_norm, float* norm,
+                  void* stream);
 
 #ifdef __cplusplus
 }

@@ -10,11 +10,14 @@ if the library is missing or the tensors are not on a GPU, the calls raise.
 
 from .binding import (  # noqa: F401
     LIB_PATH,
+    GradList,
     NVFP4MOE_BF16,
     NVFP4MOE_F32,
     Nvfp4moeError,
     abi_version,
+    grad_workspace_size,
     lib,
+    moe_balance_loss,
     moe_bwd_dgrad,
     moe_bwd_wgrad,
     moe_combine,
@@ -22,9 +25,13 @@ from .binding import (  # noqa: F401
     moe_fwd_grouped_gemm,
     moe_bwd_wgrad_nvfp4,
     moe_fwd_grouped_gemm_mxfp8,
+    moe_grad_clip,
+    moe_grad_sumsq,
     moe_padded_offsets,
     moe_permute,
     moe_permute_noalloc,
+    moe_route,
+    moe_route_bwd,
     mxfp8_gather_rows,
     mxfp8_quantize,
     mxfp8_quantize_dual,
@@ -36,5 +43,6 @@ from .binding import (  # noqa: F401
     nvfp4_quantize_tile16,
     nvfp4_requant_sr,
     permute_workspace_size,
+    route_workspace_size,
     status_string,
 )

@@ -14,12 +14,14 @@ NVFP4MOE_BF16 = 1
 _OUTER_PER_ROW, _OUTER_PER_GROUP = 0, 1
 _LAYOUT_TRANSPOSED, _LAYOUT_PER_GROUP = 0, 1
 _ROWWISE, _COLWISE_GROUPED = 0, 1
+_SCORES = {"softmax": 0, "sigmoid": 1}
 
 _c_i64 = ctypes.c_int64
 _c_int = ctypes.c_int
 _c_u32 = ctypes.c_uint32
 _c_u64 = ctypes.c_uint64
 _c_size = ctypes.c_size_t
+_c_f32 = ctypes.c_float
 _p = ctypes.c_void_p
 
 # name -> argument types (all return int status, except where noted)
@@ -59,6 +61,15 @@ SIGNATURES = {
                                    _c_u32, _p, _p, _p, _p], _c_int),
     "moe_bwd_wgrad_nvfp4": ([_p, _p, _p, _p, _p, _p, _p, _c_int, _c_i64, _c_i64, _c_i64, _p, _p],
                             _c_int),
+    "nvfp4moe_route_workspace_size": ([_c_i64, _c_int], _c_size),
+    "moe_route": ([_p, _c_int, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_f32, _p, _p, _p, _p, _p,
+                   _p, _p, _c_size, _p], _c_int),
+    "moe_balance_loss": ([_p, _p, _c_int, _c_int, _c_f32, _p, _p], _c_int),
+    "moe_route_bwd": ([_p, _c_int, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_f32, _p, _p, _p,
+                       _c_f32, _p, _p, _p], _c_int),
+    "nvfp4moe_grad_workspace_size": ([_c_int], _c_size),
+    "moe_grad_sumsq": ([_p, _p, _p, _c_int, _p, _p, _c_size, _p], _c_int),
+    "moe_grad_clip": ([_p, _p, _p, _p, _c_int, _p, _c_f32, _p, _p], _c_int),
 }
 
 _LIB = None
@@ -641,3 +652,235 @@ def moe_bwd_wgrad_nvfp4(dyT, xT, padded_offsets, N, K, dw=None):
                                    int(K), _ptr(dw), _stream(dyT[0]))
     _check("moe_bwd_wgrad_nvfp4", st)
     return dw
+
+
+# ------------------------------------------ routing and gradient clipping
+
+def _launch(dev, name, *args):
+    """Call the library with ``dev`` as the current device (the stream that
+    ends the arguments is one of it) and check the status."""
+    torch = _torch()
+    f = getattr(lib(), name)
+    args = args + (torch.cuda.current_stream(dev).cuda_stream,)
+    if torch.cuda.current_device() == dev.index:
+        st = f(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args)
+    _check(name, st)
+
+
+def _buf(t, name, dtype, shape, dev):
+    """An output buffer: the caller's, checked, or a new one."""
+    if t is None:
+        return _torch().empty(shape, dtype=dtype, device=dev)
+    _dev(t, name, dtype)
+    if tuple(t.shape) != tuple(shape) or t.device != dev:
+        raise ValueError(f"{name} must have shape {tuple(shape)} on {dev} "
+                         f"(got {tuple(t.shape)} on {t.device})")
+    return t
+
+
+def _on(t, name, dtype, shape, dev):
+    """An input that goes with another one: its type, shape and device."""
+    _dev(t, name, dtype)
+    if tuple(t.shape) != tuple(shape) or t.device != dev:
+        raise ValueError(f"{name} must have shape {tuple(shape)} on {dev} "
+                         f"(got {tuple(t.shape)} on {t.device})")
+    return t.data_ptr()
+
+
+def _score(score):
+    if score not in _SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid' (got {score!r})")
+    return _SCORES[score]
+
+
+def route_workspace_size(T, E):
+    return int(lib().nvfp4moe_route_workspace_size(int(T), int(E)))
+
+
+def moe_route(logits, k, score="softmax", renorm=True, scale=1.0, bias=None, token_mask=None,
+              stats=False, workspace=None, out=None):
+    """Select k experts per token of logits [T, E] (bf16|f32; -inf closes an
+    expert). Returns a dict with topk_ids int32 [T, k] (-1: no expert left),
+    gate f32 [T, k], and with ``stats`` counts int64 [E+1] (pairs on each
+    expert, then the tokens that have one) and prob_sum f32 [E].
+
+    score 'softmax' or 'sigmoid'; renorm: gates divided by their sum; bias f32
+    [E] ('sigmoid' only) shifts the choice, not the gates; token_mask bool or
+    uint8 [T], False for padding; ``out`` may hold any of the results' buffers."""
+    torch = _torch()
+    _dev(logits, "logits", ndim=2)
+    T, E = logits.shape
+    k = int(k)
+    dev = logits.device
+    o = {} if out is None else dict(out)
+    ids = o["topk_ids"] = _buf(o.get("topk_ids"), "topk_ids", torch.int32, (T, k), dev)
+    gate = o["gate"] = _buf(o.get("gate"), "gate", torch.float32, (T, k), dev)
+    counts = prob_sum = ws = None
+    ws_bytes = 0
+    if stats:
+        counts = o["counts"] = _buf(o.get("counts"), "counts", torch.int64, (E + 1,), dev)
+        prob_sum = o["prob_sum"] = _buf(o.get("prob_sum"), "prob_sum", torch.float32, (E,), dev)
+        ws_bytes = route_workspace_size(T, E)
+        if workspace is None:
+            workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=dev)
+        else:
+            _dev(workspace, "workspace", torch.uint8)
+            if workspace.device != dev:
+                raise ValueError(f"workspace must be on {dev}")
+            ws_bytes = workspace.numel()
+        counts, prob_sum, ws = counts.data_ptr(), prob_sum.data_ptr(), workspace.data_ptr()
+    if token_mask is not None and token_mask.dtype == torch.bool:
+        token_mask = token_mask.view(torch.uint8)
+    _launch(dev, "moe_route", logits.data_ptr(), _in_dtype(logits), T, E, k, _score(score),
+            int(bool(renorm)), float(scale),
+            None if bias is None else _on(bias, "bias", torch.float32, (E,), dev),
+            None if token_mask is None else _on(token_mask, "token_mask", torch.uint8, (T,), dev),
+            ids.data_ptr(), gate.data_ptr(), counts, prob_sum, ws, ws_bytes)
+    return o
+
+
+def moe_balance_loss(counts, prob_sum, k, alpha, loss=None):
+    """Balance loss f32 [1] of moe_route's statistics: alpha * E * sum_e
+    counts[e] / (N k) * prob_sum[e] / N with N = counts[E]."""
+    torch = _torch()
+    _dev(prob_sum, "prob_sum", torch.float32, 1)
+    dev, E = prob_sum.device, prob_sum.shape[0]
+    loss = _buf(loss, "loss", torch.float32, (1,), dev)
+    _launch(dev, "moe_balance_loss", _on(counts, "counts", torch.int64, (E + 1,), dev),
+            prob_sum.data_ptr(), E, int(k), float(alpha), loss.data_ptr())
+    return loss
+
+
+def moe_route_bwd(logits, topk_ids, dgate=None, score="softmax", renorm=True, scale=1.0,
+                  counts=None, alpha=0.0, dloss=None, dlogits=None):
+    """dlogits [T, E] (of the logits' type) from the gates' gradient dgate f32
+    [T, k] (None: zero) and, when counts int64 [E+1] is given, the balance
+    loss's: alpha as in moe_balance_loss, dloss f32 [1] on the device (None: 1)."""
+    torch = _torch()
+    _dev(logits, "logits", ndim=2)
+    _dev(topk_ids, "topk_ids", torch.int32, 2)
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    dev = logits.device
+    dlogits = _buf(dlogits, "dlogits", logits.dtype, (T, E), dev)
+    _launch(dev, "moe_route_bwd", logits.data_ptr(), _in_dtype(logits), T, E, k, _score(score),
+            int(bool(renorm)), float(scale), _on(topk_ids, "topk_ids", torch.int32, (T, k), dev),
+            None if dgate is None else _on(dgate, "dgate", torch.float32, (T, k), dev),
+            None if counts is None else _on(counts, "counts", torch.int64, (E + 1,), dev),
+            float(alpha),
+            None if dloss is None else _on(dloss, "dloss", torch.float32, (1,), dev),
+            dlogits.data_ptr())
+    return dlogits
+
+
+class GradList:
+    """The gradients (or their clipped copies) of one device as the calls
+    below take them: contiguous bf16|f32 tensors of any alignment that do not
+    overlap. Made once of buffers that live on; it keeps the tensors, and a
+    tensor whose memory or size has changed since is looked at again."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        self._look()
+
+    def _look(self):
+        torch = _torch()
+        ts = self.tensors
+        self.device = None
+        for i, t in enumerate(ts):
+            _dev(t, f"tensor {i}")
+            if self.device is None:
+                self.device = t.device
+            elif t.device != self.device:
+                raise ValueError(f"tensor {i} is on {t.device}, the first on {self.device}")
+        n = len(ts)
+        self.key = [(t.data_ptr(), t.numel()) for t in ts]
+        spans = sorted((p, p + t.numel() * t.element_size())
+                       for t, (p, m) in zip(ts, self.key) if m)
+        for (_, end), (start, _) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError("tensors overlap (or one is listed twice)")
+        self.spans = spans
+        self.dtypes = tuple(t.dtype for t in ts)
+        self.ptrs = (_p * n)(*[p for p, _ in self.key])
+        self.numels = (_c_i64 * n)(*[m for _, m in self.key])
+        self.codes = (_c_int * n)(*[_in_dtype(t) for t in ts])
+
+    def __len__(self):
+        return len(self.tensors)
+
+    def current(self):
+        if [(t.data_ptr(), t.numel()) for t in self.tensors] != self.key:
+            self._look()
+        return self
+
+
+def _grad_list(grads):
+    return grads.current() if isinstance(grads, GradList) else GradList(grads)
+
+
+def _overlap(a, b):
+    """Whether any span of one list meets any of the other (each sorted, disjoint)."""
+    if not a or not b or a[-1][1] <= b[0][0] or b[-1][1] <= a[0][0]:
+        return False
+    i = j = 0
+    while i < len(a) and j < len(b):
+        if a[i][0] < b[j][1] and b[j][0] < a[i][1]:
+            return True
+        if a[i][1] <= b[j][1]:
+            i += 1
+        else:
+            j += 1
+    return False
+
+
+def grad_workspace_size(n):
+    return int(lib().nvfp4moe_grad_workspace_size(int(n)))
+
+
+def moe_grad_sumsq(grads, sumsq=None, workspace=None):
+    """Sum of squares f64 [1] over a list of gradients (a GradList or tensors)."""
+    torch = _torch()
+    g = _grad_list(grads)
+    dev = g.device
+    if dev is None:
+        if sumsq is None:
+            raise ValueError("an empty list needs sumsq (which device?)")
+        dev = sumsq.device
+    sumsq = _buf(sumsq, "sumsq", torch.float64, (1,), dev)
+    if workspace is None:
+        workspace = torch.empty((grad_workspace_size(len(g)),), dtype=torch.uint8, device=dev)
+    else:
+        _dev(workspace, "workspace", torch.uint8)
+        if workspace.device != dev:
+            raise ValueError(f"workspace must be on {dev}")
+    _launch(dev, "moe_grad_sumsq", g.ptrs, g.codes, g.numels, len(g), sumsq.data_ptr(),
+            workspace.data_ptr(), workspace.numel())
+    return sumsq
+
+
+def moe_grad_clip(grads, sumsq, max_norm, outs=None, norm=None):
+    """Scale a list of gradients by min(1, max_norm / (norm + 1e-6)), norm =
+    sqrt(sumsq) of moe_grad_sumsq (or a sum of several ranks' values): in
+    place, or into ``outs`` (same types and sizes, apart from the gradients).
+    Returns norm f32 [1], the norm before clipping."""
+    torch = _torch()
+    _dev(sumsq, "sumsq", torch.float64)
+    g = _grad_list(grads)
+    dev = sumsq.device
+    o = g
+    if outs is not None and outs is not grads:
+        o = _grad_list(outs)
+        if o.dtypes != g.dtypes or [m for _, m in o.key] != [m for _, m in g.key]:
+            raise ValueError("outs must have the gradients' types and sizes")
+        if o.key != g.key and _overlap(g.spans, o.spans):
+            raise ValueError("outs must be the gradients themselves or apart from them")
+    if any(d not in (None, dev) for d in (g.device, o.device)):
+        raise ValueError(f"sumsq is on {dev}, the gradients or outs elsewhere")
+    norm = _buf(norm, "norm", torch.float32, (1,), dev)
+    _launch(dev, "moe_grad_clip", g.ptrs, o.ptrs, g.codes, g.numels, len(g),
+            _on(sumsq, "sumsq", torch.float64, (1,), dev), float(max_norm), norm.data_ptr())
+    return norm

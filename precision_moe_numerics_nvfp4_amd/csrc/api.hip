@@ -10,6 +10,10 @@ namespace {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+inline bool aligned(const void* p, uintptr_t size) {
+  return reinterpret_cast<uintptr_t>(p) % size == 0;
+}
+
 // The MXFP8 GEMMs address a 256-row operand tile with 32-bit byte offsets.
 constexpr int64_t kMaxGemmRowBytes = (int64_t)0xFFFFFFFF / 257;
 // wgrad ranks the groups by size in shared memory.
@@ -23,6 +27,32 @@ inline hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
   do {                      \
     if (!(cond)) return (code); \
   } while (0)
+
+// The list of tensors of the gradient calls: every entry of a known type, its
+// pointers aligned to that type, each output its own gradient or apart from it.
+int grad_list_status(const void* const* grads, void* const* outs, const int* dtypes,
+                     const int64_t* numels, int n) {
+  if (n > 0) REQUIRE(grads && dtypes && numels, NVFP4MOE_EINVAL);
+  REQUIRE(n <= 1 << 20, NVFP4MOE_EUNSUPPORTED);
+  int64_t total = 0;
+  for (int i = 0; i < n; ++i) {
+    REQUIRE(dtypes[i] == NVFP4MOE_F32 || dtypes[i] == NVFP4MOE_BF16, NVFP4MOE_EINVAL);
+    REQUIRE(numels[i] >= 0, NVFP4MOE_EINVAL);
+    if (numels[i] == 0) continue;
+    REQUIRE(grads[i] && (!outs || outs[i]), NVFP4MOE_EINVAL);
+    const uintptr_t size = dtypes[i] == NVFP4MOE_F32 ? 4 : 2;
+    REQUIRE(numels[i] <= ((int64_t)1 << 44) - total, NVFP4MOE_EUNSUPPORTED);
+    total += numels[i];
+    const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]), bytes = size * (uintptr_t)numels[i];
+    REQUIRE(g % size == 0, NVFP4MOE_EUNSUPPORTED);
+    if (outs) {
+      const uintptr_t o = reinterpret_cast<uintptr_t>(outs[i]);
+      REQUIRE(o % size == 0, NVFP4MOE_EUNSUPPORTED);
+      REQUIRE(o == g || o + bytes <= g || g + bytes <= o, NVFP4MOE_EINVAL);
+    }
+  }
+  return NVFP4MOE_OK;
+}
 
 }  // namespace
 
@@ -403,6 +433,92 @@ int moe_bwd_wgrad_nvfp4(const uint8_t* dyT_codes, const uint8_t* dyT_scales,
   return hip_status(launch_wgrad_nvfp4(dyT_codes, dyT_scales, dyT_outer, xT_codes, xT_scales,
                                        xT_outer, padded_offsets, G, P, N, K, dw,
                                        as_stream(stream)));
+}
+
+size_t nvfp4moe_route_workspace_size(int64_t T, int E) {
+  if (T < 0 || E <= 0) return 0;
+  return route_workspace_bytes(T, E);
+}
+
+int moe_route(const void* logits, int logits_dtype, int64_t T, int E, int k, int score,
+              int renorm, float scale, const float* bias, const uint8_t* token_mask,
+              int32_t* topk_ids, float* gate, int64_t* counts, float* prob_sum, void* workspace,
+              size_t workspace_bytes, void* stream) {
+  REQUIRE(T >= 0 && E > 0 && k > 0, NVFP4MOE_EINVAL);
+  REQUIRE(logits_dtype == NVFP4MOE_F32 || logits_dtype == NVFP4MOE_BF16, NVFP4MOE_EINVAL);
+  REQUIRE(score == NVFP4MOE_SCORE_SOFTMAX || score == NVFP4MOE_SCORE_SIGMOID, NVFP4MOE_EINVAL);
+  REQUIRE((counts == nullptr) == (prob_sum == nullptr), NVFP4MOE_EINVAL);
+  if (T > 0) REQUIRE(logits && topk_ids && gate, NVFP4MOE_EINVAL);
+  if (counts && T > 0) REQUIRE(workspace != nullptr, NVFP4MOE_EINVAL);
+  REQUIRE(E <= 1024 && k <= 64 && k <= E, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(T * (int64_t)k < (int64_t)1 << 31, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(!bias || score == NVFP4MOE_SCORE_SIGMOID, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(aligned(logits, logits_dtype == NVFP4MOE_BF16 ? 2 : 4) && aligned(topk_ids, 4) &&
+              aligned(gate, 4) && aligned(bias, 4) && aligned(counts, 8) && aligned(prob_sum, 4),
+          NVFP4MOE_EUNSUPPORTED);
+  if (counts && T > 0) {
+    REQUIRE(workspace_bytes >= route_workspace_bytes(T, E), NVFP4MOE_EWORKSPACE);
+    REQUIRE(aligned16(workspace), NVFP4MOE_EUNSUPPORTED);
+  }
+  if (T == 0 && !counts) return NVFP4MOE_OK;
+  return hip_status(launch_route(logits, logits_dtype == NVFP4MOE_BF16, T, E, k,
+                                 score == NVFP4MOE_SCORE_SIGMOID, renorm != 0, scale, bias,
+                                 token_mask, topk_ids, gate, counts, prob_sum, workspace,
+                                 as_stream(stream)));
+}
+
+int moe_balance_loss(const int64_t* counts, const float* prob_sum, int E, int k, float alpha,
+                     float* loss, void* stream) {
+  REQUIRE(E > 0 && k > 0, NVFP4MOE_EINVAL);
+  REQUIRE(counts && prob_sum && loss, NVFP4MOE_EINVAL);
+  REQUIRE(E <= 1024 && k <= 64 && k <= E, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(aligned(counts, 8) && aligned(prob_sum, 4) && aligned(loss, 4), NVFP4MOE_EUNSUPPORTED);
+  return hip_status(launch_balance_loss(counts, prob_sum, E, k, alpha, loss, as_stream(stream)));
+}
+
+int moe_route_bwd(const void* logits, int logits_dtype, int64_t T, int E, int k, int score,
+                  int renorm, float scale, const int32_t* topk_ids, const float* dgate,
+                  const int64_t* counts, float alpha, const float* dloss, void* dlogits,
+                  void* stream) {
+  REQUIRE(T >= 0 && E > 0 && k > 0, NVFP4MOE_EINVAL);
+  REQUIRE(logits_dtype == NVFP4MOE_F32 || logits_dtype == NVFP4MOE_BF16, NVFP4MOE_EINVAL);
+  REQUIRE(score == NVFP4MOE_SCORE_SOFTMAX || score == NVFP4MOE_SCORE_SIGMOID, NVFP4MOE_EINVAL);
+  if (T > 0) REQUIRE(logits && topk_ids && dlogits, NVFP4MOE_EINVAL);
+  REQUIRE(E <= 1024 && k <= 64 && k <= E, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(T * (int64_t)k < (int64_t)1 << 31, NVFP4MOE_EUNSUPPORTED);
+  const uintptr_t size = logits_dtype == NVFP4MOE_BF16 ? 2 : 4;
+  REQUIRE(aligned(logits, size) && aligned(dlogits, size) && aligned(topk_ids, 4) &&
+              aligned(dgate, 4) && aligned(counts, 8) && aligned(dloss, 4),
+          NVFP4MOE_EUNSUPPORTED);
+  return hip_status(launch_route_bwd(logits, logits_dtype == NVFP4MOE_BF16, T, E, k,
+                                     score == NVFP4MOE_SCORE_SIGMOID, renorm != 0, scale,
+                                     topk_ids, dgate, counts, alpha, dloss, dlogits,
+                                     as_stream(stream)));
+}
+
+size_t nvfp4moe_grad_workspace_size(int n) { return n < 0 ? 0 : grad_workspace_bytes(n); }
+
+int moe_grad_sumsq(const void* const* grads, const int* dtypes, const int64_t* numels, int n,
+                   double* sumsq, void* workspace, size_t workspace_bytes, void* stream) {
+  REQUIRE(n >= 0 && sumsq && workspace, NVFP4MOE_EINVAL);
+  const int bad = grad_list_status(grads, nullptr, dtypes, numels, n);
+  if (bad != NVFP4MOE_OK) return bad;
+  REQUIRE(workspace_bytes >= grad_workspace_bytes(n), NVFP4MOE_EWORKSPACE);
+  REQUIRE(aligned16(workspace) && aligned(sumsq, 8), NVFP4MOE_EUNSUPPORTED);
+  return hip_status(launch_grad_sumsq(grads, dtypes, numels, n, sumsq, workspace,
+                                      as_stream(stream)));
+}
+
+int moe_grad_clip(const void* const* grads, void* const* outs, const int* dtypes,
+                  const int64_t* numels, int n, const double* sumsq, float max_norm, float* norm,
+                  void* stream) {
+  REQUIRE(n >= 0 && sumsq && (n == 0 || outs), NVFP4MOE_EINVAL);
+  REQUIRE(max_norm >= 0.0f, NVFP4MOE_EINVAL);
+  const int bad = grad_list_status(grads, outs, dtypes, numels, n);
+  if (bad != NVFP4MOE_OK) return bad;
+  REQUIRE(aligned(sumsq, 8) && aligned(norm, 4), NVFP4MOE_EUNSUPPORTED);
+  return hip_status(launch_grad_clip(grads, outs, dtypes, numels, n, sumsq, max_norm, norm,
+                                     as_stream(stream)));
 }
 
 }  // extern "C"

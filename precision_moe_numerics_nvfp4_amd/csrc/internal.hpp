@@ -89,6 +89,28 @@ hipError_t launch_nvfp4_quantize_sr(const void* x, bool bf16, int64_t rows, int6
 hipError_t launch_padded_offsets(const int64_t* offsets, int G, int64_t align, int64_t* padded,
                                  hipStream_t stream);
 
+// route.hip
+constexpr int64_t kMaxRouteParts = 1024;   // workgroups that leave statistics partials
+size_t route_workspace_bytes(int64_t T, int E);
+hipError_t launch_route(const void* logits, bool bf16, int64_t T, int E, int k, bool sigmoid,
+                        bool renorm, float scale, const float* bias, const uint8_t* token_mask,
+                        int32_t* topk_ids, float* gate, int64_t* counts, float* prob_sum,
+                        void* workspace, hipStream_t stream);
+hipError_t launch_balance_loss(const int64_t* counts, const float* prob_sum, int E, int k,
+                               float alpha, float* loss, hipStream_t stream);
+hipError_t launch_route_bwd(const void* logits, bool bf16, int64_t T, int E, int k, bool sigmoid,
+                            bool renorm, float scale, const int32_t* topk_ids, const float* dgate,
+                            const int64_t* counts, float alpha, const float* dloss, void* dlogits,
+                            hipStream_t stream);
+
+// gradclip.hip
+size_t grad_workspace_bytes(int n);
+hipError_t launch_grad_sumsq(const void* const* grads, const int* dtypes, const int64_t* numels,
+                             int n, double* sumsq, void* workspace, hipStream_t stream);
+hipError_t launch_grad_clip(const void* const* grads, void* const* outs, const int* dtypes,
+                            const int64_t* numels, int n, const double* sumsq, float max_norm,
+                            float* norm, hipStream_t stream);
+
 // gemm_fwd.hip
 hipError_t launch_wgrad_nvfp4(const uint8_t* ac, const uint8_t* as, const float* ao,
                               const uint8_t* bc, const uint8_t* bs, const float* bo,
