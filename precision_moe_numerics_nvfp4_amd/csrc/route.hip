@@ -27,15 +27,36 @@ __device__ __forceinline__ float load1(const void* p, bool bf16, int64_t i) {
   return bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 
+// The value of the lane across in a group of 2, 4, 8, 16 (each step reaches the
+// half of its group that the earlier ones did not): DPP operands, no LDS.
+template <int STEP>
+__device__ __forceinline__ uint32_t across(uint32_t v) {
+  constexpr int ctrl = STEP == 0 ? 0xB1 /* quad_perm 1,0,3,2 */
+                       : STEP == 1 ? 0x4E /* quad_perm 2,3,0,1 */
+                       : STEP == 2 ? 0x141 /* row_half_mirror */ : 0x140 /* row_mirror */;
+  return __builtin_amdgcn_update_dpp(v, v, ctrl, 0xF, 0xF, true);
+}
+template <int STEP>
+__device__ __forceinline__ float across(float v) { return u2f(across<STEP>(f2u(v))); }
+
+// Sum and maximum over the wavefront, in every lane: four DPP steps make rows
+// of 16 uniform, the row swaps join them.
+template <class Op>
+__device__ __forceinline__ float wave_join(float v, Op op) {
+  v = op(v, across<0>(v));
+  v = op(v, across<1>(v));
+  v = op(v, across<2>(v));
+  v = op(v, across<3>(v));
+  const auto r16 = __builtin_amdgcn_permlane16_swap(f2u(v), f2u(v), false, false);
+  v = op(u2f(r16[0]), u2f(r16[1]));
+  const auto r32 = __builtin_amdgcn_permlane32_swap(f2u(v), f2u(v), false, false);
+  return op(u2f(r32[0]), u2f(r32[1]));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+  return wave_join(v, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
-  return v;
+  return wave_join(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // Orders the LDS accesses of one wavefront's lanes before and after it (the
@@ -99,6 +120,153 @@ __device__ __forceinline__ void select_rounds(Key (&key)[NV], int k, int lane, i
   }
 }
 
+// float32 -> uint32 of the same order (-0 below +0), and back.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = f2u(x);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return u2f(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+
+// A value that at least k of the wavefront's 64 values reach and few more do
+// (or the lowest one above -inf): the largest of each group of 64 / 2^n lanes
+// with 2^n >= k groups, of those the least; then a few bisections between it
+// and the maximum, each one comparison and a count of the ballot.
+__device__ __forceinline__ float k_reached(float v, int k) {
+  const uint32_t u = ordered(v + 0.0f);          // + 0: -0 is +0, as comparisons have it
+  const int level = k <= 8 ? 3 : k <= 16 ? 2 : k <= 32 ? 1 : 0;
+  uint32_t hi = u, lo = u;
+#define NVFP4MOE_STEP(S)                          \
+  do {                                            \
+    hi = max(hi, across<S>(hi));                  \
+    if (S < level) lo = hi;                       \
+    else lo = min(lo, across<S>(lo));             \
+  } while (0)
+  NVFP4MOE_STEP(0);
+  NVFP4MOE_STEP(1);
+  NVFP4MOE_STEP(2);
+  NVFP4MOE_STEP(3);
+#undef NVFP4MOE_STEP
+  const auto at = [](uint32_t x, int lane) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)x, lane);
+  };
+  uint32_t top = max(max(at(hi, 0), at(hi, 16)), max(at(hi, 32), at(hi, 48)));
+  uint32_t low = min(min(at(lo, 0), at(lo, 16)), min(at(lo, 32), at(lo, 48)));
+  low = max(low, ordered(kNegInf) + 1u);
+  for (int step = 0; step < 8; ++step) {
+    const uint32_t mid = low + ((top - low + 1u) >> 1);
+    if (mid <= low || top < low) break;
+    const int n = __popcll(__ballot(u >= mid));
+    if (n >= k) {
+      low = mid;
+      if (n == k) break;
+    } else {
+      top = mid - 1u;
+    }
+  }
+  return unordered(low);
+}
+
+struct Candidate {
+  float x;
+  int e;
+};
+
+// The k largest keys: lanes keep what reaches a value that at least k lanes
+// reach (a dozen candidates of 384 experts, compacted in expert order through
+// LDS, one per lane) and each candidate counts those ahead of it; its count is
+// its slot. Lane j ends with slot j's expert and logit. With a bias the first
+// cut is by float32 keys less a margin that covers their rounding, and the
+// order by 64-bit keys of the candidates alone. More than 64 candidates (rows
+// of equal logits, k near 64) go through select_rounds.
+template <bool BIAS, int NV>
+__device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g,
+                                       const float* bias, int k, int lane, Candidate* list,
+                                       int& id, float& sx) {
+  float key[NV], best = kNegInf;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    key[i] = x[i];
+    if constexpr (BIAS) {
+      float s, ds;
+      sigmoid(x[i], s, ds);
+      key[i] = x[i] > kNegInf ? s + bias[i] : kNegInf;
+    }
+    best = fmaxf(best, key[i]);
+  }
+  float cut = k_reached(best, k);
+  // |float32 key - key| <= 8 * 2^-24 + 2^-24 |key| (sigmoid and the sum): twice that is far inside
+  if constexpr (BIAS) cut -= 0x1p-19f + 0x1p-21f * fabsf(cut);
+  int n = 0;
+  uint64_t hit[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    hit[i] = __ballot(key[i] >= cut && key[i] > kNegInf);
+    n += __popcll(hit[i]);
+  }
+  id = -1;
+  sx = kNegInf;
+  if (n > 64) {
+    if constexpr (BIAS) {
+      double key64[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        key64[i] = x[i] > kNegInf ? biased_key(x[i], bias[i]) : (double)kNegInf;
+      select_rounds<NV>(key64, k, lane, id);
+    } else {
+      select_rounds<NV>(key, k, lane, id);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float v = __shfl(x[i], id & 63, 64);
+      if (id >= 0 && (id >> 6) == i) sx = v;
+    }
+    return;
+  }
+  int base = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int at = base + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(hit[i] >> 32),
+                                                         __builtin_amdgcn_mbcnt_lo((uint32_t)hit[i], 0));
+    if ((hit[i] >> lane) & 1) list[at] = Candidate{x[i], i * 64 + lane};
+    base += __popcll(hit[i]);
+  }
+  wave_lds_fence();
+  const Candidate c = lane < n ? list[lane] : Candidate{kNegInf, -1};
+  wave_lds_fence();
+  int rank = 0;
+  if constexpr (BIAS) {
+    const double mine = lane < n ? biased_key(c.x, bias_g[c.e]) : (double)kNegInf;
+    const uint64_t bits = __double_as_longlong(mine);
+    for (int j = 0; j < n; ++j) {
+      const uint64_t o = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(bits >> 32), j) << 32) |
+                         (uint32_t)__builtin_amdgcn_readlane((int)bits, j);
+      const double other = __longlong_as_double(o);
+      rank += other > mine || (other == mine && j < lane);
+    }
+  } else {
+    for (int j = 0; j < n; ++j) {
+      const float other = u2f((uint32_t)__builtin_amdgcn_readlane((int)f2u(c.x), j));
+      rank += other > c.x || (other == c.x && j < lane);
+    }
+  }
+  if (lane < n && rank < k) list[rank] = c;
+  wave_lds_fence();
+  if (lane < k && lane < n) {
+    const Candidate mine = list[lane];
+    id = mine.e;
+    sx = mine.x;
+  }
+  wave_lds_fence();
+}
+
+// One workgroup's share of an expert's statistics.
+struct alignas(8) RoutePart {
+  float prob;
+  int32_t count;
+};
+
 struct RouteArgs {
   const void* logits;
   int64_t T;
@@ -108,14 +276,14 @@ struct RouteArgs {
   float scale;
   int32_t* topk_ids;
   float* gate;
-  float* part_prob;      // [grid, E] probability sums of each workgroup's rows
-  int32_t* part_count;   // [grid, E + 1]
+  RoutePart* parts;      // [grid, E + 1], the last one's count the tokens
 };
 
 template <bool BF, bool SIG, bool RENORM, bool BIAS, bool STATS, int NV>
 __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
   __shared__ float sh_prob[STATS ? kWaves * NV * 64 : 1];
   __shared__ int32_t sh_count[STATS ? NV * 64 + 1 : 1];
+  __shared__ Candidate list[kWaves][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int E = a.E, k = a.k;
   float bias[BIAS ? NV : 1];
@@ -139,18 +307,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
       x[i] = on && e < E ? load1(a.logits, BF, t * E + e) : kNegInf;
     }
     int id;
-    if constexpr (BIAS) {
-      double key[NV];
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        key[i] = x[i] > kNegInf ? biased_key(x[i], bias[i]) : (double)kNegInf;
-      select_rounds<NV>(key, k, lane, id);
-    } else {
-      float key[NV];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) key[i] = x[i];
-      select_rounds<NV>(key, k, lane, id);
-    }
+    float sx;
+    select<BIAS, NV>(x, a.bias, bias, k, lane, list[w], id, sx);
     const bool live = __builtin_amdgcn_readfirstlane(id) >= 0;
     // scores; the row's probabilities where they are needed
     float top = kNegInf, total = 0.0f, p[NV];
@@ -184,7 +342,6 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
       if (lane == 0 && live) atomicAdd(&sh_count[E], 1);
     }
     // gates of the selected, one per lane
-    const float sx = id >= 0 ? load1(a.logits, BF, t * E + id) : kNegInf;
     float g = 0.0f;
     if (live) {
       if constexpr (SIG) {
@@ -209,44 +366,56 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) sh_prob[w * NV * 64 + i * 64 + lane] = psum[i];
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += 64 * kWaves) {
+    for (int e = threadIdx.x; e <= E; e += 64 * kWaves) {
       float s = 0.0f;
+      if (e < E) {
 #pragma unroll
-      for (int v = 0; v < kWaves; ++v) s += sh_prob[v * NV * 64 + e];
-      a.part_prob[(int64_t)blockIdx.x * E + e] = s;
+        for (int v = 0; v < kWaves; ++v) s += sh_prob[v * NV * 64 + e];
+      }
+      a.parts[(int64_t)blockIdx.x * (E + 1) + e] = RoutePart{s, sh_count[e]};
     }
-    for (int e = threadIdx.x; e <= E; e += 64 * kWaves)
-      a.part_count[(int64_t)blockIdx.x * (E + 1) + e] = sh_count[e];
   }
 }
 
 // Column sums of the workgroups' partials, in a fixed order: 16 columns per
-// workgroup, 16 threads down each.
-__global__ __launch_bounds__(256) void k_route_stats(const float* __restrict__ part_prob,
-                                                     const int32_t* __restrict__ part_count,
-                                                     int parts, int E,
-                                                     int64_t* __restrict__ counts,
-                                                     float* __restrict__ prob_sum) {
-  __shared__ double sp[256];
-  __shared__ int64_t sc[256];
+// workgroup, 64 threads down each, eight loads of a thread in flight.
+__global__ __launch_bounds__(1024) void k_route_stats(const RoutePart* __restrict__ parts, int n,
+                                                      int E, int64_t* __restrict__ counts,
+                                                      float* __restrict__ prob_sum) {
+  __shared__ double sp[1024];
+  __shared__ int64_t sc[1024];
   const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
   const int e = blockIdx.x * 16 + col;
+  const int at = e <= E ? e : E;
   double p = 0.0;
   int64_t c = 0;
-  for (int g = row; g < parts; g += 16) {
-    if (e < E) p += (double)part_prob[(int64_t)g * E + e];
-    if (e <= E) c += part_count[(int64_t)g * (E + 1) + e];
+  for (int g0 = row; g0 < n; g0 += 64 * 8) {
+    RoutePart v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {            // past the end: the last row again, not added
+      const int g = g0 + 64 * j < n ? g0 + 64 * j : n - 1;
+      v[j] = parts[(int64_t)g * (E + 1) + at];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (g0 + 64 * j < n) {
+        p += (double)v[j].prob;
+        c += v[j].count;
+      }
   }
   sp[threadIdx.x] = p;
   sc[threadIdx.x] = c;
   __syncthreads();
-  if (row == 0 && e <= E) {
-    for (int r = 1; r < 16; ++r) {
-      p += sp[16 * r + col];
-      c += sc[16 * r + col];
+  for (int d = 32; d >= 1; d >>= 1) {
+    if (row < d) {
+      sp[threadIdx.x] += sp[threadIdx.x + 16 * d];
+      sc[threadIdx.x] += sc[threadIdx.x + 16 * d];
     }
-    if (e < E) prob_sum[e] = (float)p;
-    counts[e] = c;
+    __syncthreads();
+  }
+  if (row == 0 && e <= E) {
+    if (e < E) prob_sum[e] = (float)sp[col];
+    counts[e] = sc[col];
   }
 }
 
@@ -448,7 +617,7 @@ void bwd_nv(const RouteBwdArgs& a, unsigned grid, hipStream_t s) {
 size_t route_workspace_bytes(int64_t T, int E) {
   const int64_t need = (T + kWaves - 1) / kWaves;
   const int64_t parts = need < kMaxRouteParts ? need : kMaxRouteParts;
-  return (size_t)(parts * (2 * (int64_t)E + 1) * 4);
+  return (size_t)(parts * ((int64_t)E + 1) * sizeof(RoutePart));
 }
 
 hipError_t launch_route(const void* logits, bool bf16, int64_t T, int E, int k, bool sigmoid,
@@ -458,11 +627,8 @@ hipError_t launch_route(const void* logits, bool bf16, int64_t T, int E, int k, 
   const bool stats = counts != nullptr;
   int64_t grid = route_grid(T, stats ? kStatsPerCu : 8);
   if (stats && grid > kMaxRouteParts) grid = kMaxRouteParts;
-  RouteArgs a{logits, T, E, k, bias, token_mask, scale, topk_ids, gate, nullptr, nullptr};
-  if (stats) {
-    a.part_prob = static_cast<float*>(workspace);
-    a.part_count = reinterpret_cast<int32_t*>(a.part_prob + grid * E);
-  }
+  RouteArgs a{logits, T, E, k, bias, token_mask, scale, topk_ids, gate,
+              static_cast<RoutePart*>(workspace)};
   if (grid > 0) {
     const unsigned g = (unsigned)grid;
     if (bf16) {
@@ -486,8 +652,8 @@ hipError_t launch_route(const void* logits, bool bf16, int64_t T, int E, int k, 
     if (e != hipSuccess) return e;
   }
   if (stats)
-    k_route_stats<<<(unsigned)(E / 16 + 1), 256, 0, stream>>>(a.part_prob, a.part_count, (int)grid,
-                                                              E, counts, prob_sum);
+    k_route_stats<<<(unsigned)(E / 16 + 1), 1024, 0, stream>>>(a.parts, (int)grid, E, counts,
+                                                               prob_sum);
   return hipGetLastError();
 }
 
