@@ -4,11 +4,11 @@
 //           overflow or lost small terms whatever the gradients' scale);
 //   out   = g * min(1, max_norm / (sqrt(sumsq) + 1e-6)).
 //
-// Both passes stream: the tensors are cut into chunks of 16384 elements, each
-// workgroup takes a contiguous run of chunks of the whole list, so a list of
-// many small tensors and one of a few large ones both fill the device. The
-// list travels in the kernel arguments (no copy to the device, nothing to keep
-// alive), up to kTable tensors a launch.
+// Both passes stream: the tensors are cut into chunks, each workgroup takes a
+// contiguous run of chunks of the whole list, so a list of many small tensors
+// and one of a few large ones both fill the device. The list travels in the
+// kernel arguments (no copy to the device, nothing to keep alive): up to 280
+// tensors a launch for the sum, 180 for the scaling, within 4 KiB.
 #include "codecs.hpp"
 #include "internal.hpp"
 
@@ -16,21 +16,52 @@ namespace nvfp4moe {
 
 namespace {
 
-constexpr int kTable = 96;              // tensors per launch: 2.9 KB of arguments
-constexpr int kChunkElems = 16384;
+constexpr int kSumTable = 280, kClipTable = 180;    // tensors per launch
 constexpr int kThreads = 256;
-constexpr int kMaxParts = 2048;         // workgroups, so partial sums, per launch
+constexpr int kMaxParts = 2048;                     // workgroups, so partial sums, per launch
+// Chunk sizes, 2^shift elements: the largest one streams with the least
+// overhead, smaller ones spread a short list over the compute units.
+constexpr int kMinShift = 11, kMaxShift = 14;
 
+template <int N, bool OUT>
 struct GradTable {
-  const void* in[kTable];
-  void* out[kTable];
-  int64_t numel[kTable];
-  uint32_t first[kTable + 1];           // the tensor's first chunk; [n]: all chunks
-  uint8_t bf16[kTable];
-  int n;
+  const void* in[N];
+  void* out[OUT ? N : 1];
+  uint32_t first[N + 1];                // the tensor's first chunk; [n]: all chunks
+  uint16_t last[N];                     // elements of its last chunk less one; bit 15: bfloat16
+  int n, shift;
 };
 
-// Sum over the 256 threads of the workgroup, in a fixed order (thread 0 has it).
+// A run of one tensor's elements.
+struct Chunk {
+  int j;
+  int64_t at;
+  int len;
+  bool bf16;
+};
+
+// Chunk c of the list; j: a tensor at or before it.
+template <class Table>
+__device__ __forceinline__ Chunk chunk(const Table& t, uint32_t c, int j) {
+  while (t.first[j + 1] <= c) ++j;
+  const int size = 1 << t.shift;
+  const uint32_t last = t.last[j];
+  return Chunk{j, (int64_t)(c - t.first[j]) << t.shift,
+               c + 1 == t.first[j + 1] ? (int)(last & 0x7FFFu) + 1 : size, (last & 0x8000u) != 0};
+}
+
+// The tensor that chunk c lies in: the last one whose first chunk is not past c.
+template <class Table>
+__device__ __forceinline__ int table_find(const Table& t, uint32_t c) {
+  int lo = 0, hi = t.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.first[mid] <= c) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Sum over the 256 threads of the workgroup, in a fixed order (every thread has it).
 __device__ __forceinline__ double block_sum(double v) {
   __shared__ double sh[kThreads / 64];
 #pragma unroll
@@ -43,70 +74,123 @@ __device__ __forceinline__ double block_sum(double v) {
   return s;
 }
 
-// The tensor that chunk c lies in: the last one whose first chunk is not past c.
-__device__ __forceinline__ int table_find(const GradTable& t, uint32_t c) {
-  int lo = 0, hi = t.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.first[mid] <= c) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-
 __device__ __forceinline__ double sq(float v, double acc) {
   const double d = (double)v;
   return __fma_rn(d, d, acc);
 }
 
-__global__ __launch_bounds__(kThreads) void k_grad_sumsq(GradTable t, uint32_t per,
+template <bool BF>
+__device__ __forceinline__ float element(const void* p, int i) {
+  if constexpr (BF) return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
+  else return static_cast<const float*>(p)[i];
+}
+
+template <bool BF>
+__device__ __forceinline__ void sq16(const uint4& v, double (&acc)[4]) {
+  if constexpr (BF) {
+    acc[0] = sq(u2f(v.x << 16), acc[0]);
+    acc[1] = sq(u2f(v.x & 0xFFFF0000u), acc[1]);
+    acc[2] = sq(u2f(v.y << 16), acc[2]);
+    acc[3] = sq(u2f(v.y & 0xFFFF0000u), acc[3]);
+    acc[0] = sq(u2f(v.z << 16), acc[0]);
+    acc[1] = sq(u2f(v.z & 0xFFFF0000u), acc[1]);
+    acc[2] = sq(u2f(v.w << 16), acc[2]);
+    acc[3] = sq(u2f(v.w & 0xFFFF0000u), acc[3]);
+  } else {
+    acc[0] = sq(u2f(v.x), acc[0]);
+    acc[1] = sq(u2f(v.y), acc[1]);
+    acc[2] = sq(u2f(v.z), acc[2]);
+    acc[3] = sq(u2f(v.w), acc[3]);
+  }
+}
+
+template <bool BF>
+__device__ __forceinline__ uint4 scale16(const uint4& v, float c) {
+  if constexpr (BF)
+    return make_uint4(pk_bf16(u2f(v.x << 16) * c, u2f(v.x & 0xFFFF0000u) * c),
+                      pk_bf16(u2f(v.y << 16) * c, u2f(v.y & 0xFFFF0000u) * c),
+                      pk_bf16(u2f(v.z << 16) * c, u2f(v.z & 0xFFFF0000u) * c),
+                      pk_bf16(u2f(v.w << 16) * c, u2f(v.w & 0xFFFF0000u) * c));
+  else
+    return make_uint4(f2u(u2f(v.x) * c), f2u(u2f(v.y) * c), f2u(u2f(v.z) * c), f2u(u2f(v.w) * c));
+}
+
+// Elements before the first 16-byte boundary, at most len.
+template <bool BF>
+__device__ __forceinline__ int head_of(const void* p, int len) {
+  const int h = (int)((16u - ((uint32_t)reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / (BF ? 2 : 4);
+  return h < len ? h : len;
+}
+
+constexpr int kFlight = 4;              // 16-byte loads of a thread in flight
+
+template <bool BF>
+__device__ __forceinline__ void sum_run(const void* base, int len, double (&acc)[4]) {
+  constexpr int per = BF ? 8 : 4;       // elements of 16 bytes
+  const int tid = threadIdx.x, head = head_of<BF>(base, len);
+  const int nq = (len - head) / per, tail = head + nq * per;
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + head * (BF ? 2 : 4));
+  int i = tid;
+  for (; i + (kFlight - 1) * kThreads < nq; i += kFlight * kThreads) {
+    uint4 v[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) v[u] = q[i + u * kThreads];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) sq16<BF>(v[u], acc);
+  }
+  for (; i < nq; i += kThreads) sq16<BF>(q[i], acc);
+  if (tid < head) acc[0] = sq(element<BF>(base, tid), acc[0]);
+  if (tid < len - tail) acc[1] = sq(element<BF>(base, tail + tid), acc[1]);
+}
+
+template <bool BF>
+__device__ __forceinline__ void scale_run(const void* base, void* out, int len, float c) {
+  constexpr int per = BF ? 8 : 4;
+  const int tid = threadIdx.x;
+  const auto put = [&](int i) {
+    const float y = element<BF>(base, i) * c;
+    if constexpr (BF) static_cast<uint16_t*>(out)[i] = (uint16_t)pk_bf16(y, 0.0f);
+    else static_cast<float*>(out)[i] = y;
+  };
+  if (((reinterpret_cast<uintptr_t>(base) ^ reinterpret_cast<uintptr_t>(out)) & 15u) != 0) {
+    for (int i = tid; i < len; i += kThreads) put(i);      // no common 16-byte grid
+    return;
+  }
+  const int head = head_of<BF>(base, len);
+  const int nq = (len - head) / per, tail = head + nq * per;
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + head * (BF ? 2 : 4));
+  uint4* r = reinterpret_cast<uint4*>(static_cast<char*>(out) + head * (BF ? 2 : 4));
+  int i = tid;
+  for (; i + (kFlight - 1) * kThreads < nq; i += kFlight * kThreads) {
+    uint4 v[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) v[u] = ld_stream16(q + i + u * kThreads);
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const uint4 y = scale16<BF>(v[u], c);
+      __builtin_nontemporal_store(u32x4_t{y.x, y.y, y.z, y.w},
+                                  reinterpret_cast<u32x4_t*>(r + i + u * kThreads));
+    }
+  }
+  for (; i < nq; i += kThreads) r[i] = scale16<BF>(q[i], c);
+  if (tid < head) put(tid);
+  if (tid < len - tail) put(tail + tid);
+}
+
+using SumTable = GradTable<kSumTable, false>;
+using ClipTable = GradTable<kClipTable, true>;
+
+__global__ __launch_bounds__(kThreads) void k_grad_sumsq(SumTable t, uint32_t per,
                                                          double* __restrict__ parts) {
   const uint32_t all = t.first[t.n];
   const uint32_t c0 = blockIdx.x * per, c1 = c0 + per < all ? c0 + per : all;
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
   int j = table_find(t, c0);
   for (uint32_t c = c0; c < c1; ++c) {
-    while (t.first[j + 1] <= c) ++j;
-    const int64_t at = (int64_t)(c - t.first[j]) * kChunkElems;
-    const int64_t left = t.numel[j] - at;
-    const int len = left < kChunkElems ? (int)left : kChunkElems;
-    const bool wide = (reinterpret_cast<uintptr_t>(t.in[j]) & 15u) == 0;
-    if (t.bf16[j]) {
-      const uint16_t* p = static_cast<const uint16_t*>(t.in[j]) + at;
-      int done = 0;
-      if (wide) {
-        const uint4* q = reinterpret_cast<const uint4*>(p);
-        const int nq = len / 8;
-        for (int i = threadIdx.x; i < nq; i += kThreads) {
-          const uint4 v = q[i];
-          acc[0] = sq(u2f(v.x << 16), acc[0]);
-          acc[1] = sq(u2f(v.x & 0xFFFF0000u), acc[1]);
-          acc[2] = sq(u2f(v.y << 16), acc[2]);
-          acc[3] = sq(u2f(v.y & 0xFFFF0000u), acc[3]);
-          acc[0] = sq(u2f(v.z << 16), acc[0]);
-          acc[1] = sq(u2f(v.z & 0xFFFF0000u), acc[1]);
-          acc[2] = sq(u2f(v.w << 16), acc[2]);
-          acc[3] = sq(u2f(v.w & 0xFFFF0000u), acc[3]);
-        }
-        done = nq * 8;
-      }
-      for (int i = done + threadIdx.x; i < len; i += kThreads) acc[0] = sq(bf16_to_f32(p[i]), acc[0]);
-    } else {
-      const float* p = static_cast<const float*>(t.in[j]) + at;
-      int done = 0;
-      if (wide) {
-        const float4* q = reinterpret_cast<const float4*>(p);
-        const int nq = len / 4;
-        for (int i = threadIdx.x; i < nq; i += kThreads) {
-          const float4 v = q[i];
-          acc[0] = sq(v.x, acc[0]);
-          acc[1] = sq(v.y, acc[1]);
-          acc[2] = sq(v.z, acc[2]);
-          acc[3] = sq(v.w, acc[3]);
-        }
-        done = nq * 4;
-      }
-      for (int i = done + threadIdx.x; i < len; i += kThreads) acc[0] = sq(p[i], acc[0]);
-    }
+    const Chunk k = chunk(t, c, j);
+    j = k.j;
+    if (k.bf16) sum_run<true>(static_cast<const uint16_t*>(t.in[j]) + k.at, k.len, acc);
+    else sum_run<false>(static_cast<const float*>(t.in[j]) + k.at, k.len, acc);
   }
   const double s = block_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
   if (threadIdx.x == 0) parts[blockIdx.x] = s;
@@ -120,7 +204,7 @@ __global__ __launch_bounds__(kThreads) void k_grad_join(const double* __restrict
   if (threadIdx.x == 0) *sumsq = s;
 }
 
-__global__ __launch_bounds__(kThreads) void k_grad_clip(GradTable t, uint32_t per,
+__global__ __launch_bounds__(kThreads) void k_grad_clip(ClipTable t, uint32_t per,
                                                         const double* __restrict__ sumsq,
                                                         float max_norm, float* __restrict__ norm) {
   const double root = sqrt(*sumsq);
@@ -132,94 +216,70 @@ __global__ __launch_bounds__(kThreads) void k_grad_clip(GradTable t, uint32_t pe
   const uint32_t c0 = blockIdx.x * per, c1 = c0 + per < all ? c0 + per : all;
   int j = table_find(t, c0);
   for (uint32_t c = c0; c < c1; ++c) {
-    while (t.first[j + 1] <= c) ++j;
+    const Chunk k = chunk(t, c, j);
+    j = k.j;
     if (coef == 1.0f && t.out[j] == t.in[j]) continue;        // in place and within the bound
-    const int64_t at = (int64_t)(c - t.first[j]) * kChunkElems;
-    const int64_t left = t.numel[j] - at;
-    const int len = left < kChunkElems ? (int)left : kChunkElems;
-    const bool wide = ((reinterpret_cast<uintptr_t>(t.in[j]) |
-                        reinterpret_cast<uintptr_t>(t.out[j])) & 15u) == 0;
-    if (t.bf16[j]) {
-      const uint16_t* p = static_cast<const uint16_t*>(t.in[j]) + at;
-      uint16_t* o = static_cast<uint16_t*>(t.out[j]) + at;
-      int done = 0;
-      if (wide) {
-        const uint4* q = reinterpret_cast<const uint4*>(p);
-        uint4* r = reinterpret_cast<uint4*>(o);
-        const int nq = len / 8;
-        for (int i = threadIdx.x; i < nq; i += kThreads) {
-          const uint4 v = q[i];
-          uint4 y;
-          y.x = pk_bf16(u2f(v.x << 16) * coef, u2f(v.x & 0xFFFF0000u) * coef);
-          y.y = pk_bf16(u2f(v.y << 16) * coef, u2f(v.y & 0xFFFF0000u) * coef);
-          y.z = pk_bf16(u2f(v.z << 16) * coef, u2f(v.z & 0xFFFF0000u) * coef);
-          y.w = pk_bf16(u2f(v.w << 16) * coef, u2f(v.w & 0xFFFF0000u) * coef);
-          r[i] = y;
-        }
-        done = nq * 8;
-      }
-      for (int i = done + threadIdx.x; i < len; i += kThreads)
-        o[i] = (uint16_t)pk_bf16(bf16_to_f32(p[i]) * coef, 0.0f);
-    } else {
-      const float* p = static_cast<const float*>(t.in[j]) + at;
-      float* o = static_cast<float*>(t.out[j]) + at;
-      int done = 0;
-      if (wide) {
-        const float4* q = reinterpret_cast<const float4*>(p);
-        float4* r = reinterpret_cast<float4*>(o);
-        const int nq = len / 4;
-        for (int i = threadIdx.x; i < nq; i += kThreads) {
-          float4 v = q[i];
-          v.x *= coef; v.y *= coef; v.z *= coef; v.w *= coef;
-          r[i] = v;
-        }
-        done = nq * 4;
-      }
-      for (int i = done + threadIdx.x; i < len; i += kThreads) o[i] = p[i] * coef;
-    }
+    if (k.bf16)
+      scale_run<true>(static_cast<const uint16_t*>(t.in[j]) + k.at,
+                      static_cast<uint16_t*>(t.out[j]) + k.at, k.len, coef);
+    else
+      scale_run<false>(static_cast<const float*>(t.in[j]) + k.at,
+                       static_cast<float*>(t.out[j]) + k.at, k.len, coef);
   }
 }
 
-// Tensors [at, at + ...) of the list, empty ones left out; returns the first
-// one that the next launch takes.
-int fill_table(GradTable& t, int at, const void* const* grads, void* const* outs,
-               const int* dtypes, const int64_t* numels, int n) {
-  uint32_t chunks = 0;                  // below 2^31: the C ABI bounds the elements and tensors
+// The chunk size for a list: the smallest whose chunks, two per workgroup,
+// still fill kMaxParts workgroups.
+int chunk_shift(const int64_t* numels, int n) {
+  int64_t total = 0;
+  for (int i = 0; i < n; ++i) total += numels[i];
+  int shift = kMinShift;
+  while (shift < kMaxShift && (total >> shift) > 2 * kMaxParts) ++shift;
+  return shift;
+}
+
+// Tensors [at, ...) of the list, empty ones left out, into one launch's table;
+// returns the first one that the next launch takes. Chunks stay below 2^32:
+// the C ABI bounds elements and tensors.
+template <int N, bool OUT>
+int fill_table(GradTable<N, OUT>& t, int shift, int at, const void* const* grads,
+               void* const* outs, const int* dtypes, const int64_t* numels, int n) {
+  uint32_t chunks = 0;
   t.n = 0;
-  for (; at < n && t.n < kTable; ++at) {
+  t.shift = shift;
+  for (; at < n && t.n < N; ++at) {
     if (numels[at] == 0) continue;
+    const int64_t whole = (numels[at] - 1) >> shift;           // chunks before the last
     t.in[t.n] = grads[at];
-    t.out[t.n] = outs ? outs[at] : nullptr;
-    t.numel[t.n] = numels[at];
-    t.bf16[t.n] = dtypes[at] == 1;
+    if constexpr (OUT) t.out[t.n] = outs[at];
     t.first[t.n] = chunks;
-    chunks += (uint32_t)((numels[at] + kChunkElems - 1) / kChunkElems);
+    t.last[t.n] = (uint16_t)((numels[at] - 1 - (whole << shift)) | (dtypes[at] == 1 ? 0x8000 : 0));
+    chunks += (uint32_t)whole + 1;
     ++t.n;
   }
   t.first[t.n] = chunks;
   return at;
 }
 
-uint32_t per_workgroup(uint32_t chunks, int64_t most) {
-  return (uint32_t)((chunks + most - 1) / most);
-}
+uint32_t per_workgroup(uint32_t chunks) { return (chunks + kMaxParts - 1) / kMaxParts; }
 
 }  // namespace
 
 size_t grad_workspace_bytes(int n) {
-  return (size_t)(n / kTable + 2) * kMaxParts * sizeof(double);
+  return (size_t)(n / kSumTable + 1) * kMaxParts * sizeof(double);
 }
 
 hipError_t launch_grad_sumsq(const void* const* grads, const int* dtypes, const int64_t* numels,
                              int n, double* sumsq, void* workspace, hipStream_t stream) {
   double* parts = static_cast<double*>(workspace);
+  const int shift = chunk_shift(numels, n);
   int used = 0;
   for (int at = 0; at < n;) {
-    GradTable t;
-    at = fill_table(t, at, grads, nullptr, dtypes, numels, n);
+    SumTable t;
+    at = fill_table(t, shift, at, grads, nullptr, dtypes, numels, n);
     if (t.n == 0) break;
     const uint32_t chunks = t.first[t.n];
-    const uint32_t per = per_workgroup(chunks, kMaxParts);
+    const uint32_t per = per_workgroup(chunks);
     const unsigned grid = (chunks + per - 1) / per;
     k_grad_sumsq<<<grid, kThreads, 0, stream>>>(t, per, parts + used);
     const hipError_t e = hipGetLastError();
@@ -233,13 +293,14 @@ hipError_t launch_grad_sumsq(const void* const* grads, const int* dtypes, const 
 hipError_t launch_grad_clip(const void* const* grads, void* const* outs, const int* dtypes,
                             const int64_t* numels, int n, const double* sumsq, float max_norm,
                             float* norm, hipStream_t stream) {
+  const int shift = chunk_shift(numels, n);
   int at = 0;
   do {
-    GradTable t;
-    at = fill_table(t, at, grads, outs, dtypes, numels, n);
+    ClipTable t;
+    at = fill_table(t, shift, at, grads, outs, dtypes, numels, n);
     if (t.n == 0 && norm == nullptr) break;
-    const uint32_t chunks = t.n ? t.first[t.n] : 0;
-    const uint32_t per = chunks ? per_workgroup(chunks, kMaxParts) : 1;
+    const uint32_t chunks = t.first[t.n];
+    const uint32_t per = chunks ? per_workgroup(chunks) : 1;
     const unsigned grid = chunks ? (chunks + per - 1) / per : 1;
     k_grad_clip<<<grid, kThreads, 0, stream>>>(t, per, sumsq, max_norm, norm);
     const hipError_t e = hipGetLastError();
