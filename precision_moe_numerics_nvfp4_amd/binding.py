@@ -657,37 +657,51 @@ def moe_bwd_wgrad_nvfp4(dyT, xT, padded_offsets, N, K, dw=None):
 # ------------------------------------------ routing and gradient clipping
 
 def _launch(dev, name, *args):
-    """Call the library with ``dev`` as the current device (the stream that
-    ends the arguments is one of it) and check the status."""
+    """Call the library with ``dev`` as the current device, on its current
+    stream (the last argument of every call), and check the status."""
     torch = _torch()
-    f = getattr(lib(), name)
-    args = args + (torch.cuda.current_stream(dev).cuda_stream,)
-    if torch.cuda.current_device() == dev.index:
-        st = f(*args)
+    f = getattr(_LIB or lib(), name)
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    if torch._C._cuda_getDevice() == dev.index:
+        st = f(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = f(*args)
-    _check(name, st)
-
-
-def _buf(t, name, dtype, shape, dev):
-    """An output buffer: the caller's, checked, or a new one."""
-    if t is None:
-        return _torch().empty(shape, dtype=dtype, device=dev)
-    _dev(t, name, dtype)
-    if tuple(t.shape) != tuple(shape) or t.device != dev:
-        raise ValueError(f"{name} must have shape {tuple(shape)} on {dev} "
-                         f"(got {tuple(t.shape)} on {t.device})")
-    return t
+            st = f(*args, stream)
+    if st:
+        _check(name, st)
 
 
 def _on(t, name, dtype, shape, dev):
-    """An input that goes with another one: its type, shape and device."""
-    _dev(t, name, dtype)
-    if tuple(t.shape) != tuple(shape) or t.device != dev:
+    """The address of a tensor that goes with another one: its type, shape
+    and device."""
+    if t.__class__ is not _torch().Tensor or t.dtype != dtype or not t.is_contiguous():
+        _dev(t, name, dtype)
+    if t.shape != shape or t.device != dev:
         raise ValueError(f"{name} must have shape {tuple(shape)} on {dev} "
                          f"(got {tuple(t.shape)} on {t.device})")
     return t.data_ptr()
+
+
+def _buf(out, name, dtype, shape, dev):
+    """The address of an output buffer: the caller's in the dict ``out``,
+    checked, or a new one put there."""
+    t = out.get(name)
+    if t is None:
+        t = out[name] = _torch().empty(shape, dtype=dtype, device=dev)
+        return t.data_ptr()
+    return _on(t, name, dtype, shape, dev)
+
+
+def _workspace(t, need, dev):
+    """(workspace, bytes): the caller's, or a new one (live until the call returns:
+    torch hands its memory to later work of the same stream only)."""
+    torch = _torch()
+    if t is None:
+        return torch.empty((need,), dtype=torch.uint8, device=dev), need
+    _dev(t, "workspace", torch.uint8)
+    if t.device != dev:
+        raise ValueError(f"workspace must be on {dev} (got {t.device})")
+    return t, t.numel()
 
 
 def _score(score):
@@ -716,29 +730,23 @@ def moe_route(logits, k, score="softmax", renorm=True, scale=1.0, bias=None, tok
     k = int(k)
     dev = logits.device
     o = {} if out is None else dict(out)
-    ids = o["topk_ids"] = _buf(o.get("topk_ids"), "topk_ids", torch.int32, (T, k), dev)
-    gate = o["gate"] = _buf(o.get("gate"), "gate", torch.float32, (T, k), dev)
+    ids = _buf(o, "topk_ids", torch.int32, (T, k), dev)
+    gate = _buf(o, "gate", torch.float32, (T, k), dev)
     counts = prob_sum = ws = None
     ws_bytes = 0
     if stats:
-        counts = o["counts"] = _buf(o.get("counts"), "counts", torch.int64, (E + 1,), dev)
-        prob_sum = o["prob_sum"] = _buf(o.get("prob_sum"), "prob_sum", torch.float32, (E,), dev)
-        ws_bytes = route_workspace_size(T, E)
-        if workspace is None:
-            workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=dev)
-        else:
-            _dev(workspace, "workspace", torch.uint8)
-            if workspace.device != dev:
-                raise ValueError(f"workspace must be on {dev}")
-            ws_bytes = workspace.numel()
-        counts, prob_sum, ws = counts.data_ptr(), prob_sum.data_ptr(), workspace.data_ptr()
-    if token_mask is not None and token_mask.dtype == torch.bool:
-        token_mask = token_mask.view(torch.uint8)
+        counts = _buf(o, "counts", torch.int64, (E + 1,), dev)
+        prob_sum = _buf(o, "prob_sum", torch.float32, (E,), dev)
+        ws, ws_bytes = _workspace(workspace, route_workspace_size(T, E), dev)
+    if bias is not None:
+        bias = _on(bias, "bias", torch.float32, (E,), dev)
+    if token_mask is not None:
+        if token_mask.dtype == torch.bool:
+            token_mask = token_mask.view(torch.uint8)
+        token_mask = _on(token_mask, "token_mask", torch.uint8, (T,), dev)
     _launch(dev, "moe_route", logits.data_ptr(), _in_dtype(logits), T, E, k, _score(score),
-            int(bool(renorm)), float(scale),
-            None if bias is None else _on(bias, "bias", torch.float32, (E,), dev),
-            None if token_mask is None else _on(token_mask, "token_mask", torch.uint8, (T,), dev),
-            ids.data_ptr(), gate.data_ptr(), counts, prob_sum, ws, ws_bytes)
+            1 if renorm else 0, scale, bias, token_mask, ids, gate, counts, prob_sum,
+            None if ws is None else ws.data_ptr(), ws_bytes)
     return o
 
 
@@ -748,10 +756,10 @@ def moe_balance_loss(counts, prob_sum, k, alpha, loss=None):
     torch = _torch()
     _dev(prob_sum, "prob_sum", torch.float32, 1)
     dev, E = prob_sum.device, prob_sum.shape[0]
-    loss = _buf(loss, "loss", torch.float32, (1,), dev)
+    o = {"loss": loss}
     _launch(dev, "moe_balance_loss", _on(counts, "counts", torch.int64, (E + 1,), dev),
-            prob_sum.data_ptr(), E, int(k), float(alpha), loss.data_ptr())
-    return loss
+            prob_sum.data_ptr(), E, int(k), alpha, _buf(o, "loss", torch.float32, (1,), dev))
+    return o["loss"]
 
 
 def moe_route_bwd(logits, topk_ids, dgate=None, score="softmax", renorm=True, scale=1.0,
@@ -765,22 +773,25 @@ def moe_route_bwd(logits, topk_ids, dgate=None, score="softmax", renorm=True, sc
     T, E = logits.shape
     k = topk_ids.shape[1]
     dev = logits.device
-    dlogits = _buf(dlogits, "dlogits", logits.dtype, (T, E), dev)
+    o = {"dlogits": dlogits}
+    if dgate is not None:
+        dgate = _on(dgate, "dgate", torch.float32, (T, k), dev)
+    if counts is not None:
+        counts = _on(counts, "counts", torch.int64, (E + 1,), dev)
+    if dloss is not None:
+        dloss = _on(dloss, "dloss", torch.float32, (1,), dev)
     _launch(dev, "moe_route_bwd", logits.data_ptr(), _in_dtype(logits), T, E, k, _score(score),
-            int(bool(renorm)), float(scale), _on(topk_ids, "topk_ids", torch.int32, (T, k), dev),
-            None if dgate is None else _on(dgate, "dgate", torch.float32, (T, k), dev),
-            None if counts is None else _on(counts, "counts", torch.int64, (E + 1,), dev),
-            float(alpha),
-            None if dloss is None else _on(dloss, "dloss", torch.float32, (1,), dev),
-            dlogits.data_ptr())
-    return dlogits
+            1 if renorm else 0, scale, _on(topk_ids, "topk_ids", torch.int32, (T, k), dev), dgate,
+            counts, alpha, dloss, _buf(o, "dlogits", logits.dtype, (T, E), dev))
+    return o["dlogits"]
 
 
 class GradList:
     """The gradients (or their clipped copies) of one device as the calls
     below take them: contiguous bf16|f32 tensors of any alignment that do not
-    overlap. Made once of buffers that live on; it keeps the tensors, and a
-    tensor whose memory or size has changed since is looked at again."""
+    overlap. Made once of buffers that live on, it keeps the tensors and their
+    memory; a tensor given other memory since (``t.data = ...``) is looked at
+    again in the next call, but sizes must not be changed in place."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
@@ -789,31 +800,33 @@ class GradList:
     def _look(self):
         torch = _torch()
         ts = self.tensors
-        self.device = None
+        dev = None
         for i, t in enumerate(ts):
-            _dev(t, f"tensor {i}")
-            if self.device is None:
-                self.device = t.device
-            elif t.device != self.device:
-                raise ValueError(f"tensor {i} is on {t.device}, the first on {self.device}")
-        n = len(ts)
-        self.key = [(t.data_ptr(), t.numel()) for t in ts]
-        spans = sorted((p, p + t.numel() * t.element_size())
-                       for t, (p, m) in zip(ts, self.key) if m)
+            if not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous()):
+                _dev(t, f"tensor {i}")
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"tensor {i} is on {t.device}, the first on {dev}")
+        # the storages stay alive: an address seen again is the same memory
+        storages = [t.untyped_storage() for t in ts]
+        starts, sizes = [t.data_ptr() for t in ts], [t.numel() for t in ts]
+        codes = [_in_dtype(t) for t in ts]
+        spans = sorted((p, p + m * (2 if c == NVFP4MOE_BF16 else 4))
+                       for p, m, c in zip(starts, sizes, codes) if m)
         for (_, end), (start, _) in zip(spans, spans[1:]):
             if start < end:
                 raise ValueError("tensors overlap (or one is listed twice)")
-        self.spans = spans
-        self.dtypes = tuple(t.dtype for t in ts)
-        self.ptrs = (_p * n)(*[p for p, _ in self.key])
-        self.numels = (_c_i64 * n)(*[m for _, m in self.key])
-        self.codes = (_c_int * n)(*[_in_dtype(t) for t in ts])
+        n = len(ts)
+        self.device, self.spans, self.storages = dev, spans, storages
+        self.starts, self.sizes, self.types = starts, sizes, codes
+        self.ptrs, self.numels, self.codes = (_p * n)(*starts), (_c_i64 * n)(*sizes), (_c_int * n)(*codes)
 
     def __len__(self):
         return len(self.tensors)
 
     def current(self):
-        if [(t.data_ptr(), t.numel()) for t in self.tensors] != self.key:
+        if list(map(_torch().Tensor.data_ptr, self.tensors)) != self.starts:
             self._look()
         return self
 
@@ -850,16 +863,11 @@ def moe_grad_sumsq(grads, sumsq=None, workspace=None):
         if sumsq is None:
             raise ValueError("an empty list needs sumsq (which device?)")
         dev = sumsq.device
-    sumsq = _buf(sumsq, "sumsq", torch.float64, (1,), dev)
-    if workspace is None:
-        workspace = torch.empty((grad_workspace_size(len(g)),), dtype=torch.uint8, device=dev)
-    else:
-        _dev(workspace, "workspace", torch.uint8)
-        if workspace.device != dev:
-            raise ValueError(f"workspace must be on {dev}")
-    _launch(dev, "moe_grad_sumsq", g.ptrs, g.codes, g.numels, len(g), sumsq.data_ptr(),
-            workspace.data_ptr(), workspace.numel())
-    return sumsq
+    o = {"sumsq": sumsq}
+    ws, ws_bytes = _workspace(workspace, grad_workspace_size(len(g)), dev)
+    _launch(dev, "moe_grad_sumsq", g.ptrs, g.codes, g.numels, len(g),
+            _buf(o, "sumsq", torch.float64, (1,), dev), ws.data_ptr(), ws_bytes)
+    return o["sumsq"]
 
 
 def moe_grad_clip(grads, sumsq, max_norm, outs=None, norm=None):
@@ -874,13 +882,14 @@ def moe_grad_clip(grads, sumsq, max_norm, outs=None, norm=None):
     o = g
     if outs is not None and outs is not grads:
         o = _grad_list(outs)
-        if o.dtypes != g.dtypes or [m for _, m in o.key] != [m for _, m in g.key]:
+        if o.types != g.types or o.sizes != g.sizes:
             raise ValueError("outs must have the gradients' types and sizes")
-        if o.key != g.key and _overlap(g.spans, o.spans):
+        if o.starts != g.starts and _overlap(g.spans, o.spans):
             raise ValueError("outs must be the gradients themselves or apart from them")
-    if any(d not in (None, dev) for d in (g.device, o.device)):
+    if not (g.device in (None, dev) and o.device in (None, dev)):
         raise ValueError(f"sumsq is on {dev}, the gradients or outs elsewhere")
-    norm = _buf(norm, "norm", torch.float32, (1,), dev)
+    res = {"norm": norm}
     _launch(dev, "moe_grad_clip", g.ptrs, o.ptrs, g.codes, g.numels, len(g),
-            _on(sumsq, "sumsq", torch.float64, (1,), dev), float(max_norm), norm.data_ptr())
-    return norm
+            _on(sumsq, "sumsq", torch.float64, (1,), dev), max_norm,
+            _buf(res, "norm", torch.float32, (1,), dev))
+    return res["norm"]
