@@ -9,10 +9,11 @@
 //           p the scores of a row summing to one;
 //   loss    alpha * E * sum_e counts[e] / (N k) * prob_sum[e] / N.
 //
-// One wavefront takes a row, lane l its experts l, l + 64, ...: every load and
-// store is one run of lanes, a lane meets the same experts in every row (their
-// probability sums and loss gradients stay in registers), and the k results
-// sit in the first k lanes.
+// A group of L lanes takes a row, lane l its experts l, l + L, ...: every load
+// and store is one run of lanes, a lane meets the same experts in every row
+// (their probability sums and loss gradients stay in registers), and the k
+// results sit in the group's first k lanes. L is the wavefront, or 16 (four
+// rows to a wavefront, joined by DPP operands alone) up to 64 experts.
 #include "codecs.hpp"
 #include "internal.hpp"
 
@@ -20,7 +21,7 @@ namespace nvfp4moe {
 
 namespace {
 
-constexpr int kWaves = 4;                  // rows in flight per workgroup
+constexpr int kWaves = 8;                  // wavefronts of a workgroup
 constexpr float kNegInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ float load1(const void* p, bool bf16, int64_t i) {
@@ -38,25 +39,56 @@ __device__ __forceinline__ uint32_t across(uint32_t v) {
 }
 template <int STEP>
 __device__ __forceinline__ float across(float v) { return u2f(across<STEP>(f2u(v))); }
+template <int STEP>
+__device__ __forceinline__ int across(int v) { return (int)across<STEP>((uint32_t)v); }
+template <int STEP>
+__device__ __forceinline__ double across(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const uint64_t r = ((uint64_t)across<STEP>((uint32_t)(u >> 32)) << 32) | across<STEP>((uint32_t)u);
+  return __longlong_as_double((int64_t)r);
+}
 
-// Sum and maximum over the wavefront, in every lane: four DPP steps make rows
-// of 16 uniform, the row swaps join them.
-template <class Op>
-__device__ __forceinline__ float wave_join(float v, Op op) {
+// A value joined over the group of L lanes, in every lane: four DPP steps make
+// rows of 16 uniform; the two halves of each pair of rows, then of the
+// wavefront, meet in the results of a row swap.
+template <int L, class T, class Op>
+__device__ __forceinline__ T group_join(T v, Op op) {
   v = op(v, across<0>(v));
   v = op(v, across<1>(v));
   v = op(v, across<2>(v));
   v = op(v, across<3>(v));
-  const auto r16 = __builtin_amdgcn_permlane16_swap(f2u(v), f2u(v), false, false);
-  v = op(u2f(r16[0]), u2f(r16[1]));
-  const auto r32 = __builtin_amdgcn_permlane32_swap(f2u(v), f2u(v), false, false);
-  return op(u2f(r32[0]), u2f(r32[1]));
+  if constexpr (L == 64) {
+    if constexpr (sizeof(T) == 4) {
+      const uint32_t u = __builtin_bit_cast(uint32_t, v);
+      const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+      const uint32_t r0 = r[0], r1 = r[1];
+      v = op(__builtin_bit_cast(T, r0), __builtin_bit_cast(T, r1));
+      const uint32_t x = __builtin_bit_cast(uint32_t, v);
+      const auto q = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+      const uint32_t q0 = q[0], q1 = q[1];
+      v = op(__builtin_bit_cast(T, q0), __builtin_bit_cast(T, q1));
+    } else {
+      v = op(v, __shfl_xor(v, 16, 64));
+      v = op(v, __shfl_xor(v, 32, 64));
+    }
+  }
+  return v;
 }
-__device__ __forceinline__ float wave_sum(float v) {
-  return wave_join(v, [](float a, float b) { return a + b; });
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+  return group_join<L>(v, [](float a, float b) { return a + b; });
 }
-__device__ __forceinline__ float wave_max(float v) {
-  return wave_join(v, [](float a, float b) { return fmaxf(a, b); });
+template <int L>
+__device__ __forceinline__ float group_max(float v) {
+  return group_join<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int L>
+__device__ __forceinline__ double group_max(double v) {
+  return group_join<L>(v, [](double a, double b) { return fmax(a, b); });
+}
+template <int L>
+__device__ __forceinline__ int group_min(int v) {
+  return group_join<L>(v, [](int a, int b) { return a < b ? a : b; });
 }
 
 // Orders the LDS accesses of one wavefront's lanes before and after it (the
@@ -88,35 +120,38 @@ __device__ __forceinline__ double biased_key(float x, float bias) {
   return 1.0 / (1.0 + exp(-(double)x)) + (double)bias;
 }
 
-// k rounds of taking the largest remaining key, the lowest expert first among
-// equals. Lane j ends with the j-th expert (or -1) in id.
-template <int NV, typename Key>
-__device__ __forceinline__ void select_rounds(Key (&key)[NV], int k, int lane, int& id) {
+// k rounds of taking the group's largest remaining key, the lowest expert
+// first among equals. Lane j of the group ends with the j-th expert (or -1)
+// in id and its logit in sx.
+template <int L, int NV, typename Key>
+__device__ __forceinline__ void select_rounds(Key (&key)[NV], const float (&x)[NV], int k, int l,
+                                              int& id, float& sx) {
   const Key none = (Key)kNegInf;
+  constexpr int far = 0x7FFFFFFF;
   id = -1;
+  sx = kNegInf;
   for (int j = 0; j < k; ++j) {
     Key best = none;
-    int at = 0x7FFFFFFF;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) best = key[i] > best ? key[i] : best;
+    best = group_max<L>(best);
+    if (!__any(best > none)) break;        // no group of the wavefront has one left
+    int at = far;
+#pragma unroll
+    for (int i = NV - 1; i >= 0; --i) at = key[i] == best ? i * L + l : at;
+    at = best > none ? group_min<L>(at) : far;
+    float v = kNegInf;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i * 64 + lane;
+      if (at == i * L + l) {
+        key[i] = none;
+        v = x[i];
       }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      const Key o = __shfl_xor(best, off, 64);
-      const int oat = __shfl_xor(at, off, 64);
-      if (o > best || (o == best && oat < at)) {
-        best = o;
-        at = oat;
-      }
+    v = group_max<L>(v);
+    if (l == j && at != far) {
+      id = at;
+      sx = v;
     }
-    if (!(best > none)) return;            // the same for the whole wavefront
-    if (lane == j) id = at;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (at == i * 64 + lane) key[i] = none;
   }
 }
 
@@ -211,16 +246,13 @@ __device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g
     if constexpr (BIAS) {
       double key64[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i) {       // one after the other: a rare path, few registers
         key64[i] = x[i] > kNegInf ? biased_key(x[i], bias[i]) : (double)kNegInf;
-      select_rounds<NV>(key64, k, lane, id);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      select_rounds<64, NV>(key64, x, k, lane, id, sx);
     } else {
-      select_rounds<NV>(key, k, lane, id);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const float v = __shfl(x[i], id & 63, 64);
-      if (id >= 0 && (id >> 6) == i) sx = v;
+      select_rounds<64, NV>(key, x, k, lane, id, sx);
     }
     return;
   }
@@ -273,23 +305,27 @@ struct RouteArgs {
   int E, k;
   const float* bias;
   const uint8_t* token_mask;
+  bool renorm;
   float scale;
   int32_t* topk_ids;
   float* gate;
   RoutePart* parts;      // [grid, E + 1], the last one's count the tokens
 };
 
-template <bool BF, bool SIG, bool RENORM, bool BIAS, bool STATS, int NV>
+template <bool BF, bool SIG, bool BIAS, bool STATS, int L, int NV>
 __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
-  __shared__ float sh_prob[STATS ? kWaves * NV * 64 : 1];
-  __shared__ int32_t sh_count[STATS ? NV * 64 + 1 : 1];
-  __shared__ Candidate list[kWaves][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  constexpr int R = 64 / L;                // rows of a wavefront
+  __shared__ float sh_prob[STATS ? kWaves * 64 * NV : 1];
+  __shared__ int32_t sh_count[STATS ? NV * L + 1 : 1];
+  __shared__ Candidate list[L == 64 ? kWaves : 1][64];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l = lane & (L - 1), g = L == 64 ? 0 : lane / L;
   const int E = a.E, k = a.k;
+  const bool renorm = a.renorm;
   float bias[BIAS ? NV : 1];
   if constexpr (BIAS) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) bias[i] = i * 64 + lane < E ? a.bias[i * 64 + lane] : 0.0f;
+    for (int i = 0; i < NV; ++i) bias[i] = i * L + l < E ? a.bias[i * L + l] : 0.0f;
   }
   float psum[STATS ? NV : 1];
   if constexpr (STATS) {
@@ -298,79 +334,100 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
     for (int e = threadIdx.x; e <= E; e += 64 * kWaves) sh_count[e] = 0;
     __syncthreads();
   }
-  for (int64_t t = (int64_t)blockIdx.x * kWaves + w; t < a.T; t += (int64_t)gridDim.x * kWaves) {
-    const bool on = a.token_mask == nullptr || a.token_mask[t] != 0;
+  // a row's logits, loaded one row ahead of their use
+  const auto load = [&](int64_t t, float (&v)[NV], bool& on) {
+    on = t < a.T && (a.token_mask == nullptr || a.token_mask[t] != 0);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      v[i] = t < a.T && i * L + l < E ? load1(a.logits, BF, t * E + i * L + l) : kNegInf;
+  };
+  const int64_t stride = (int64_t)gridDim.x * kWaves * R;
+  int64_t t0 = ((int64_t)blockIdx.x * kWaves + w) * R;
+  float next[NV];
+  bool next_on;
+  load(t0 + g, next, next_on);
+  for (; t0 < a.T; t0 += stride) {
+    const int64_t t = t0 + g;
     float x[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = i * 64 + lane;
-      x[i] = on && e < E ? load1(a.logits, BF, t * E + e) : kNegInf;
-    }
+    for (int i = 0; i < NV; ++i) x[i] = next_on ? next[i] : kNegInf;
+    load(t + stride, next, next_on);
     int id;
     float sx;
-    select<BIAS, NV>(x, a.bias, bias, k, lane, list[w], id, sx);
-    const bool live = __builtin_amdgcn_readfirstlane(id) >= 0;
+    if constexpr (L == 64) {
+      select<BIAS, NV>(x, a.bias, bias, k, lane, list[w], id, sx);
+    } else if constexpr (BIAS) {
+      double key[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        key[i] = x[i] > kNegInf ? biased_key(x[i], bias[i]) : (double)kNegInf;
+      select_rounds<L, NV>(key, x, k, l, id, sx);
+    } else {
+      float key[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) key[i] = x[i];
+      select_rounds<L, NV>(key, x, k, l, id, sx);
+    }
+    // the row has an expert: its first slot is taken
+    const bool live = L == 64 ? __builtin_amdgcn_readfirstlane(id) >= 0 : group_max<L>((float)id) >= 0.0f;
     // scores; the row's probabilities where they are needed
-    float top = kNegInf, total = 0.0f, p[NV];
-    if constexpr (STATS || (!SIG && !RENORM)) {
-      if (live) {
-        if constexpr (!SIG) {
+    float top = 0.0f, total = 0.0f, p[NV];
+    if (STATS || (!SIG && !renorm)) {
+      if constexpr (!SIG) {
+        float m = kNegInf;
 #pragma unroll
-          for (int i = 0; i < NV; ++i) top = fmaxf(top, x[i]);
-          top = wave_max(top);
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          if constexpr (SIG) {
-            float ds;
-            sigmoid(x[i], p[i], ds);
-          } else {
-            p[i] = exp_neg(x[i] - top);
-          }
-          total += p[i];
-        }
-        total = wave_sum(total);
+        for (int i = 0; i < NV; ++i) m = fmaxf(m, x[i]);
+        m = group_max<L>(m);
+        top = live ? m : 0.0f;
       }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if constexpr (SIG) {
+          float ds;
+          sigmoid(x[i], p[i], ds);
+        } else {
+          p[i] = exp_neg(x[i] - top);
+        }
+        total += p[i];
+      }
+      total = group_sum<L>(total);
     }
     if constexpr (STATS) {
-      if (live && total > 0.0f) {
-        const float r = 1.0f / total;
+      const float r = live && total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) psum[i] += p[i] * r;
-      }
-      if (lane < k && id >= 0) atomicAdd(&sh_count[id], 1);
-      if (lane == 0 && live) atomicAdd(&sh_count[E], 1);
+      for (int i = 0; i < NV; ++i) psum[i] += p[i] * r;
+      if (l < k && id >= 0) atomicAdd(&sh_count[id], 1);
+      if (l == 0 && live) atomicAdd(&sh_count[E], 1);
     }
     // gates of the selected, one per lane
-    float g = 0.0f;
-    if (live) {
-      if constexpr (SIG) {
-        float ds;
-        if (id >= 0) sigmoid(sx, g, ds);
-      } else if constexpr (RENORM) {
-        g = exp_neg(sx - wave_max(sx));
-      } else {
-        g = exp_neg(sx - top) / total;
-      }
-      if constexpr (RENORM) {
-        const float sum = wave_sum(g);
-        g = sum > 0.0f ? g / sum : 0.0f;
-      }
+    float gate = 0.0f;
+    if constexpr (SIG) {
+      float ds;
+      sigmoid(sx, gate, ds);               // 0 in empty slots, whose logit is -inf
+    } else if (renorm) {
+      const float m = group_max<L>(sx);
+      gate = exp_neg(sx - (live ? m : 0.0f));
+    } else {
+      gate = total > 0.0f ? exp_neg(sx - top) / total : 0.0f;
     }
-    if (lane < k) {
-      a.topk_ids[t * k + lane] = id;
-      a.gate[t * k + lane] = g * a.scale;
+    if (renorm) {
+      const float sum = group_sum<L>(gate);
+      gate = sum > 0.0f ? gate / sum : 0.0f;
+    }
+    if (l < k && t < a.T) {
+      a.topk_ids[t * k + l] = id;
+      a.gate[t * k + l] = gate * a.scale;
     }
   }
   if constexpr (STATS) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) sh_prob[w * NV * 64 + i * 64 + lane] = psum[i];
+    for (int i = 0; i < NV; ++i) sh_prob[(w * R + g) * NV * L + i * L + l] = psum[i];
     __syncthreads();
     for (int e = threadIdx.x; e <= E; e += 64 * kWaves) {
       float s = 0.0f;
       if (e < E) {
 #pragma unroll
-        for (int v = 0; v < kWaves; ++v) s += sh_prob[v * NV * 64 + e];
+        for (int v = 0; v < kWaves * R; ++v) s += sh_prob[v * NV * L + e];
       }
       a.parts[(int64_t)blockIdx.x * (E + 1) + e] = RoutePart{s, sh_count[e]};
     }
@@ -453,10 +510,13 @@ struct RouteBwdArgs {
 
 // The selected experts' part of a row's gradient is computed one slot per
 // lane and reaches the lanes that own the experts through LDS.
-template <bool BF, bool SIG, bool RENORM, bool BAL, int NV>
+template <bool BF, bool SIG, bool RENORM, bool BAL, int L, int NV>
 __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
-  __shared__ float sh[kWaves][NV * 64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  constexpr int R = 64 / L;
+  __shared__ float sh_all[kWaves * R][NV * L];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l = lane & (L - 1), g = L == 64 ? 0 : lane / L;
+  float* sh = sh_all[w * R + g];
   const int E = a.E, k = a.k;
   float coef[BAL ? NV : 1];
   if constexpr (BAL) {
@@ -465,102 +525,127 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
                              : 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      coef[i] = i * 64 + lane < E ? (float)(c * (double)a.counts[i * 64 + lane]) : 0.0f;
+      coef[i] = i * L + l < E ? (float)(c * (double)a.counts[i * L + l]) : 0.0f;
   }
 #pragma unroll
-  for (int i = 0; i < NV; ++i) sh[w][i * 64 + lane] = 0.0f;
-  for (int64_t t = (int64_t)blockIdx.x * kWaves + w; t < a.T; t += (int64_t)gridDim.x * kWaves) {
-    int id = lane < k ? a.topk_ids[t * k + lane] : -1;
-    if (id >= E) id = -1;
-    const float dg = id >= 0 && a.dgate ? a.dgate[t * k + lane] * a.scale : 0.0f;
+  for (int i = 0; i < NV; ++i) sh[i * L + l] = 0.0f;
+  // a row's operands, loaded one row ahead of their use
+  const auto load = [&](int64_t t, float (&v)[NV], int& id, float& dg) {
+    const bool slot = t < a.T && l < k;
+    id = slot ? a.topk_ids[t * k + l] : -1;
+    dg = slot && a.dgate ? a.dgate[t * k + l] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      v[i] = t < a.T && i * L + l < E ? load1(a.logits, BF, t * E + i * L + l) : kNegInf;
+  };
+  const int64_t stride = (int64_t)gridDim.x * kWaves * R;
+  int64_t t0 = ((int64_t)blockIdx.x * kWaves + w) * R;
+  float next[NV], next_dg;
+  int next_id;
+  load(t0 + g, next, next_id, next_dg);
+  for (; t0 < a.T; t0 += stride) {
+    const int64_t t = t0 + g;
+    const int id = next_id < E ? next_id : -1;
+    const float dg = id >= 0 ? next_dg * a.scale : 0.0f;
     float x[NV], d[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = i * 64 + lane;
-      x[i] = e < E ? load1(a.logits, BF, t * E + e) : kNegInf;
+    for (int i = 0; i < NV; ++i) x[i] = next[i];
+    load(t + stride, next, next_id, next_dg);
+    const bool live = group_max<L>((float)id) >= 0.0f;
+    // the selected logits: out of the lanes that hold the row
+    float sx = kNegInf;
+    if constexpr (RENORM) {
+      wave_lds_fence();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) sh[i * L + l] = x[i];
+      wave_lds_fence();
+      if (id >= 0) sx = sh[id];
+      wave_lds_fence();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) sh[i * L + l] = 0.0f;
     }
-    const float sx = id >= 0 ? load1(a.logits, BF, t * E + id) : kNegInf;
-    const bool live = __any(id >= 0);
-    if (!live) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) d[i] = 0.0f;
-    } else {
-      // per slot
-      float u = dg;
-      if constexpr (RENORM) {
-        float q = 0.0f;
-        if constexpr (SIG) {
-          float ds;
-          if (id >= 0) sigmoid(sx, q, ds);
-        } else {
-          q = exp_neg(sx - wave_max(sx));
-        }
-        const float sum = wave_sum(q), dot = wave_sum(q * u);
-        const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
-        u = id >= 0 ? (u - dot * r) * r : 0.0f;
-        if constexpr (!SIG) u *= q;
-      }
-      if (id >= 0) atomicAdd(&sh[w][id], u);
-      wave_lds_fence();
-#pragma unroll
-      for (int i = 0; i < NV; ++i) d[i] = sh[w][i * 64 + lane];
-      wave_lds_fence();
-      if (id >= 0) sh[w][id] = 0.0f;
-      // per expert
+    // per slot
+    float u = dg;
+    if constexpr (RENORM) {
+      float q;
       if constexpr (SIG) {
-        float s[NV], ds[NV], total = 0.0f, dot = 0.0f;
+        float ds;
+        sigmoid(sx, q, ds);                // 0 in empty slots, whose logit is -inf
+      } else {
+        const float m = group_max<L>(sx);
+        q = exp_neg(sx - (m > kNegInf ? m : 0.0f));
+      }
+      const float sum = group_sum<L>(q), dot = group_sum<L>(q * u);
+      const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
+      u = (u - dot * r) * r;
+      if constexpr (!SIG) u *= q;
+    }
+    wave_lds_fence();
+    if (id >= 0) atomicAdd(&sh[id], u);
+    wave_lds_fence();
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          sigmoid(x[i], s[i], ds[i]);
-          if constexpr (BAL) {
-            total += s[i];
-            dot += s[i] * coef[i];
-          }
-        }
+    for (int i = 0; i < NV; ++i) d[i] = sh[i * L + l];
+    wave_lds_fence();
+    if (id >= 0) sh[id] = 0.0f;
+    // per expert
+    if constexpr (SIG) {
+      float s[NV], ds[NV], total = 0.0f, dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        sigmoid(x[i], s[i], ds[i]);
         if constexpr (BAL) {
-          total = wave_sum(total);
-          dot = wave_sum(dot);
-          const float r = total > 0.0f ? 1.0f / total : 0.0f;
-#pragma unroll
-          for (int i = 0; i < NV; ++i) d[i] += (coef[i] - dot * r) * r;
+          total += s[i];
+          dot += s[i] * coef[i];
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) d[i] *= ds[i];
-      } else if constexpr (BAL || !RENORM) {
-        float top = kNegInf, total = 0.0f, dot = 0.0f, p[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) top = fmaxf(top, x[i]);
-        top = wave_max(top);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          p[i] = exp_neg(x[i] - top);
-          float v = RENORM ? 0.0f : d[i];
-          if constexpr (BAL) v += coef[i];
-          total += p[i];
-          dot += p[i] * v;
-        }
-        total = wave_sum(total);
-        dot = wave_sum(dot);
+      }
+      if constexpr (BAL) {
+        total = group_sum<L>(total);
+        dot = group_sum<L>(dot);
         const float r = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          float v = RENORM ? 0.0f : d[i];
-          if constexpr (BAL) v += coef[i];
-          const float dp = p[i] * r * (v - dot * r);
-          d[i] = RENORM ? d[i] + dp : dp;
-        }
+        for (int i = 0; i < NV; ++i) d[i] += (coef[i] - dot * r) * r;
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) d[i] *= ds[i];
+    } else if constexpr (BAL || !RENORM) {
+      float top = kNegInf, total = 0.0f, dot = 0.0f, p[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) top = fmaxf(top, x[i]);
+      top = group_max<L>(top);
+      top = top > kNegInf ? top : 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        p[i] = exp_neg(x[i] - top);
+        float v = RENORM ? 0.0f : d[i];
+        if constexpr (BAL) v += coef[i];
+        total += p[i];
+        dot += p[i] * v;
+      }
+      total = group_sum<L>(total);
+      dot = group_sum<L>(dot);
+      const float r = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float v = RENORM ? 0.0f : d[i];
+        if constexpr (BAL) v += coef[i];
+        const float dp = p[i] * r * (v - dot * r);
+        d[i] = RENORM ? d[i] + dp : dp;
       }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = i * 64 + lane;
-      if (e < E) {
-        if constexpr (BF) static_cast<uint16_t*>(a.dlogits)[t * E + e] = (uint16_t)pk_bf16(d[i], 0.0f);
-        else static_cast<float*>(a.dlogits)[t * E + e] = d[i];
+      const int e = i * L + l;
+      if (e < E && t < a.T) {
+        const float y = live ? d[i] : 0.0f;
+        if constexpr (BF) static_cast<uint16_t*>(a.dlogits)[t * E + e] = (uint16_t)pk_bf16(y, 0.0f);
+        else static_cast<float*>(a.dlogits)[t * E + e] = y;
       }
     }
   }
 }
+
+// Whether rows go to groups of 16 lanes.
+bool narrow(int E, int k) { return E <= 64 && k <= 16; }
 
 // Experts per lane, rounded up to a form that is built.
 int lanes_experts(int E) {
@@ -568,47 +653,78 @@ int lanes_experts(int E) {
   return nv <= 1 ? 1 : nv <= 2 ? 2 : nv <= 4 ? 4 : nv <= 6 ? 6 : nv <= 8 ? 8 : 16;
 }
 
-int64_t route_grid(int64_t T, int per_cu) {
-  const int64_t need = (T + kWaves - 1) / kWaves, most = (int64_t)device_cu_count() * per_cu;
+constexpr int kPerCu = 4;                  // workgroups that fill a compute unit
+
+// Workgroups of a launch over T rows.
+int64_t route_grid(int64_t T, int E, int k) {
+  const int64_t rows = narrow(E, k) ? kWaves * 4 : kWaves;
+  const int64_t need = (T + rows - 1) / rows;
+  const int64_t most = (int64_t)device_cu_count() * kPerCu;
   return need < most ? need : most;
 }
 
-constexpr int kStatsPerCu = 4;             // workgroups per CU that leave a partial
-
-template <bool BF, bool SIG, bool RENORM, bool BIAS, bool STATS>
+template <bool BF, bool SIG, bool BIAS, bool STATS>
 void route_nv(const RouteArgs& a, unsigned grid, hipStream_t s) {
-  switch (lanes_experts(a.E)) {
-    case 1: k_route<BF, SIG, RENORM, BIAS, STATS, 1><<<grid, 64 * kWaves, 0, s>>>(a); break;
-    case 2: k_route<BF, SIG, RENORM, BIAS, STATS, 2><<<grid, 64 * kWaves, 0, s>>>(a); break;
-    case 4: k_route<BF, SIG, RENORM, BIAS, STATS, 4><<<grid, 64 * kWaves, 0, s>>>(a); break;
-    case 6: k_route<BF, SIG, RENORM, BIAS, STATS, 6><<<grid, 64 * kWaves, 0, s>>>(a); break;
-    case 8: k_route<BF, SIG, RENORM, BIAS, STATS, 8><<<grid, 64 * kWaves, 0, s>>>(a); break;
-    default: k_route<BF, SIG, RENORM, BIAS, STATS, 16><<<grid, 64 * kWaves, 0, s>>>(a); break;
+#define NVFP4MOE_ROUTE(L, NV) k_route<BF, SIG, BIAS, STATS, L, NV><<<grid, 64 * kWaves, 0, s>>>(a)
+  if (narrow(a.E, a.k)) {
+    if (a.E <= 16) NVFP4MOE_ROUTE(16, 1);
+    else if (a.E <= 32) NVFP4MOE_ROUTE(16, 2);
+    else NVFP4MOE_ROUTE(16, 4);
+    return;
   }
+  switch (lanes_experts(a.E)) {
+    case 1: NVFP4MOE_ROUTE(64, 1); break;
+    case 2: NVFP4MOE_ROUTE(64, 2); break;
+    case 4: NVFP4MOE_ROUTE(64, 4); break;
+    case 6: NVFP4MOE_ROUTE(64, 6); break;
+    case 8: NVFP4MOE_ROUTE(64, 8); break;
+    default: NVFP4MOE_ROUTE(64, 16); break;
+  }
+#undef NVFP4MOE_ROUTE
 }
 
-template <bool BF, bool SIG, bool RENORM>
-void route_form(const RouteArgs& a, bool stats, unsigned grid, hipStream_t s) {
-  if constexpr (SIG) {
-    if (a.bias) {
-      if (stats) route_nv<BF, SIG, RENORM, true, true>(a, grid, s);
-      else route_nv<BF, SIG, RENORM, true, false>(a, grid, s);
-      return;
-    }
+template <bool BF>
+void route_form(const RouteArgs& a, bool sigmoid, bool stats, unsigned grid, hipStream_t s) {
+  if (!sigmoid) {
+    if (stats) route_nv<BF, false, false, true>(a, grid, s);
+    else route_nv<BF, false, false, false>(a, grid, s);
+  } else if (a.bias) {
+    if (stats) route_nv<BF, true, true, true>(a, grid, s);
+    else route_nv<BF, true, true, false>(a, grid, s);
+  } else {
+    if (stats) route_nv<BF, true, false, true>(a, grid, s);
+    else route_nv<BF, true, false, false>(a, grid, s);
   }
-  if (stats) route_nv<BF, SIG, RENORM, false, true>(a, grid, s);
-  else route_nv<BF, SIG, RENORM, false, false>(a, grid, s);
 }
 
 template <bool BF, bool SIG, bool RENORM, bool BAL>
 void bwd_nv(const RouteBwdArgs& a, unsigned grid, hipStream_t s) {
+#define NVFP4MOE_BWD(L, NV) k_route_bwd<BF, SIG, RENORM, BAL, L, NV><<<grid, 64 * kWaves, 0, s>>>(a)
+  if (narrow(a.E, a.k)) {
+    if (a.E <= 16) NVFP4MOE_BWD(16, 1);
+    else if (a.E <= 32) NVFP4MOE_BWD(16, 2);
+    else NVFP4MOE_BWD(16, 4);
+    return;
+  }
   switch (lanes_experts(a.E)) {
-    case 1: k_route_bwd<BF, SIG, RENORM, BAL, 1><<<grid, 64 * kWaves, 0, s>>>(a); break;
-    case 2: k_route_bwd<BF, SIG, RENORM, BAL, 2><<<grid, 64 * kWaves, 0, s>>>(a); break;
-    case 4: k_route_bwd<BF, SIG, RENORM, BAL, 4><<<grid, 64 * kWaves, 0, s>>>(a); break;
-    case 6: k_route_bwd<BF, SIG, RENORM, BAL, 6><<<grid, 64 * kWaves, 0, s>>>(a); break;
-    case 8: k_route_bwd<BF, SIG, RENORM, BAL, 8><<<grid, 64 * kWaves, 0, s>>>(a); break;
-    default: k_route_bwd<BF, SIG, RENORM, BAL, 16><<<grid, 64 * kWaves, 0, s>>>(a); break;
+    case 1: NVFP4MOE_BWD(64, 1); break;
+    case 2: NVFP4MOE_BWD(64, 2); break;
+    case 4: NVFP4MOE_BWD(64, 4); break;
+    case 6: NVFP4MOE_BWD(64, 6); break;
+    case 8: NVFP4MOE_BWD(64, 8); break;
+    default: NVFP4MOE_BWD(64, 16); break;
+  }
+#undef NVFP4MOE_BWD
+}
+
+template <bool BF, bool SIG>
+void bwd_form(const RouteBwdArgs& a, bool renorm, unsigned grid, hipStream_t s) {
+  if (renorm) {
+    if (a.counts) bwd_nv<BF, SIG, true, true>(a, grid, s);
+    else bwd_nv<BF, SIG, true, false>(a, grid, s);
+  } else {
+    if (a.counts) bwd_nv<BF, SIG, false, true>(a, grid, s);
+    else bwd_nv<BF, SIG, false, false>(a, grid, s);
   }
 }
 
@@ -625,29 +741,13 @@ hipError_t launch_route(const void* logits, bool bf16, int64_t T, int E, int k, 
                         int32_t* topk_ids, float* gate, int64_t* counts, float* prob_sum,
                         void* workspace, hipStream_t stream) {
   const bool stats = counts != nullptr;
-  int64_t grid = route_grid(T, stats ? kStatsPerCu : 8);
+  int64_t grid = route_grid(T, E, k);
   if (stats && grid > kMaxRouteParts) grid = kMaxRouteParts;
-  RouteArgs a{logits, T, E, k, bias, token_mask, scale, topk_ids, gate,
-              static_cast<RoutePart*>(workspace)};
+  const RouteArgs a{logits, T, E, k, bias, token_mask, renorm, scale, topk_ids, gate,
+                    static_cast<RoutePart*>(workspace)};
   if (grid > 0) {
-    const unsigned g = (unsigned)grid;
-    if (bf16) {
-      if (sigmoid) {
-        if (renorm) route_form<true, true, true>(a, stats, g, stream);
-        else route_form<true, true, false>(a, stats, g, stream);
-      } else {
-        if (renorm) route_form<true, false, true>(a, stats, g, stream);
-        else route_form<true, false, false>(a, stats, g, stream);
-      }
-    } else {
-      if (sigmoid) {
-        if (renorm) route_form<false, true, true>(a, stats, g, stream);
-        else route_form<false, true, false>(a, stats, g, stream);
-      } else {
-        if (renorm) route_form<false, false, true>(a, stats, g, stream);
-        else route_form<false, false, false>(a, stats, g, stream);
-      }
-    }
+    if (bf16) route_form<true>(a, sigmoid, stats, (unsigned)grid, stream);
+    else route_form<false>(a, sigmoid, stats, (unsigned)grid, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -669,26 +769,14 @@ hipError_t launch_route_bwd(const void* logits, bool bf16, int64_t T, int E, int
                             hipStream_t stream) {
   if (T == 0) return hipSuccess;
   const RouteBwdArgs a{logits, T, E, k, topk_ids, dgate, scale, counts, alpha, dloss, dlogits};
-  const unsigned g = (unsigned)route_grid(T, 8);
-#define NVFP4MOE_BWD(BF, SIG, REN)                                   \
-  do {                                                               \
-    if (counts) bwd_nv<BF, SIG, REN, true>(a, g, stream);            \
-    else bwd_nv<BF, SIG, REN, false>(a, g, stream);                  \
-  } while (0)
+  const unsigned g = (unsigned)route_grid(T, E, k);
   if (bf16) {
-    if (sigmoid) {
-      if (renorm) NVFP4MOE_BWD(true, true, true); else NVFP4MOE_BWD(true, true, false);
-    } else {
-      if (renorm) NVFP4MOE_BWD(true, false, true); else NVFP4MOE_BWD(true, false, false);
-    }
+    if (sigmoid) bwd_form<true, true>(a, renorm, g, stream);
+    else bwd_form<true, false>(a, renorm, g, stream);
   } else {
-    if (sigmoid) {
-      if (renorm) NVFP4MOE_BWD(false, true, true); else NVFP4MOE_BWD(false, true, false);
-    } else {
-      if (renorm) NVFP4MOE_BWD(false, false, true); else NVFP4MOE_BWD(false, false, false);
-    }
+    if (sigmoid) bwd_form<false, true>(a, renorm, g, stream);
+    else bwd_form<false, false>(a, renorm, g, stream);
   }
-#undef NVFP4MOE_BWD
   return hipGetLastError();
 }
 
