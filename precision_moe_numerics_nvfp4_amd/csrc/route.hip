@@ -28,6 +28,11 @@ __device__ __forceinline__ float load1(const void* p, bool bf16, int64_t i) {
   return bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 
+template <bool BF>
+__device__ __forceinline__ const void* row_of(const void* p, int64_t i) {
+  return static_cast<const char*>(p) + i * (BF ? 2 : 4);
+}
+
 // The value of the lane across in a group of 2, 4, 8, 16 (each step reaches the
 // half of its group that the earlier ones did not): DPP operands, no LDS.
 template <int STEP>
@@ -189,16 +194,14 @@ __device__ __forceinline__ float k_reached(float v, int k) {
   uint32_t top = max(max(at(hi, 0), at(hi, 16)), max(at(hi, 32), at(hi, 48)));
   uint32_t low = min(min(at(lo, 0), at(lo, 16)), min(at(lo, 32), at(lo, 48)));
   low = max(low, ordered(kNegInf) + 1u);
+  // enough is a few more than k: a candidate costs less than another step (and
+  // a step with low and top met changes neither)
   for (int step = 0; step < 8; ++step) {
     const uint32_t mid = low + ((top - low + 1u) >> 1);
-    if (mid <= low || top < low) break;
-    const int n = __popcll(__ballot(u >= mid));
-    if (n >= k) {
-      low = mid;
-      if (n == k) break;
-    } else {
-      top = mid - 1u;
-    }
+    const int more = (int)__popcll(__ballot(u >= mid)) - k;
+    low = more >= 0 ? mid : low;
+    top = more >= 0 ? top : mid - 1u;
+    if ((uint32_t)more <= 2u) break;
   }
   return unordered(low);
 }
@@ -232,12 +235,12 @@ __device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g
   }
   float cut = k_reached(best, k);
   // |float32 key - key| <= 8 * 2^-24 + 2^-24 |key| (sigmoid and the sum): twice that is far inside
-  if constexpr (BIAS) cut -= 0x1p-19f + 0x1p-21f * fabsf(cut);
+  if constexpr (BIAS) cut = fmaxf(cut - (0x1p-19f + 0x1p-21f * fabsf(cut)), -3.402823466e38f);
   int n = 0;
   uint64_t hit[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    hit[i] = __ballot(key[i] >= cut && key[i] > kNegInf);
+    hit[i] = __ballot(key[i] >= cut);         // the cut is above -inf
     n += __popcll(hit[i]);
   }
   id = -1;
@@ -261,7 +264,7 @@ __device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g
   for (int i = 0; i < NV; ++i) {
     const int at = base + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(hit[i] >> 32),
                                                          __builtin_amdgcn_mbcnt_lo((uint32_t)hit[i], 0));
-    if ((hit[i] >> lane) & 1) list[at] = Candidate{x[i], i * 64 + lane};
+    if (key[i] >= cut) list[at] = Candidate{x[i], i * 64 + lane};
     base += __popcll(hit[i]);
   }
   wave_lds_fence();
@@ -278,9 +281,13 @@ __device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g
       rank += other > mine || (other == mine && j < lane);
     }
   } else {
+    // one unsigned comparison: the logit, then the earlier place in the list
+    const uint32_t u = ordered(c.x + 0.0f);
+    const uint64_t mine = ((uint64_t)u << 32) | (uint32_t)(63 - lane);
     for (int j = 0; j < n; ++j) {
-      const float other = u2f((uint32_t)__builtin_amdgcn_readlane((int)f2u(c.x), j));
-      rank += other > c.x || (other == c.x && j < lane);
+      const uint64_t other =
+          ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)u, j) << 32) | (uint32_t)(63 - j);
+      rank += other > mine;
     }
   }
   if (lane < n && rank < k) list[rank] = c;
@@ -334,12 +341,16 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
     for (int e = threadIdx.x; e <= E; e += 64 * kWaves) sh_count[e] = 0;
     __syncthreads();
   }
-  // a row's logits, loaded one row ahead of their use
-  const auto load = [&](int64_t t, float (&v)[NV], bool& on) {
-    on = t < a.T && (a.token_mask == nullptr || a.token_mask[t] != 0);
+  // A row's logits, loaded one row ahead of their use. Every lane loads (past
+  // the experts or the rows: the last one again), so that no branch waits.
+  int off[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      v[i] = t < a.T && i * L + l < E ? load1(a.logits, BF, t * E + i * L + l) : kNegInf;
+  for (int i = 0; i < NV; ++i) off[i] = i * L + l < E ? i * L + l : E - 1;
+  const auto load = [&](int64_t t, float (&v)[NV], bool& on) {
+    const int64_t row = t < a.T ? t : a.T - 1;
+    on = t < a.T && (a.token_mask == nullptr || a.token_mask[row] != 0);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = load1(row_of<BF>(a.logits, row * E), BF, off[i]);
   };
   const int64_t stride = (int64_t)gridDim.x * kWaves * R;
   int64_t t0 = ((int64_t)blockIdx.x * kWaves + w) * R;
@@ -350,7 +361,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
     const int64_t t = t0 + g;
     float x[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) x[i] = next_on ? next[i] : kNegInf;
+    for (int i = 0; i < NV; ++i) x[i] = next_on && i * L + l < E ? next[i] : kNegInf;
     load(t + stride, next, next_on);
     int id;
     float sx;
@@ -393,7 +404,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
       total = group_sum<L>(total);
     }
     if constexpr (STATS) {
-      const float r = live && total > 0.0f ? 1.0f / total : 0.0f;
+      const float r = live && total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) psum[i] += p[i] * r;
       if (l < k && id >= 0) atomicAdd(&sh_count[id], 1);
@@ -408,11 +419,11 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
       const float m = group_max<L>(sx);
       gate = exp_neg(sx - (live ? m : 0.0f));
     } else {
-      gate = total > 0.0f ? exp_neg(sx - top) / total : 0.0f;
+      gate = total > 0.0f ? exp_neg(sx - top) * __builtin_amdgcn_rcpf(total) : 0.0f;
     }
     if (renorm) {
       const float sum = group_sum<L>(gate);
-      gate = sum > 0.0f ? gate / sum : 0.0f;
+      gate = sum > 0.0f ? gate * __builtin_amdgcn_rcpf(sum) : 0.0f;
     }
     if (l < k && t < a.T) {
       a.topk_ids[t * k + l] = id;
@@ -529,14 +540,17 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) sh[i * L + l] = 0.0f;
-  // a row's operands, loaded one row ahead of their use
-  const auto load = [&](int64_t t, float (&v)[NV], int& id, float& dg) {
-    const bool slot = t < a.T && l < k;
-    id = slot ? a.topk_ids[t * k + l] : -1;
-    dg = slot && a.dgate ? a.dgate[t * k + l] : 0.0f;
+  // a row's operands, loaded one row ahead of their use (as in k_route)
+  int off[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      v[i] = t < a.T && i * L + l < E ? load1(a.logits, BF, t * E + i * L + l) : kNegInf;
+  for (int i = 0; i < NV; ++i) off[i] = i * L + l < E ? i * L + l : E - 1;
+  const int slot = l < k ? l : k - 1;
+  const auto load = [&](int64_t t, float (&v)[NV], int& id, float& dg) {
+    const int64_t row = t < a.T ? t : a.T - 1;
+    id = a.topk_ids[row * k + slot];
+    dg = a.dgate ? a.dgate[row * k + slot] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = load1(row_of<BF>(a.logits, row * E), BF, off[i]);
   };
   const int64_t stride = (int64_t)gridDim.x * kWaves * R;
   int64_t t0 = ((int64_t)blockIdx.x * kWaves + w) * R;
@@ -545,11 +559,11 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
   load(t0 + g, next, next_id, next_dg);
   for (; t0 < a.T; t0 += stride) {
     const int64_t t = t0 + g;
-    const int id = next_id < E ? next_id : -1;
+    const int id = l < k && t < a.T && next_id >= 0 && next_id < E ? next_id : -1;
     const float dg = id >= 0 ? next_dg * a.scale : 0.0f;
     float x[NV], d[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) x[i] = next[i];
+    for (int i = 0; i < NV; ++i) x[i] = i * L + l < E ? next[i] : kNegInf;
     load(t + stride, next, next_id, next_dg);
     const bool live = group_max<L>((float)id) >= 0.0f;
     // the selected logits: out of the lanes that hold the row
@@ -576,7 +590,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
         q = exp_neg(sx - (m > kNegInf ? m : 0.0f));
       }
       const float sum = group_sum<L>(q), dot = group_sum<L>(q * u);
-      const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
+      const float r = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
       u = (u - dot * r) * r;
       if constexpr (!SIG) u *= q;
     }
@@ -601,7 +615,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
       if constexpr (BAL) {
         total = group_sum<L>(total);
         dot = group_sum<L>(dot);
-        const float r = total > 0.0f ? 1.0f / total : 0.0f;
+        const float r = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) d[i] += (coef[i] - dot * r) * r;
       }
@@ -623,7 +637,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
       }
       total = group_sum<L>(total);
       dot = group_sum<L>(dot);
-      const float r = total > 0.0f ? 1.0f / total : 0.0f;
+      const float r = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float v = RENORM ? 0.0f : d[i];
