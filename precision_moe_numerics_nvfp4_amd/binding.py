@@ -5,6 +5,7 @@ torch (device memory), the current stream, and status-code -> exception.
 """
 
 import ctypes
+import functools
 import os
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4moe.so")
@@ -73,6 +74,7 @@ SIGNATURES = {
 }
 
 _LIB = None
+_TORCH = None
 
 
 class Nvfp4moeError(RuntimeError):
@@ -112,8 +114,12 @@ def _check(fn, status):
 
 
 def _torch():
-    import torch
-    return torch
+    """torch, imported with the first call that needs it."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _dev(t, name, dtype=None, ndim=None):
@@ -710,6 +716,7 @@ def _score(score):
     return _SCORES[score]
 
 
+@functools.lru_cache(maxsize=256)
 def route_workspace_size(T, E):
     return int(lib().nvfp4moe_route_workspace_size(int(T), int(E)))
 
@@ -850,6 +857,7 @@ def _overlap(a, b):
     return False
 
 
+@functools.lru_cache(maxsize=256)
 def grad_workspace_size(n):
     return int(lib().nvfp4moe_grad_workspace_size(int(n)))
 

@@ -10,8 +10,10 @@ orientations, run the dgrad and wgrad grouped GEMMs.
 
 Also here: the expert FFN around the layer (ExpertFFNStep: down-projection,
 per-token re-quantization of the intermediate, weighted combine, backward
-through both projections) and the NVFP4 backward (NVFP4BackwardStep), the
-alternative the pages report as tried first and given up.
+through both projections), the FFN with the router in front of it and the
+clipping of its gradients behind (RoutedFFNStep), and the NVFP4 backward
+(NVFP4BackwardStep), the alternative the pages report as tried first and given
+up.
 
 Every step is a library call on the current stream; buffers are allocated
 once here (torch is the device allocator) so a step allocates nothing.
@@ -201,6 +203,75 @@ class ExpertFFNStep:
         self.quantize_weights(w1, w2)
         self.forward(x, topk_ids, gate)
         self.backward(dout, gate)
+
+
+class RoutedFFNStep:
+    """A training step of the expert FFN from the router's logits on: the
+    selection of k of n_experts experts per token with its gates and per-expert
+    statistics, the balance loss, ExpertFFNStep over the local experts
+    [e0, e0+E), the gradient back to the logits, and the global norm of the
+    expert weight gradients with their clipping in place.
+
+    The FFN's own buffers are ``ffn``'s; ``counts`` and ``prob_sum`` may be
+    summed over data-parallel ranks between route() and loss(), ``ffn.dgate``
+    completed with other ranks' experts between backward_ffn() and
+    backward_route(), and ``sumsq`` summed over ranks between grad_sumsq() and
+    clip(); step() is the single-GPU order of them all."""
+
+    def __init__(self, T, K, F, E, k, n_experts=None, e0=0, score="softmax", renorm=True,
+                 scale=1.0, alpha=0.0, logits_dtype=torch.float32, seed=0x5EED0002, device="cuda"):
+        self.ffn = ExpertFFNStep(T, K, F, E, k, e0=e0, seed=seed, device=device)
+        self.k, self.alpha = k, alpha
+        self.how = dict(score=score, renorm=renorm, scale=scale)
+        n = E if n_experts is None else n_experts
+        dev = self.ffn.out.device
+        e = lambda *s, dt=torch.float32: torch.empty(s, dtype=dt, device=dev)
+        self.routed = dict(topk_ids=e(T, k, dt=torch.int32), gate=e(T, k),
+                           counts=e(n + 1, dt=torch.int64), prob_sum=e(n))
+        self.topk_ids, self.gate, self.counts, self.prob_sum = self.routed.values()
+        self.balance = e(1)
+        self.dlogits = e(T, n, dt=logits_dtype)
+        self.route_ws = e(B.route_workspace_size(T, n), dt=torch.uint8)
+        self.grads = B.GradList([self.ffn.dw1, self.ffn.dw2])
+        self.sumsq, self.norm = e(1, dt=torch.float64), e(1)
+        self.grad_ws = e(B.grad_workspace_size(len(self.grads)), dt=torch.uint8)
+
+    def route(self, logits, bias=None, token_mask=None):
+        B.moe_route(logits, self.k, bias=bias, token_mask=token_mask, stats=True,
+                    workspace=self.route_ws, out=self.routed, **self.how)
+
+    def loss(self):
+        return B.moe_balance_loss(self.counts, self.prob_sum, self.k, self.alpha, loss=self.balance)
+
+    def forward_ffn(self, x):
+        return self.ffn.forward(x, self.topk_ids, self.gate)
+
+    def backward_ffn(self, dout):
+        # gates of experts elsewhere get no gradient here, nor keep an earlier step's
+        self.ffn.dgate.zero_()
+        return self.ffn.backward(dout, self.gate)
+
+    def backward_route(self, logits, dloss=None):
+        return B.moe_route_bwd(logits, self.topk_ids, self.ffn.dgate, counts=self.counts,
+                               alpha=self.alpha, dloss=dloss, dlogits=self.dlogits, **self.how)
+
+    def grad_sumsq(self):
+        return B.moe_grad_sumsq(self.grads, sumsq=self.sumsq, workspace=self.grad_ws)
+
+    def clip(self, max_norm):
+        return B.moe_grad_clip(self.grads, self.sumsq, max_norm, norm=self.norm)
+
+    def step(self, x, w1, w2, logits, dout, max_norm, bias=None, token_mask=None, dloss=None):
+        """Forward and backward once: (out, balance loss, dx, dlogits, norm of
+        the expert gradients before clipping)."""
+        self.ffn.quantize_weights(w1, w2)
+        self.route(logits, bias, token_mask)
+        loss = self.loss()
+        out = self.forward_ffn(x)
+        dx = self.backward_ffn(dout)
+        dlogits = self.backward_route(logits, dloss)
+        self.grad_sumsq()
+        return out, loss, dx, dlogits, self.clip(max_norm)
 
 
 class NVFP4BackwardStep:
