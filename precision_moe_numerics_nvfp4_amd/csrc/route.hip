@@ -22,6 +22,7 @@ namespace nvfp4moe {
 namespace {
 
 constexpr int kWaves = 8;                  // wavefronts of a workgroup
+constexpr int kNarrowK = 16;               // slots of the forms with less than a wavefront per row
 constexpr float kNegInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ float load1(const void* p, bool bf16, int64_t i) {
@@ -445,6 +446,180 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
   }
 }
 
+// ---- one thread per row (few experts): the row in its registers, no traffic
+// between lanes but for the statistics.
+
+constexpr int kRowThreads = 256;
+
+// The row's E <= NE logits, -inf behind them. vec: rows are whole 16-byte pieces.
+template <bool BF, int NE>
+__device__ __forceinline__ void load_own_row(const void* logits, int64_t t, int E, bool vec,
+                                             float (&v)[NE]) {
+  const void* row = row_of<BF>(logits, t * E);
+  if (vec) {
+    const uint4* q = static_cast<const uint4*>(row);
+    constexpr int per = BF ? 8 : 4;
+#pragma unroll
+    for (int i = 0; i < NE / per; ++i) {
+      const uint4 u = q[i];
+      if constexpr (BF) {
+        v[8 * i + 0] = u2f(u.x << 16); v[8 * i + 1] = u2f(u.x & 0xFFFF0000u);
+        v[8 * i + 2] = u2f(u.y << 16); v[8 * i + 3] = u2f(u.y & 0xFFFF0000u);
+        v[8 * i + 4] = u2f(u.z << 16); v[8 * i + 5] = u2f(u.z & 0xFFFF0000u);
+        v[8 * i + 6] = u2f(u.w << 16); v[8 * i + 7] = u2f(u.w & 0xFFFF0000u);
+      } else {
+        v[4 * i + 0] = u2f(u.x); v[4 * i + 1] = u2f(u.y);
+        v[4 * i + 2] = u2f(u.z); v[4 * i + 3] = u2f(u.w);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < NE; ++e) v[e] = load1(row, BF, e < E ? e : E - 1);
+#pragma unroll
+    for (int e = 0; e < NE; ++e) v[e] = e < E ? v[e] : kNegInf;
+  }
+}
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+// One row per thread. The statistics' sums over rows are matrix products: the
+// wavefront's values for expert e are the 16 x 4 operand, the other one is 1 in
+// column e (mod 16), so that expert's sums land in that column of the
+// accumulator, which stays over all rows (four registers for 16 experts). The
+// matrix instruction reads every lane: lanes past the rows hold zeros.
+template <bool BF, bool SIG, bool BIAS, bool STATS, int NE>
+__global__ __launch_bounds__(kRowThreads) void k_route_rows(RouteArgs a, bool vec) {
+  constexpr int W = kRowThreads / 64, NA = (NE + 15) / 16;
+  __shared__ float chosen[kNarrowK][kRowThreads];   // the selected logits of each row
+  __shared__ float sh_prob[STATS ? W * NA * 16 : 1];
+  __shared__ int32_t sh_count[STATS ? NE + 1 : 1];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int E = a.E, k = a.k;
+  const bool renorm = a.renorm;
+  f32x4_t acc[STATS ? NA : 1];
+  float column[STATS ? 16 : 1];
+  if constexpr (STATS) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < 16; ++c) column[c] = (lane & 15) == c ? 1.0f : 0.0f;
+    for (int e = tid; e <= NE; e += kRowThreads) sh_count[e] = 0;
+    __syncthreads();
+  }
+  for (int64_t t0 = (int64_t)blockIdx.x * kRowThreads; t0 < a.T;
+       t0 += (int64_t)gridDim.x * kRowThreads) {
+    const int64_t t = t0 + tid;
+    const int64_t row = t < a.T ? t : a.T - 1;
+    const bool in = t < a.T;
+    float x[NE];
+    load_own_row<BF, NE>(a.logits, row, E, vec, x);
+    if (!in || (a.token_mask && a.token_mask[row] == 0)) {
+#pragma unroll
+      for (int e = 0; e < NE; ++e) x[e] = kNegInf;
+    }
+    float top = kNegInf;
+#pragma unroll
+    for (int e = 0; e < NE; ++e) top = fmaxf(top, x[e]);
+    const bool open = top > kNegInf;
+    top = open ? top : 0.0f;
+    const auto score = [&](float v) {
+      float s, ds;
+      if constexpr (SIG) sigmoid(v, s, ds);   // 0 for -inf
+      else s = exp_neg(v - top);
+      return s;
+    };
+    float total = 0.0f;
+    if (STATS || (!SIG && !renorm)) {
+#pragma unroll
+      for (int e = 0; e < NE; ++e) total += score(x[e]);
+    }
+    if constexpr (STATS) {
+      // the row counts where it selects: where an open expert's bias is above -inf
+      bool counts = open;
+      if constexpr (BIAS) {
+        counts = false;
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+          counts = counts || (x[e] > kNegInf && a.bias[e < E ? e : E - 1] > kNegInf);
+      }
+      const float r = counts && total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+#pragma unroll
+      for (int e = 0; e < NE; ++e)
+        acc[e / 16] = __builtin_amdgcn_mfma_f32_16x16x4f32(score(x[e]) * r, column[e % 16],
+                                                           acc[e / 16], 0, 0, 0);
+      if (counts) atomicAdd(&sh_count[NE], 1);
+    }
+    // k rounds of the largest remaining key, the lowest expert among equals
+    float sum = 0.0f;
+    double key[BIAS ? NE : 1];
+    if constexpr (BIAS) {
+#pragma unroll
+      for (int e = 0; e < NE; ++e)
+        key[e] = x[e] > kNegInf ? biased_key(x[e], a.bias[e < E ? e : E - 1]) : (double)kNegInf;
+    }
+    for (int j = 0; j < k; ++j) {
+      int at = -1;
+      float v = kNegInf;
+      if constexpr (BIAS) {
+        double best = (double)kNegInf;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) best = key[e] > best ? key[e] : best;
+        if (best > (double)kNegInf) {
+#pragma unroll
+          for (int e = NE - 1; e >= 0; --e) at = key[e] == best ? e : at;
+        }
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+          if (e == at) {
+            key[e] = (double)kNegInf;
+            v = x[e];
+          }
+      } else {
+#pragma unroll
+        for (int e = 0; e < NE; ++e) v = fmaxf(v, x[e]);
+        if (v > kNegInf) {
+#pragma unroll
+          for (int e = NE - 1; e >= 0; --e) at = x[e] == v ? e : at;
+        }
+#pragma unroll
+        for (int e = 0; e < NE; ++e) x[e] = e == at ? kNegInf : x[e];
+      }
+      chosen[j][tid] = v;
+      if (in) a.topk_ids[t * k + j] = at;
+      sum += score(v);                     // 0 in empty slots, whose logit is -inf
+      if constexpr (STATS) {
+        if (at >= 0) atomicAdd(&sh_count[at], 1);
+      }
+    }
+    const float den = renorm ? sum : SIG ? 1.0f : total;
+    const float r = den > 0.0f ? __builtin_amdgcn_rcpf(den) : 0.0f;
+    for (int j = 0; j < k; ++j) {
+      float g = score(chosen[j][tid]);
+      if (!SIG || renorm) g *= r;
+      if (in) a.gate[t * k + j] = g * a.scale;
+    }
+  }
+  if constexpr (STATS) {
+    // a lane's accumulator: four rows of column (lane mod 16)
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      float s = (acc[i][0] + acc[i][1]) + (acc[i][2] + acc[i][3]);
+      s += __shfl_xor(s, 16, 64);
+      s += __shfl_xor(s, 32, 64);
+      if (lane < 16) sh_prob[(w * NA + i) * 16 + lane] = s;
+    }
+    __syncthreads();
+    for (int e = tid; e <= E; e += kRowThreads) {
+      float s = 0.0f;
+      if (e < E) {
+#pragma unroll
+        for (int v = 0; v < W; ++v) s += sh_prob[v * NA * 16 + e];
+      }
+      a.parts[(int64_t)blockIdx.x * (E + 1) + e] = RoutePart{s, sh_count[e < E ? e : NE]};
+    }
+  }
+}
+
 // Column sums of the workgroups' partials, in a fixed order: 16 columns per
 // workgroup, 64 threads down each, eight loads of a thread in flight.
 __global__ __launch_bounds__(1024) void k_route_stats(const RoutePart* __restrict__ parts, int n,
@@ -658,8 +833,145 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
   }
 }
 
+template <bool BF, bool SIG, bool RENORM, bool BAL, int NE>
+__global__ __launch_bounds__(kRowThreads) void k_route_bwd_rows(RouteBwdArgs a, bool vec) {
+  const int E = a.E, k = a.k;
+  float coef[BAL ? NE : 1];
+  if constexpr (BAL) {
+    const double n = (double)a.counts[E];
+    const double c = n > 0.0 ? (double)a.alpha * E / (n * n * k) * (a.dloss ? (double)*a.dloss : 1.0)
+                             : 0.0;
+#pragma unroll
+    for (int e = 0; e < NE; ++e) coef[e] = e < E ? (float)(c * (double)a.counts[e]) : 0.0f;
+  }
+  for (int64_t t = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; t < a.T;
+       t += (int64_t)gridDim.x * kRowThreads) {
+    float x[NE], d[NE];
+    load_own_row<BF, NE>(a.logits, t, E, vec, x);
+#pragma unroll
+    for (int e = 0; e < NE; ++e) d[e] = 0.0f;
+    bool live = false;
+    float top = kNegInf, sum = 0.0f, dot = 0.0f;
+    if constexpr (!SIG) {
+#pragma unroll
+      for (int e = 0; e < NE; ++e) top = fmaxf(top, x[e]);
+      top = top > kNegInf ? top : 0.0f;
+    }
+    // the selected: first the renormalisation's sums, then each slot's part
+    const auto slot = [&](int j, int& id, float& u, float& q) {
+      id = a.topk_ids[t * k + j];
+      id = id >= 0 && id < E ? id : -1;
+      u = id >= 0 && a.dgate ? a.dgate[t * k + j] * a.scale : 0.0f;
+      if constexpr (RENORM) {
+        float v = kNegInf;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) v = e == id ? x[e] : v;
+        if constexpr (SIG) {
+          float ds;
+          sigmoid(v, q, ds);
+        } else {
+          q = exp_neg(v - top);
+        }
+      }
+    };
+    if constexpr (RENORM) {
+      for (int j = 0; j < k; ++j) {
+        int id;
+        float u, q;
+        slot(j, id, u, q);
+        sum += q;
+        dot += q * u;
+      }
+    }
+    const float r = RENORM && sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
+    for (int j = 0; j < k; ++j) {
+      int id;
+      float u, q;
+      slot(j, id, u, q);
+      if constexpr (RENORM) {
+        u = (u - dot * r) * r;
+        if constexpr (!SIG) u *= q;
+      }
+      live = live || id >= 0;
+#pragma unroll
+      for (int e = 0; e < NE; ++e) d[e] += e == id ? u : 0.0f;
+    }
+    // per expert
+    if constexpr (SIG) {
+      float s[BAL ? NE : 1], ds[NE], total = 0.0f, all = 0.0f;
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        float v;
+        sigmoid(x[e], v, ds[e]);
+        if constexpr (BAL) {
+          s[e] = v;
+          total += v;
+          all += v * coef[e];
+        }
+      }
+      if constexpr (BAL) {
+        const float rt = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) d[e] += (coef[e] - all * rt) * rt;
+      }
+#pragma unroll
+      for (int e = 0; e < NE; ++e) d[e] *= ds[e];
+    } else if constexpr (BAL || !RENORM) {
+      float total = 0.0f, all = 0.0f, p[NE];
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        p[e] = exp_neg(x[e] - top);
+        float v = RENORM ? 0.0f : d[e];
+        if constexpr (BAL) v += coef[e];
+        total += p[e];
+        all += p[e] * v;
+      }
+      const float rt = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        float v = RENORM ? 0.0f : d[e];
+        if constexpr (BAL) v += coef[e];
+        const float dp = p[e] * rt * (v - all * rt);
+        d[e] = RENORM ? d[e] + dp : dp;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < NE; ++e) d[e] = live ? d[e] : 0.0f;
+    if (vec) {
+      constexpr int per = BF ? 8 : 4;
+      uint4* q = static_cast<uint4*>(const_cast<void*>(row_of<BF>(a.dlogits, t * E)));
+#pragma unroll
+      for (int i = 0; i < NE / per; ++i) {
+        if constexpr (BF)
+          q[i] = make_uint4(pk_bf16(d[8 * i], d[8 * i + 1]), pk_bf16(d[8 * i + 2], d[8 * i + 3]),
+                            pk_bf16(d[8 * i + 4], d[8 * i + 5]), pk_bf16(d[8 * i + 6], d[8 * i + 7]));
+        else
+          q[i] = make_uint4(f2u(d[4 * i]), f2u(d[4 * i + 1]), f2u(d[4 * i + 2]), f2u(d[4 * i + 3]));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < NE; ++e)
+        if (e < E) {
+          if constexpr (BF) static_cast<uint16_t*>(a.dlogits)[t * E + e] = (uint16_t)pk_bf16(d[e], 0.0f);
+          else static_cast<float*>(a.dlogits)[t * E + e] = d[e];
+        }
+    }
+  }
+}
+
 // Whether rows go to groups of 16 lanes.
-bool narrow(int E, int k) { return E <= 64 && k <= 16; }
+bool narrow(int E, int k) { return E <= 64 && k <= kNarrowK; }
+
+// Whether rows go to single threads.
+bool single(int64_t T, int E, int k, bool biased, bool backward) {
+  if (k > kNarrowK || E > (biased || backward ? 8 : 64)) return false;
+  return T >= (biased || backward ? 32768 : 1024 * E);
+}
+
+bool whole_rows(const void* p, int E, bool bf16) {
+  return (E == 8 || E == 16 || E == 32 || E == 64) &&   // the row kernels' sizes
+         (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
 
 // Experts per lane, rounded up to a form that is built.
 int lanes_experts(int E) {
@@ -670,8 +982,8 @@ int lanes_experts(int E) {
 constexpr int kPerCu = 4;                  // workgroups that fill a compute unit
 
 // Workgroups of a launch over T rows.
-int64_t route_grid(int64_t T, int E, int k) {
-  const int64_t rows = narrow(E, k) ? kWaves * 4 : kWaves;
+int64_t route_grid(int64_t T, int E, int k, bool rows_form) {
+  const int64_t rows = rows_form ? kRowThreads : narrow(E, k) ? kWaves * 4 : kWaves;
   const int64_t need = (T + rows - 1) / rows;
   const int64_t most = (int64_t)device_cu_count() * kPerCu;
   return need < most ? need : most;
@@ -680,6 +992,20 @@ int64_t route_grid(int64_t T, int E, int k) {
 template <bool BF, bool SIG, bool BIAS, bool STATS>
 void route_nv(const RouteArgs& a, unsigned grid, hipStream_t s) {
 #define NVFP4MOE_ROUTE(L, NV) k_route<BF, SIG, BIAS, STATS, L, NV><<<grid, 64 * kWaves, 0, s>>>(a)
+  if (single(a.T, a.E, a.k, BIAS, false)) {
+#define NVFP4MOE_ROWS(NE) \
+  k_route_rows<BF, SIG, BIAS, STATS, NE><<<grid, kRowThreads, 0, s>>>(a, whole_rows(a.logits, a.E, BF))
+    if constexpr (BIAS) {
+      NVFP4MOE_ROWS(8);
+    } else {
+      if (a.E <= 8) NVFP4MOE_ROWS(8);
+      else if (a.E <= 16) NVFP4MOE_ROWS(16);
+      else if (a.E <= 32) NVFP4MOE_ROWS(32);
+      else NVFP4MOE_ROWS(64);
+    }
+#undef NVFP4MOE_ROWS
+    return;
+  }
   if (narrow(a.E, a.k)) {
     if (a.E <= 16) NVFP4MOE_ROUTE(16, 1);
     else if (a.E <= 32) NVFP4MOE_ROUTE(16, 2);
@@ -714,6 +1040,14 @@ void route_form(const RouteArgs& a, bool sigmoid, bool stats, unsigned grid, hip
 template <bool BF, bool SIG, bool RENORM, bool BAL>
 void bwd_nv(const RouteBwdArgs& a, unsigned grid, hipStream_t s) {
 #define NVFP4MOE_BWD(L, NV) k_route_bwd<BF, SIG, RENORM, BAL, L, NV><<<grid, 64 * kWaves, 0, s>>>(a)
+  if (single(a.T, a.E, a.k, false, true)) {
+    const bool vec = whole_rows(a.logits, a.E, BF) && whole_rows(a.dlogits, a.E, BF);
+#define NVFP4MOE_ROWS(NE) \
+  k_route_bwd_rows<BF, SIG, RENORM, BAL, NE><<<grid, kRowThreads, 0, s>>>(a, vec)
+    NVFP4MOE_ROWS(8);
+#undef NVFP4MOE_ROWS
+    return;
+  }
   if (narrow(a.E, a.k)) {
     if (a.E <= 16) NVFP4MOE_BWD(16, 1);
     else if (a.E <= 32) NVFP4MOE_BWD(16, 2);
@@ -755,7 +1089,7 @@ hipError_t launch_route(const void* logits, bool bf16, int64_t T, int E, int k, 
                         int32_t* topk_ids, float* gate, int64_t* counts, float* prob_sum,
                         void* workspace, hipStream_t stream) {
   const bool stats = counts != nullptr;
-  int64_t grid = route_grid(T, E, k);
+  int64_t grid = route_grid(T, E, k, single(T, E, k, bias != nullptr, false));
   if (stats && grid > kMaxRouteParts) grid = kMaxRouteParts;
   const RouteArgs a{logits, T, E, k, bias, token_mask, renorm, scale, topk_ids, gate,
                     static_cast<RoutePart*>(workspace)};
@@ -783,7 +1117,7 @@ hipError_t launch_route_bwd(const void* logits, bool bf16, int64_t T, int E, int
                             hipStream_t stream) {
   if (T == 0) return hipSuccess;
   const RouteBwdArgs a{logits, T, E, k, topk_ids, dgate, scale, counts, alpha, dloss, dlogits};
-  const unsigned g = (unsigned)route_grid(T, E, k);
+  const unsigned g = (unsigned)route_grid(T, E, k, single(T, E, k, false, true));
   if (bf16) {
     if (sigmoid) bwd_form<true, true>(a, renorm, g, stream);
     else bwd_form<true, false>(a, renorm, g, stream);

@@ -155,6 +155,51 @@ def test_moe_route_bwd(nv, T, E, k, score, renorm, dtype, balance, closed):
                bound + (2.0 ** -8 * np.abs(ref) if dtype == "bf16" else 0.0), "dlogits of the loss")
 
 
+LONG = [
+    # T, E, k, form, dtype: enough rows for one thread each, whole and odd row lengths
+    (9001, 8, 2, "softmax", "bf16"), (6000, 5, 3, "softmax-sum", "f32"), (17000, 16, 4, "sigmoid", "f32"),
+    (31000, 30, 16, "softmax-sum", "bf16"), (33000, 32, 5, "softmax", "f32"),
+    (66001, 64, 6, "sigmoid", "bf16"), (65536, 64, 2, "softmax-sum", "f32"),
+    (60000, 57, 3, "softmax", "f32"), (40000, 8, 8, "sigmoid-bias", "f32"),
+    (33001, 7, 2, "sigmoid-bias", "bf16"), (300000, 1, 1, "softmax", "f32"),
+    (70000, 20, 17, "softmax-sum", "f32"),
+]
+
+
+@pytest.mark.parametrize("T,E,k,form,dtype", LONG)
+@pytest.mark.parametrize("kind,closed", [("normal", 0.1), ("ties", 0.0)])
+def test_moe_route_long(nv, T, E, k, form, dtype, kind, closed):
+    """Many rows of few experts, both directions, with padding."""
+    x = _logits(T + E, T, E, dtype, kind, closed)
+    rng = np.random.default_rng(E)
+    score = form.split("-")[0]
+    renorm = form != "softmax"
+    bias = (0.2 * rng.normal(size=E)).astype(np.float32) if form == "sigmoid-bias" else None
+    mask = rng.random(T) < 0.7
+    xm = x.copy()
+    xm[~mask] = 0x7FC0 if dtype == "bf16" else np.nan            # padding holds anything
+    o = nv.moe_route(to_dev(xm), k, score=score, renorm=renorm, scale=2.5,
+                     bias=None if bias is None else to_dev(bias), token_mask=to_dev(mask), stats=True)
+    p = nv.moe_route(to_dev(xm), k, score=score, renorm=renorm, scale=2.5,
+                     bias=None if bias is None else to_dev(bias), token_mask=to_dev(mask))
+    r = R.route(x, k, score, renorm, 2.5, bias, mask)
+    rel = (6 * _spread(x, score) + E + 16) * U
+    for got in (o, p):
+        assert np.array_equal(from_dev(got["topk_ids"]), r["topk_ids"])
+        _close(from_dev(got["gate"]), r["gate"], rel * r["gate"], "gate")
+    assert np.array_equal(from_dev(o["counts"]), r["counts"])
+    _close(from_dev(o["prob_sum"]), r["prob_sum"], (rel + T * U) * r["prob_sum"], "prob_sum")
+    dg = rng.normal(size=(T, k)).astype(np.float32)
+    dg[r["topk_ids"] < 0] = np.nan
+    for with_loss in (True, False):
+        got = nv.moe_route_bwd(to_dev(xm), o["topk_ids"], to_dev(dg), score=score, renorm=renorm,
+                               scale=2.5, counts=o["counts"] if with_loss else None, alpha=T * 0.5)
+        ref, mag = R.route_bwd(x, r["topk_ids"], dg, score, renorm, 2.5,
+                               r["counts"] if with_loss else None, T * 0.5)
+        bound = 2 * rel * mag + (2.0 ** -8 * np.abs(ref) if dtype == "bf16" else 0.0)
+        _close(R._vals(from_dev(got)), ref, bound, "dlogits")
+
+
 def test_moe_route_bwd_foreign_indices(nv):
     """Indices outside [0, E) are empty slots; one expert twice counts twice."""
     T, E, k = 3, 40, 4
