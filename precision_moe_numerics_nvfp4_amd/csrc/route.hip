@@ -959,10 +959,21 @@ __global__ __launch_bounds__(kRowThreads) void k_route_bwd_rows(RouteBwdArgs a, 
   }
 }
 
-// Whether rows go to groups of 16 lanes.
-bool narrow(int E, int k) { return E <= 64 && k <= kNarrowK; }
+// Whether rows go to groups of 16 lanes. A round of the selection costs each of
+// four rows less than the wavefront's form costs one, up to some k; measured
+// against it at 131072 rows of 128 experts: top-2 18 against 45 us, top-8 44
+// against 51, top-16 82 against 62; backward 35 against 48 us, but 4.5 against
+// 3.2 us at 512 rows.
+bool narrow(int64_t T, int E, int k, bool biased, bool backward) {
+  if (k > kNarrowK || E > 128) return false;
+  return E <= 64 || (backward ? T >= 32768 : !biased && k <= 4);
+}
 
-// Whether rows go to single threads.
+// Whether rows go to single threads: rows enough to fill the device, few enough
+// experts for the registers. Against groups of 16 lanes, both at the bound and
+// at 262144 rows: 8 experts 2.4 against 2.7 us (at 4096) and 3.5 against 18.3,
+// 64 experts top-6 12 against 14 and 22 against 50; backward and biased, 8
+// experts, 4.2 against 4.6 and 9.0 against 17.
 bool single(int64_t T, int E, int k, bool biased, bool backward) {
   if (k > kNarrowK || E > (biased || backward ? 8 : 64)) return false;
   return T >= (biased || backward ? 32768 : 1024 * E);
@@ -982,8 +993,9 @@ int lanes_experts(int E) {
 constexpr int kPerCu = 4;                  // workgroups that fill a compute unit
 
 // Workgroups of a launch over T rows.
-int64_t route_grid(int64_t T, int E, int k, bool rows_form) {
-  const int64_t rows = rows_form ? kRowThreads : narrow(E, k) ? kWaves * 4 : kWaves;
+int64_t route_grid(int64_t T, int E, int k, bool biased, bool backward) {
+  const int64_t rows = single(T, E, k, biased, backward) ? kRowThreads
+                       : narrow(T, E, k, biased, backward) ? kWaves * 4 : kWaves;
   const int64_t need = (T + rows - 1) / rows;
   const int64_t most = (int64_t)device_cu_count() * kPerCu;
   return need < most ? need : most;
@@ -1006,10 +1018,11 @@ void route_nv(const RouteArgs& a, unsigned grid, hipStream_t s) {
 #undef NVFP4MOE_ROWS
     return;
   }
-  if (narrow(a.E, a.k)) {
+  if (narrow(a.T, a.E, a.k, BIAS, false)) {
     if (a.E <= 16) NVFP4MOE_ROUTE(16, 1);
     else if (a.E <= 32) NVFP4MOE_ROUTE(16, 2);
-    else NVFP4MOE_ROUTE(16, 4);
+    else if (BIAS || a.E <= 64) NVFP4MOE_ROUTE(16, 4);
+    else if constexpr (!BIAS) NVFP4MOE_ROUTE(16, 8);
     return;
   }
   switch (lanes_experts(a.E)) {
@@ -1048,10 +1061,11 @@ void bwd_nv(const RouteBwdArgs& a, unsigned grid, hipStream_t s) {
 #undef NVFP4MOE_ROWS
     return;
   }
-  if (narrow(a.E, a.k)) {
+  if (narrow(a.T, a.E, a.k, false, true)) {
     if (a.E <= 16) NVFP4MOE_BWD(16, 1);
     else if (a.E <= 32) NVFP4MOE_BWD(16, 2);
-    else NVFP4MOE_BWD(16, 4);
+    else if (a.E <= 64) NVFP4MOE_BWD(16, 4);
+    else NVFP4MOE_BWD(16, 8);
     return;
   }
   switch (lanes_experts(a.E)) {
@@ -1089,7 +1103,7 @@ hipError_t launch_route(const void* logits, bool bf16, int64_t T, int E, int k, 
                         int32_t* topk_ids, float* gate, int64_t* counts, float* prob_sum,
                         void* workspace, hipStream_t stream) {
   const bool stats = counts != nullptr;
-  int64_t grid = route_grid(T, E, k, single(T, E, k, bias != nullptr, false));
+  int64_t grid = route_grid(T, E, k, bias != nullptr, false);
   if (stats && grid > kMaxRouteParts) grid = kMaxRouteParts;
   const RouteArgs a{logits, T, E, k, bias, token_mask, renorm, scale, topk_ids, gate,
                     static_cast<RoutePart*>(workspace)};
@@ -1117,7 +1131,7 @@ hipError_t launch_route_bwd(const void* logits, bool bf16, int64_t T, int E, int
                             hipStream_t stream) {
   if (T == 0) return hipSuccess;
   const RouteBwdArgs a{logits, T, E, k, topk_ids, dgate, scale, counts, alpha, dloss, dlogits};
-  const unsigned g = (unsigned)route_grid(T, E, k, single(T, E, k, false, true));
+  const unsigned g = (unsigned)route_grid(T, E, k, false, true);
   if (bf16) {
     if (sigmoid) bwd_form<true, true>(a, renorm, g, stream);
     else bwd_form<true, false>(a, renorm, g, stream);
