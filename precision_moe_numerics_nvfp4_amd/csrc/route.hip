@@ -29,6 +29,15 @@ __device__ __forceinline__ float load1(const void* p, bool bf16, int64_t i) {
   return bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 
+// The element at a byte offset from a row's start (32 bits unsigned: the row's
+// address can stay in scalar registers).
+template <bool BF>
+__device__ __forceinline__ float load_at(const void* row, uint32_t byte) {
+  const char* p = static_cast<const char*>(row) + byte;
+  if constexpr (BF) return bf16_to_f32(*reinterpret_cast<const uint16_t*>(p));
+  else return *reinterpret_cast<const float*>(p);
+}
+
 template <bool BF>
 __device__ __forceinline__ const void* row_of(const void* p, int64_t i) {
   return static_cast<const char*>(p) + i * (BF ? 2 : 4);
@@ -126,22 +135,37 @@ __device__ __forceinline__ double biased_key(float x, float bias) {
   return 1.0 / (1.0 + exp(-(double)x)) + (double)bias;
 }
 
+// Keys of experts nearer than this in float32 are told apart in 64 bits: twice
+// the error of a float32 key (sigmoid 7 * 2^-24 of a value below 1, the sum
+// 2^-24 of the key) with room to spare.
+__device__ __forceinline__ float key_margin(float key) {
+  return 0x1p-19f + 0x1p-21f * fabsf(key);
+}
+
 // k rounds of taking the group's largest remaining key, the lowest expert
 // first among equals. Lane j of the group ends with the j-th expert (or -1)
-// in id and its logit in sx.
-template <int L, int NV, typename Key>
-__device__ __forceinline__ void select_rounds(Key (&key)[NV], const float (&x)[NV], int k, int l,
+// in id and its logit in sx. CHECK (float32 keys of a biased selection): one
+// round more, and whether two successive keys of any row were too near.
+template <int L, int NV, bool CHECK, typename Key>
+__device__ __forceinline__ bool select_rounds(Key (&key)[NV], const float (&x)[NV], int k, int l,
                                               int& id, float& sx) {
   const Key none = (Key)kNegInf;
   constexpr int far = 0x7FFFFFFF;
   id = -1;
   sx = kNegInf;
-  for (int j = 0; j < k; ++j) {
+  bool near = false;
+  Key before = none;
+  for (int j = 0; j < (CHECK ? k + 1 : k); ++j) {
     Key best = none;
 #pragma unroll
     for (int i = 0; i < NV; ++i) best = key[i] > best ? key[i] : best;
     best = group_max<L>(best);
     if (!__any(best > none)) break;        // no group of the wavefront has one left
+    if constexpr (CHECK) {
+      near = near || (j > 0 && best > none && before - best <= key_margin(before));
+      before = best;
+      if (j == k) break;
+    }
     int at = far;
 #pragma unroll
     for (int i = NV - 1; i >= 0; --i) at = key[i] == best ? i * L + l : at;
@@ -159,6 +183,7 @@ __device__ __forceinline__ void select_rounds(Key (&key)[NV], const float (&x)[N
       sx = v;
     }
   }
+  return CHECK && __any(near);
 }
 
 // float32 -> uint32 of the same order (-0 below +0), and back.
@@ -212,18 +237,16 @@ struct Candidate {
   int e;
 };
 
-// The k largest keys: lanes keep what reaches a value that at least k lanes
-// reach (a dozen candidates of 384 experts, compacted in expert order through
-// LDS, one per lane) and each candidate counts those ahead of it; its count is
-// its slot. Lane j ends with slot j's expert and logit. With a bias the first
-// cut is by float32 keys less a margin that covers their rounding, and the
-// order by 64-bit keys of the candidates alone. More than 64 candidates (rows
-// of equal logits, k near 64) go through select_rounds.
+// LDS of a wavefront's selection.
+template <bool BIAS>
+struct Candidates {
+  Candidate of[64];
+  float key[BIAS ? 64 : 1];
+};
+
+// The float32 keys of a lane's experts.
 template <bool BIAS, int NV>
-__device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g,
-                                       const float* bias, int k, int lane, Candidate* list,
-                                       int& id, float& sx) {
-  float key[NV], best = kNegInf;
+__device__ __forceinline__ void keys32(const float (&x)[NV], const float* bias, float (&key)[NV]) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     key[i] = x[i];
@@ -232,11 +255,38 @@ __device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g
       sigmoid(x[i], s, ds);
       key[i] = x[i] > kNegInf ? s + bias[i] : kNegInf;
     }
-    best = fmaxf(best, key[i]);
   }
+}
+
+// The 64-bit keys, one after the other: a rare path, few registers.
+template <int NV>
+__device__ __forceinline__ void keys64(const float (&x)[NV], const float* bias, double (&key)[NV]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    key[i] = x[i] > kNegInf ? biased_key(x[i], bias[i]) : (double)kNegInf;
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// The k largest keys of a row held by the wavefront: lanes keep what reaches a
+// value that at least k lanes reach (a dozen candidates of 384 experts,
+// compacted in expert order through LDS, one per lane) and each candidate
+// counts those ahead of it; its count is its slot. Lane j ends with slot j's
+// expert and logit. With a bias the cut and the order are by float32 keys, the
+// cut less a margin; where two of the first k + 1 are nearer than that margin
+// (a row in some hundreds) the candidates are ordered by 64-bit keys instead.
+// More than 64 candidates (rows of equal logits, k near 64) go through
+// select_rounds.
+template <bool BIAS, int NV>
+__device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g,
+                                       const float* bias, int k, int lane, Candidates<BIAS>& list,
+                                       int& id, float& sx) {
+  float key[NV], best = kNegInf;
+  keys32<BIAS, NV>(x, bias, key);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) best = fmaxf(best, key[i]);
   float cut = k_reached(best, k);
-  // |float32 key - key| <= 8 * 2^-24 + 2^-24 |key| (sigmoid and the sum): twice that is far inside
-  if constexpr (BIAS) cut = fmaxf(cut - (0x1p-19f + 0x1p-21f * fabsf(cut)), -3.402823466e38f);
+  if constexpr (BIAS) cut = fmaxf(cut - key_margin(cut), -3.402823466e38f);
   int n = 0;
   uint64_t hit[NV];
 #pragma unroll
@@ -249,14 +299,10 @@ __device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g
   if (n > 64) {
     if constexpr (BIAS) {
       double key64[NV];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {       // one after the other: a rare path, few registers
-        key64[i] = x[i] > kNegInf ? biased_key(x[i], bias[i]) : (double)kNegInf;
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      select_rounds<64, NV>(key64, x, k, lane, id, sx);
+      keys64<NV>(x, bias, key64);
+      select_rounds<64, NV, false>(key64, x, k, lane, id, sx);
     } else {
-      select_rounds<64, NV>(key, x, k, lane, id, sx);
+      select_rounds<64, NV, false>(key, x, k, lane, id, sx);
     }
     return;
   }
@@ -265,38 +311,50 @@ __device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g
   for (int i = 0; i < NV; ++i) {
     const int at = base + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(hit[i] >> 32),
                                                          __builtin_amdgcn_mbcnt_lo((uint32_t)hit[i], 0));
-    if (key[i] >= cut) list[at] = Candidate{x[i], i * 64 + lane};
+    if (key[i] >= cut) {
+      list.of[at] = Candidate{x[i], i * 64 + lane};
+      if constexpr (BIAS) list.key[at] = key[i];
+    }
     base += __popcll(hit[i]);
   }
   wave_lds_fence();
-  const Candidate c = lane < n ? list[lane] : Candidate{kNegInf, -1};
+  const Candidate c = lane < n ? list.of[lane] : Candidate{kNegInf, 0};
+  float mine32 = c.x;
+  if constexpr (BIAS) mine32 = lane < n ? list.key[lane] : kNegInf;
   wave_lds_fence();
+  // one unsigned comparison: the key, then the earlier place in the list
+  const uint32_t u = ordered(mine32 + 0.0f);
+  const uint64_t mine = ((uint64_t)u << 32) | (uint32_t)(63 - lane);
   int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const uint64_t other =
+        ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)u, j) << 32) | (uint32_t)(63 - j);
+    rank += other > mine;
+  }
   if constexpr (BIAS) {
-    const double mine = lane < n ? biased_key(c.x, bias_g[c.e]) : (double)kNegInf;
-    const uint64_t bits = __double_as_longlong(mine);
-    for (int j = 0; j < n; ++j) {
-      const uint64_t o = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(bits >> 32), j) << 32) |
-                         (uint32_t)__builtin_amdgcn_readlane((int)bits, j);
-      const double other = __longlong_as_double(o);
-      rank += other > mine || (other == mine && j < lane);
-    }
-  } else {
-    // one unsigned comparison: the logit, then the earlier place in the list
-    const uint32_t u = ordered(c.x + 0.0f);
-    const uint64_t mine = ((uint64_t)u << 32) | (uint32_t)(63 - lane);
-    for (int j = 0; j < n; ++j) {
-      const uint64_t other =
-          ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)u, j) << 32) | (uint32_t)(63 - j);
-      rank += other > mine;
+    if (lane < n) list.key[rank] = mine32;
+    wave_lds_fence();
+    const bool near = lane < k && lane + 1 < n &&
+                      list.key[lane] - list.key[lane + 1] <= key_margin(list.key[lane]);
+    wave_lds_fence();
+    if (__any(near)) {
+      const double key64 = lane < n ? biased_key(c.x, bias_g[c.e]) : (double)kNegInf;
+      const uint64_t bits = __double_as_longlong(key64);
+      rank = 0;
+      for (int j = 0; j < n; ++j) {
+        const double other = __longlong_as_double(
+            (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(bits >> 32), j) << 32) |
+                      (uint32_t)__builtin_amdgcn_readlane((int)bits, j)));
+        rank += other > key64 || (other == key64 && j < lane);
+      }
     }
   }
-  if (lane < n && rank < k) list[rank] = c;
+  if (lane < n && rank < k) list.of[rank] = c;
   wave_lds_fence();
   if (lane < k && lane < n) {
-    const Candidate mine = list[lane];
-    id = mine.e;
-    sx = mine.x;
+    const Candidate slot = list.of[lane];
+    id = slot.e;
+    sx = slot.x;
   }
   wave_lds_fence();
 }
@@ -320,12 +378,16 @@ struct RouteArgs {
   RoutePart* parts;      // [grid, E + 1], the last one's count the tokens
 };
 
+// Eight wavefronts a SIMD where the registers allow it (share of 32768 x 384
+// 17.1 us against 18.6 without the attribute; the biased form, with its 64-bit
+// path, 42 against 26).
 template <bool BF, bool SIG, bool BIAS, bool STATS, int L, int NV>
-__global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
+__global__ __launch_bounds__(64 * kWaves)
+__attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) void k_route(RouteArgs a) {
   constexpr int R = 64 / L;                // rows of a wavefront
   __shared__ float sh_prob[STATS ? kWaves * 64 * NV : 1];
   __shared__ int32_t sh_count[STATS ? NV * L + 1 : 1];
-  __shared__ Candidate list[L == 64 ? kWaves : 1][64];
+  __shared__ Candidates<BIAS> list[L == 64 ? kWaves : 1];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & (L - 1), g = L == 64 ? 0 : lane / L;
   const int E = a.E, k = a.k;
@@ -344,54 +406,71 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
   }
   // A row's logits, loaded one row ahead of their use. Every lane loads (past
   // the experts or the rows: the last one again), so that no branch waits.
-  int off[NV];
+  uint32_t off[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) off[i] = i * L + l < E ? i * L + l : E - 1;
-  const auto load = [&](int64_t t, float (&v)[NV], bool& on) {
+  for (int i = 0; i < NV; ++i) off[i] = (uint32_t)(i * L + l < E ? i * L + l : E - 1) * (BF ? 2 : 4);
+  // without a mask any byte is loaded (of the logits) and not looked at
+  const bool masked = a.token_mask != nullptr;
+  const uint8_t* mask_bytes = masked ? a.token_mask : static_cast<const uint8_t*>(a.logits);
+  const auto load = [&](int64_t t, float (&v)[NV], uint32_t& mask) {
     const int64_t row = t < a.T ? t : a.T - 1;
-    on = t < a.T && (a.token_mask == nullptr || a.token_mask[row] != 0);
+    mask = mask_bytes[row];
+    const void* p = row_of<BF>(a.logits, row * E);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = load1(row_of<BF>(a.logits, row * E), BF, off[i]);
+    for (int i = 0; i < NV; ++i) v[i] = load_at<BF>(p, off[i]);
   };
   const int64_t stride = (int64_t)gridDim.x * kWaves * R;
   int64_t t0 = ((int64_t)blockIdx.x * kWaves + w) * R;
   float next[NV];
-  bool next_on;
-  load(t0 + g, next, next_on);
+  uint32_t next_mask;
+  load(t0 + g, next, next_mask);
   for (; t0 < a.T; t0 += stride) {
     const int64_t t = t0 + g;
+    bool on = t < a.T && (!masked || next_mask != 0);
     float x[NV];
+    if constexpr (L == 64) {
+      on = !masked || __builtin_amdgcn_readfirstlane(next_mask) != 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) x[i] = next_on && i * L + l < E ? next[i] : kNegInf;
-    load(t + stride, next, next_on);
+      for (int i = 0; i < NV; ++i) x[i] = i * L + l < E ? next[i] : kNegInf;
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) x[i] = on && i * L + l < E ? next[i] : kNegInf;
+    }
+    load(t + stride, next, next_mask);
+    if (L == 64 && !on) {                    // padding: the wavefront has nothing to select
+      if (l < k) {
+        a.topk_ids[t * k + l] = -1;
+        a.gate[t * k + l] = 0.0f;
+      }
+      continue;
+    }
     int id;
     float sx;
     if constexpr (L == 64) {
       select<BIAS, NV>(x, a.bias, bias, k, lane, list[w], id, sx);
-    } else if constexpr (BIAS) {
-      double key[NV];
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        key[i] = x[i] > kNegInf ? biased_key(x[i], bias[i]) : (double)kNegInf;
-      select_rounds<L, NV>(key, x, k, l, id, sx);
     } else {
       float key[NV];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) key[i] = x[i];
-      select_rounds<L, NV>(key, x, k, l, id, sx);
+      keys32<BIAS, NV>(x, bias, key);
+      if (select_rounds<L, NV, BIAS>(key, x, k, l, id, sx)) {
+        if constexpr (BIAS) {
+          double key64[NV];
+          keys64<NV>(x, bias, key64);
+          select_rounds<L, NV, false>(key64, x, k, l, id, sx);
+        }
+      }
     }
     // the row has an expert: its first slot is taken
     const bool live = L == 64 ? __builtin_amdgcn_readfirstlane(id) >= 0 : group_max<L>((float)id) >= 0.0f;
+    // without a bias the first slot's logit is the row's largest
+    float first = 0.0f;
+    if constexpr (!SIG) {
+      first = L == 64 ? u2f(__builtin_amdgcn_readfirstlane(f2u(sx))) : group_max<L>(sx);
+      first = live ? first : 0.0f;
+    }
     // scores; the row's probabilities where they are needed
     float top = 0.0f, total = 0.0f, p[NV];
     if (STATS || (!SIG && !renorm)) {
-      if constexpr (!SIG) {
-        float m = kNegInf;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) m = fmaxf(m, x[i]);
-        m = group_max<L>(m);
-        top = live ? m : 0.0f;
-      }
+      if constexpr (!SIG) top = first;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if constexpr (SIG) {
@@ -417,13 +496,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
       float ds;
       sigmoid(sx, gate, ds);               // 0 in empty slots, whose logit is -inf
     } else if (renorm) {
-      const float m = group_max<L>(sx);
-      gate = exp_neg(sx - (live ? m : 0.0f));
+      gate = exp_neg(sx - first);
     } else {
       gate = total > 0.0f ? exp_neg(sx - top) * __builtin_amdgcn_rcpf(total) : 0.0f;
     }
     if (renorm) {
-      const float sum = group_sum<L>(gate);
+      // up to 16 slots lie in the first 16 lanes, whose sum is all that they need
+      const float sum = L == 64 && k <= 16 ? group_sum<16>(gate) : group_sum<L>(gate);
       gate = sum > 0.0f ? gate * __builtin_amdgcn_rcpf(sum) : 0.0f;
     }
     if (l < k && t < a.T) {
@@ -716,16 +795,17 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) sh[i * L + l] = 0.0f;
   // a row's operands, loaded one row ahead of their use (as in k_route)
-  int off[NV];
+  uint32_t off[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) off[i] = i * L + l < E ? i * L + l : E - 1;
+  for (int i = 0; i < NV; ++i) off[i] = (uint32_t)(i * L + l < E ? i * L + l : E - 1) * (BF ? 2 : 4);
   const int slot = l < k ? l : k - 1;
   const auto load = [&](int64_t t, float (&v)[NV], int& id, float& dg) {
     const int64_t row = t < a.T ? t : a.T - 1;
     id = a.topk_ids[row * k + slot];
     dg = a.dgate ? a.dgate[row * k + slot] : 0.0f;
+    const void* p = row_of<BF>(a.logits, row * E);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = load1(row_of<BF>(a.logits, row * E), BF, off[i]);
+    for (int i = 0; i < NV; ++i) v[i] = load_at<BF>(p, off[i]);
   };
   const int64_t stride = (int64_t)gridDim.x * kWaves * R;
   int64_t t0 = ((int64_t)blockIdx.x * kWaves + w) * R;
