@@ -533,7 +533,8 @@ NVFP4MOE_API size_t nvfp4moe_route_workspace_size(int64_t T, int E);
  * largest s_e + bias_e (computed in 64 bits), in descending order, the lower
  * index first among equals; slots past the last open expert hold -1.
  * gate [T, k] float32: scale * s_j, with renorm != 0 scale * s_j / (sum of the
- * selected s; gates 0 where that sum is 0); 0 in slots of -1.
+ * selected s); 0 in slots of -1. Scores below 2^-126 count as 0, and so do the
+ * gates of a row whose sum is 0.
  * counts [E + 1] int64, prob_sum [E] float32 (both or neither NULL):
  * counts[e] = selected pairs of expert e, counts[E] = tokens with at least one
  * expert; prob_sum[e] = sum over those tokens of s_te (SIGMOID: of

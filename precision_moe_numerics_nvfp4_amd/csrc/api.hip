@@ -451,7 +451,7 @@ int moe_route(const void* logits, int logits_dtype, int64_t T, int E, int k, int
   if (T > 0) REQUIRE(logits && topk_ids && gate, NVFP4MOE_EINVAL);
   if (counts && T > 0) REQUIRE(workspace != nullptr, NVFP4MOE_EINVAL);
   REQUIRE(E <= 1024 && k <= 64 && k <= E, NVFP4MOE_EUNSUPPORTED);
-  REQUIRE(T * (int64_t)k < (int64_t)1 << 31, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(T <= 0x7FFFFFFF / k, NVFP4MOE_EUNSUPPORTED);
   REQUIRE(!bias || score == NVFP4MOE_SCORE_SIGMOID, NVFP4MOE_EUNSUPPORTED);
   REQUIRE(aligned(logits, logits_dtype == NVFP4MOE_BF16 ? 2 : 4) && aligned(topk_ids, 4) &&
               aligned(gate, 4) && aligned(bias, 4) && aligned(counts, 8) && aligned(prob_sum, 4),
@@ -485,7 +485,7 @@ int moe_route_bwd(const void* logits, int logits_dtype, int64_t T, int E, int k,
   REQUIRE(score == NVFP4MOE_SCORE_SOFTMAX || score == NVFP4MOE_SCORE_SIGMOID, NVFP4MOE_EINVAL);
   if (T > 0) REQUIRE(logits && topk_ids && dlogits, NVFP4MOE_EINVAL);
   REQUIRE(E <= 1024 && k <= 64 && k <= E, NVFP4MOE_EUNSUPPORTED);
-  REQUIRE(T * (int64_t)k < (int64_t)1 << 31, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(T <= 0x7FFFFFFF / k, NVFP4MOE_EUNSUPPORTED);
   const uintptr_t size = logits_dtype == NVFP4MOE_BF16 ? 2 : 4;
   REQUIRE(aligned(logits, size) && aligned(dlogits, size) && aligned(topk_ids, 4) &&
               aligned(dgate, 4) && aligned(counts, 8) && aligned(dloss, 4),

@@ -204,6 +204,9 @@ __global__ __launch_bounds__(kThreads) void k_grad_join(const double* __restrict
   if (threadIdx.x == 0) *sumsq = s;
 }
 
+// Each workgroup goes through its run backwards: what the sum read last is still
+// in the 256 MB Infinity Cache (604M float32 elements: 1314 -> 1295 us for both
+// passes; non-temporal loads and stores, against plain ones, 1362 -> 1295).
 __global__ __launch_bounds__(kThreads) void k_grad_clip(ClipTable t, uint32_t per,
                                                         const double* __restrict__ sumsq,
                                                         float max_norm, float* __restrict__ norm) {
@@ -214,10 +217,10 @@ __global__ __launch_bounds__(kThreads) void k_grad_clip(ClipTable t, uint32_t pe
   if (t.n == 0) return;
   const uint32_t all = t.first[t.n];
   const uint32_t c0 = blockIdx.x * per, c1 = c0 + per < all ? c0 + per : all;
-  int j = table_find(t, c0);
-  for (uint32_t c = c0; c < c1; ++c) {
+  int j = table_find(t, c1 - 1);
+  for (uint32_t c = c1; c-- > c0;) {
+    while (t.first[j] > c) --j;
     const Chunk k = chunk(t, c, j);
-    j = k.j;
     if (coef == 1.0f && t.out[j] == t.in[j]) continue;        // in place and within the bound
     if (k.bf16)
       scale_run<true>(static_cast<const uint16_t*>(t.in[j]) + k.at,

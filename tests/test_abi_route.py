@@ -40,6 +40,7 @@ def test_route_refusals(L):
     assert _route(L, E=1025) == EUNSUP
     assert _route(L, E=100, k=65) == EUNSUP
     assert _route(L, T=1 << 30, k=2) == EUNSUP                   # T * k
+    assert _route(L, T=1 << 62, k=4) == EUNSUP                   # T * k past 64 bits
     assert _route(L, bias=FAKE) == EUNSUP                        # softmax has no bias
     assert _route(L, logits=ODD) == EUNSUP
     assert _route(L, ids=ODD) == EUNSUP
@@ -75,6 +76,7 @@ def test_route_bwd_refusals(L):
     assert f(k=9) == EUNSUP
     assert f(E=1025) == EUNSUP
     assert f(T=1 << 31, k=1) == EUNSUP
+    assert f(T=1 << 62, k=4) == EUNSUP
     assert f(dl=ctypes.c_void_p(0x10002)) == EUNSUP
     assert f(out=ODD) == EUNSUP
     assert f(logits=None, T=0, ids=None, out=None) == 0
