@@ -90,7 +90,7 @@ hipError_t launch_padded_offsets(const int64_t* offsets, int G, int64_t align, i
                                  hipStream_t stream);
 
 // route.hip
-constexpr int64_t kMaxRouteParts = 1024;   // workgroups that leave statistics partials
+constexpr int64_t kMaxRouteParts = 512;    // workgroups that leave statistics partials
 size_t route_workspace_bytes(int64_t T, int E);
 hipError_t launch_route(const void* logits, bool bf16, int64_t T, int E, int k, bool sigmoid,
                         bool renorm, float scale, const float* bias, const uint8_t* token_mask,

@@ -21,7 +21,8 @@ namespace nvfp4moe {
 
 namespace {
 
-constexpr int kWaves = 8;                  // wavefronts of a workgroup
+constexpr int kWaves = 8;                  // wavefronts of a backward workgroup
+constexpr int kMaxWaves = 16;              // of a forward one (4, 8 or 16: route_waves)
 constexpr int kNarrowK = 16;               // slots of the forms with less than a wavefront per row
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -382,15 +383,15 @@ struct RouteArgs {
 // 17.1 us against 18.6 without the attribute; the biased form, with its 64-bit
 // path, 42 against 26).
 template <bool BF, bool SIG, bool BIAS, bool STATS, int L, int NV>
-__global__ __launch_bounds__(64 * kWaves)
+__global__ __launch_bounds__(64 * kMaxWaves)
 __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) void k_route(RouteArgs a) {
   constexpr int R = 64 / L;                // rows of a wavefront
-  __shared__ float sh_prob[STATS ? kWaves * 64 * NV : 1];
+  __shared__ float sh_prob[STATS ? kMaxWaves * 64 * NV : 1];
   __shared__ int32_t sh_count[STATS ? NV * L + 1 : 1];
-  __shared__ Candidates<BIAS> list[L == 64 ? kWaves : 1];
+  __shared__ Candidates<BIAS> list[L == 64 ? kMaxWaves : 1];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & (L - 1), g = L == 64 ? 0 : lane / L;
-  const int E = a.E, k = a.k;
+  const int E = a.E, k = a.k, waves = blockDim.x >> 6;
   const bool renorm = a.renorm;
   float bias[BIAS ? NV : 1];
   if constexpr (BIAS) {
@@ -401,7 +402,7 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
   if constexpr (STATS) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) psum[i] = 0.0f;
-    for (int e = threadIdx.x; e <= E; e += 64 * kWaves) sh_count[e] = 0;
+    for (int e = threadIdx.x; e <= E; e += 64 * waves) sh_count[e] = 0;
     __syncthreads();
   }
   // A row's logits, loaded one row ahead of their use. Every lane loads (past
@@ -419,8 +420,8 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = load_at<BF>(p, off[i]);
   };
-  const int64_t stride = (int64_t)gridDim.x * kWaves * R;
-  int64_t t0 = ((int64_t)blockIdx.x * kWaves + w) * R;
+  const int64_t stride = (int64_t)gridDim.x * waves * R;
+  int64_t t0 = ((int64_t)blockIdx.x * waves + w) * R;
   float next[NV];
   uint32_t next_mask;
   load(t0 + g, next, next_mask);
@@ -514,11 +515,10 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
 #pragma unroll
     for (int i = 0; i < NV; ++i) sh_prob[(w * R + g) * NV * L + i * L + l] = psum[i];
     __syncthreads();
-    for (int e = threadIdx.x; e <= E; e += 64 * kWaves) {
+    for (int e = threadIdx.x; e <= E; e += 64 * waves) {
       float s = 0.0f;
       if (e < E) {
-#pragma unroll
-        for (int v = 0; v < kWaves * R; ++v) s += sh_prob[v * NV * L + e];
+        for (int v = 0; v < waves * R; ++v) s += sh_prob[v * NV * L + e];
       }
       a.parts[(int64_t)blockIdx.x * (E + 1) + e] = RoutePart{s, sh_count[e]};
     }
@@ -1070,23 +1070,39 @@ int lanes_experts(int E) {
   return nv <= 1 ? 1 : nv <= 2 ? 2 : nv <= 4 ? 4 : nv <= 6 ? 6 : nv <= 8 ? 8 : 16;
 }
 
-constexpr int kPerCu = 4;                  // workgroups that fill a compute unit
+// Wavefronts of a forward workgroup: few while the rows do not fill the device
+// (512 x 384 biased: 3.9 us with 4, 4.0 with 8, 4.7 with 16), many when they do,
+// for fewer statistics partials (32768 x 384: 31.4, 28.1, 26.5 us).
+int route_waves(int64_t T, int rows_per_wave) {
+  const int64_t need = (T + rows_per_wave - 1) / rows_per_wave;
+  return need <= 1024 ? 4 : need <= 2048 ? 8 : kMaxWaves;
+}
 
-// Workgroups of a launch over T rows.
-int64_t route_grid(int64_t T, int E, int k, bool biased, bool backward) {
-  const int64_t rows = single(T, E, k, biased, backward) ? kRowThreads
-                       : narrow(T, E, k, biased, backward) ? kWaves * 4 : kWaves;
+// Threads and workgroups of a launch over T rows: up to 32 wavefronts a compute unit.
+struct RouteShape {
+  unsigned grid, threads;
+};
+RouteShape route_shape(int64_t T, int E, int k, bool biased, bool backward) {
+  int waves, rows;
+  if (single(T, E, k, biased, backward)) {
+    waves = kRowThreads / 64;
+    rows = kRowThreads;
+  } else {
+    const int per_wave = narrow(T, E, k, biased, backward) ? 4 : 1;
+    waves = backward ? kWaves : route_waves(T, per_wave);
+    rows = waves * per_wave;
+  }
   const int64_t need = (T + rows - 1) / rows;
-  const int64_t most = (int64_t)device_cu_count() * kPerCu;
-  return need < most ? need : most;
+  const int64_t most = (int64_t)device_cu_count() * 32 / waves;
+  return RouteShape{(unsigned)(need < most ? need : most), 64u * waves};
 }
 
 template <bool BF, bool SIG, bool BIAS, bool STATS>
-void route_nv(const RouteArgs& a, unsigned grid, hipStream_t s) {
-#define NVFP4MOE_ROUTE(L, NV) k_route<BF, SIG, BIAS, STATS, L, NV><<<grid, 64 * kWaves, 0, s>>>(a)
+void route_nv(const RouteArgs& a, RouteShape at, hipStream_t s) {
+#define NVFP4MOE_ROUTE(L, NV) k_route<BF, SIG, BIAS, STATS, L, NV><<<at.grid, at.threads, 0, s>>>(a)
   if (single(a.T, a.E, a.k, BIAS, false)) {
 #define NVFP4MOE_ROWS(NE) \
-  k_route_rows<BF, SIG, BIAS, STATS, NE><<<grid, kRowThreads, 0, s>>>(a, whole_rows(a.logits, a.E, BF))
+  k_route_rows<BF, SIG, BIAS, STATS, NE><<<at.grid, at.threads, 0, s>>>(a, whole_rows(a.logits, a.E, BF))
     if constexpr (BIAS) {
       NVFP4MOE_ROWS(8);
     } else {
@@ -1117,26 +1133,26 @@ void route_nv(const RouteArgs& a, unsigned grid, hipStream_t s) {
 }
 
 template <bool BF>
-void route_form(const RouteArgs& a, bool sigmoid, bool stats, unsigned grid, hipStream_t s) {
+void route_form(const RouteArgs& a, bool sigmoid, bool stats, RouteShape at, hipStream_t s) {
   if (!sigmoid) {
-    if (stats) route_nv<BF, false, false, true>(a, grid, s);
-    else route_nv<BF, false, false, false>(a, grid, s);
+    if (stats) route_nv<BF, false, false, true>(a, at, s);
+    else route_nv<BF, false, false, false>(a, at, s);
   } else if (a.bias) {
-    if (stats) route_nv<BF, true, true, true>(a, grid, s);
-    else route_nv<BF, true, true, false>(a, grid, s);
+    if (stats) route_nv<BF, true, true, true>(a, at, s);
+    else route_nv<BF, true, true, false>(a, at, s);
   } else {
-    if (stats) route_nv<BF, true, false, true>(a, grid, s);
-    else route_nv<BF, true, false, false>(a, grid, s);
+    if (stats) route_nv<BF, true, false, true>(a, at, s);
+    else route_nv<BF, true, false, false>(a, at, s);
   }
 }
 
 template <bool BF, bool SIG, bool RENORM, bool BAL>
-void bwd_nv(const RouteBwdArgs& a, unsigned grid, hipStream_t s) {
-#define NVFP4MOE_BWD(L, NV) k_route_bwd<BF, SIG, RENORM, BAL, L, NV><<<grid, 64 * kWaves, 0, s>>>(a)
+void bwd_nv(const RouteBwdArgs& a, RouteShape at, hipStream_t s) {
+#define NVFP4MOE_BWD(L, NV) k_route_bwd<BF, SIG, RENORM, BAL, L, NV><<<at.grid, at.threads, 0, s>>>(a)
   if (single(a.T, a.E, a.k, false, true)) {
     const bool vec = whole_rows(a.logits, a.E, BF) && whole_rows(a.dlogits, a.E, BF);
 #define NVFP4MOE_ROWS(NE) \
-  k_route_bwd_rows<BF, SIG, RENORM, BAL, NE><<<grid, kRowThreads, 0, s>>>(a, vec)
+  k_route_bwd_rows<BF, SIG, RENORM, BAL, NE><<<at.grid, at.threads, 0, s>>>(a, vec)
     NVFP4MOE_ROWS(8);
 #undef NVFP4MOE_ROWS
     return;
@@ -1160,20 +1176,20 @@ void bwd_nv(const RouteBwdArgs& a, unsigned grid, hipStream_t s) {
 }
 
 template <bool BF, bool SIG>
-void bwd_form(const RouteBwdArgs& a, bool renorm, unsigned grid, hipStream_t s) {
+void bwd_form(const RouteBwdArgs& a, bool renorm, RouteShape at, hipStream_t s) {
   if (renorm) {
-    if (a.counts) bwd_nv<BF, SIG, true, true>(a, grid, s);
-    else bwd_nv<BF, SIG, true, false>(a, grid, s);
+    if (a.counts) bwd_nv<BF, SIG, true, true>(a, at, s);
+    else bwd_nv<BF, SIG, true, false>(a, at, s);
   } else {
-    if (a.counts) bwd_nv<BF, SIG, false, true>(a, grid, s);
-    else bwd_nv<BF, SIG, false, false>(a, grid, s);
+    if (a.counts) bwd_nv<BF, SIG, false, true>(a, at, s);
+    else bwd_nv<BF, SIG, false, false>(a, at, s);
   }
 }
 
 }  // namespace
 
 size_t route_workspace_bytes(int64_t T, int E) {
-  const int64_t need = (T + kWaves - 1) / kWaves;
+  const int64_t need = (T + 3) / 4;           // workgroups have at least 4 rows
   const int64_t parts = need < kMaxRouteParts ? need : kMaxRouteParts;
   return (size_t)(parts * ((int64_t)E + 1) * sizeof(RoutePart));
 }
@@ -1183,18 +1199,18 @@ hipError_t launch_route(const void* logits, bool bf16, int64_t T, int E, int k, 
                         int32_t* topk_ids, float* gate, int64_t* counts, float* prob_sum,
                         void* workspace, hipStream_t stream) {
   const bool stats = counts != nullptr;
-  int64_t grid = route_grid(T, E, k, bias != nullptr, false);
-  if (stats && grid > kMaxRouteParts) grid = kMaxRouteParts;
+  RouteShape at = route_shape(T, E, k, bias != nullptr, false);
+  if (stats && at.grid > kMaxRouteParts) at.grid = (unsigned)kMaxRouteParts;
   const RouteArgs a{logits, T, E, k, bias, token_mask, renorm, scale, topk_ids, gate,
                     static_cast<RoutePart*>(workspace)};
-  if (grid > 0) {
-    if (bf16) route_form<true>(a, sigmoid, stats, (unsigned)grid, stream);
-    else route_form<false>(a, sigmoid, stats, (unsigned)grid, stream);
+  if (T > 0) {
+    if (bf16) route_form<true>(a, sigmoid, stats, at, stream);
+    else route_form<false>(a, sigmoid, stats, at, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (stats)
-    k_route_stats<<<(unsigned)(E / 16 + 1), 1024, 0, stream>>>(a.parts, (int)grid, E, counts,
+    k_route_stats<<<(unsigned)(E / 16 + 1), 1024, 0, stream>>>(a.parts, (int)at.grid, E, counts,
                                                                prob_sum);
   return hipGetLastError();
 }
@@ -1211,13 +1227,13 @@ hipError_t launch_route_bwd(const void* logits, bool bf16, int64_t T, int E, int
                             hipStream_t stream) {
   if (T == 0) return hipSuccess;
   const RouteBwdArgs a{logits, T, E, k, topk_ids, dgate, scale, counts, alpha, dloss, dlogits};
-  const unsigned g = (unsigned)route_grid(T, E, k, false, true);
+  const RouteShape at = route_shape(T, E, k, false, true);
   if (bf16) {
-    if (sigmoid) bwd_form<true, true>(a, renorm, g, stream);
-    else bwd_form<true, false>(a, renorm, g, stream);
+    if (sigmoid) bwd_form<true, true>(a, renorm, at, stream);
+    else bwd_form<true, false>(a, renorm, at, stream);
   } else {
-    if (sigmoid) bwd_form<false, true>(a, renorm, g, stream);
-    else bwd_form<false, false>(a, renorm, g, stream);
+    if (sigmoid) bwd_form<false, true>(a, renorm, at, stream);
+    else bwd_form<false, false>(a, renorm, at, stream);
   }
   return hipGetLastError();
 }
