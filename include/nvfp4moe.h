@@ -514,7 +514,8 @@ NVFP4MOE_API int moe_bwd_wgrad_nvfp4(const uint8_t* dyT_codes, const uint8_t* dy
  * these calls need the alignment of their elements only (workspaces 16 bytes).
  * ------------------------------------------------------------------------- */
 
-/* Bytes of device workspace moe_route needs for its statistics (none without). */
+/* Bytes of device workspace moe_route needs for its statistics (0 for few rows;
+ * none is needed without statistics). */
 NVFP4MOE_API size_t nvfp4moe_route_workspace_size(int64_t T, int E);
 
 /*
@@ -540,7 +541,8 @@ NVFP4MOE_API size_t nvfp4moe_route_workspace_size(int64_t T, int E);
  * expert; prob_sum[e] = sum over those tokens of s_te (SIGMOID: of
  * s_te / sum_i s_ti). Both are overwritten, and the same inputs give the same
  * bits. Sums over ranks may replace them before the calls below.
- * workspace: nvfp4moe_route_workspace_size() bytes when counts is given.
+ * workspace: nvfp4moe_route_workspace_size() bytes when counts is given (NULL
+ * where that is 0).
  * Requires E <= 1024, k <= 64, k <= E, T * k < 2^31. T may be 0.
  */
 NVFP4MOE_API int moe_route(const void* logits, int logits_dtype, int64_t T, int E, int k, int score,

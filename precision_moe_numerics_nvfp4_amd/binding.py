@@ -703,7 +703,7 @@ def _workspace(t, need, dev):
     torch hands its memory to later work of the same stream only)."""
     torch = _torch()
     if t is None:
-        return torch.empty((need,), dtype=torch.uint8, device=dev), need
+        return (torch.empty((need,), dtype=torch.uint8, device=dev) if need else None), need
     _dev(t, "workspace", torch.uint8)
     if t.device != dev:
         raise ValueError(f"workspace must be on {dev} (got {t.device})")

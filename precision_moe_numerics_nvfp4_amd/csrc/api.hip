@@ -449,7 +449,6 @@ int moe_route(const void* logits, int logits_dtype, int64_t T, int E, int k, int
   REQUIRE(score == NVFP4MOE_SCORE_SOFTMAX || score == NVFP4MOE_SCORE_SIGMOID, NVFP4MOE_EINVAL);
   REQUIRE((counts == nullptr) == (prob_sum == nullptr), NVFP4MOE_EINVAL);
   if (T > 0) REQUIRE(logits && topk_ids && gate, NVFP4MOE_EINVAL);
-  if (counts && T > 0) REQUIRE(workspace != nullptr, NVFP4MOE_EINVAL);
   REQUIRE(E <= 1024 && k <= 64 && k <= E, NVFP4MOE_EUNSUPPORTED);
   REQUIRE(T <= 0x7FFFFFFF / k, NVFP4MOE_EUNSUPPORTED);
   REQUIRE(!bias || score == NVFP4MOE_SCORE_SIGMOID, NVFP4MOE_EUNSUPPORTED);
@@ -457,7 +456,9 @@ int moe_route(const void* logits, int logits_dtype, int64_t T, int E, int k, int
               aligned(gate, 4) && aligned(bias, 4) && aligned(counts, 8) && aligned(prob_sum, 4),
           NVFP4MOE_EUNSUPPORTED);
   if (counts && T > 0) {
-    REQUIRE(workspace_bytes >= route_workspace_bytes(T, E), NVFP4MOE_EWORKSPACE);
+    const size_t need = route_workspace_bytes(T, E);
+    REQUIRE(need == 0 || workspace != nullptr, NVFP4MOE_EINVAL);
+    REQUIRE(workspace_bytes >= need, NVFP4MOE_EWORKSPACE);
     REQUIRE(aligned16(workspace), NVFP4MOE_EUNSUPPORTED);
   }
   if (T == 0 && !counts) return NVFP4MOE_OK;

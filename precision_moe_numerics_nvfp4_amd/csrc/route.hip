@@ -377,7 +377,19 @@ struct RouteArgs {
   int32_t* topk_ids;
   float* gate;
   RoutePart* parts;      // [grid, E + 1], the last one's count the tokens
+  int64_t* counts;       // of a workgroup that is the only one: the sums themselves
+  float* prob_sum;
 };
+
+// A workgroup's statistics of expert e (e = E: its tokens) on their way out.
+__device__ __forceinline__ void leave_stats(const RouteArgs& a, int e, float prob, int32_t count) {
+  if (a.parts) {
+    a.parts[(int64_t)blockIdx.x * (a.E + 1) + e] = RoutePart{prob, count};
+  } else {
+    if (e < a.E) a.prob_sum[e] = prob;
+    a.counts[e] = count;
+  }
+}
 
 // Eight wavefronts a SIMD where the registers allow it (share of 32768 x 384
 // 17.1 us against 18.6 without the attribute; the biased form, with its 64-bit
@@ -520,7 +532,7 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
       if (e < E) {
         for (int v = 0; v < waves * R; ++v) s += sh_prob[v * NV * L + e];
       }
-      a.parts[(int64_t)blockIdx.x * (E + 1) + e] = RoutePart{s, sh_count[e]};
+      leave_stats(a, e, s, sh_count[e]);
     }
   }
 }
@@ -529,6 +541,8 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
 // between lanes but for the statistics.
 
 constexpr int kRowThreads = 256;
+// The largest workgroup: 16 wavefronts where one may have to take every row.
+constexpr int row_threads(int NE) { return NE <= 8 ? 1024 : kRowThreads; }
 
 // The row's E <= NE logits, -inf behind them. vec: rows are whole 16-byte pieces.
 template <bool BF, int NE>
@@ -567,13 +581,13 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 // accumulator, which stays over all rows (four registers for 16 experts). The
 // matrix instruction reads every lane: lanes past the rows hold zeros.
 template <bool BF, bool SIG, bool BIAS, bool STATS, int NE>
-__global__ __launch_bounds__(kRowThreads) void k_route_rows(RouteArgs a, bool vec) {
-  constexpr int W = kRowThreads / 64, NA = (NE + 15) / 16;
-  __shared__ float chosen[kNarrowK][kRowThreads];   // the selected logits of each row
-  __shared__ float sh_prob[STATS ? W * NA * 16 : 1];
+__global__ __launch_bounds__(row_threads(NE)) void k_route_rows(RouteArgs a, bool vec) {
+  constexpr int most = row_threads(NE), NA = (NE + 15) / 16, slots = NE < kNarrowK ? NE : kNarrowK;
+  __shared__ float chosen[slots][most];             // the selected logits of each row
+  __shared__ float sh_prob[STATS ? most / 64 * NA * 16 : 1];
   __shared__ int32_t sh_count[STATS ? NE + 1 : 1];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int E = a.E, k = a.k;
+  const int E = a.E, k = a.k, threads = blockDim.x;
   const bool renorm = a.renorm;
   f32x4_t acc[STATS ? NA : 1];
   float column[STATS ? 16 : 1];
@@ -582,11 +596,11 @@ __global__ __launch_bounds__(kRowThreads) void k_route_rows(RouteArgs a, bool ve
     for (int i = 0; i < NA; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < 16; ++c) column[c] = (lane & 15) == c ? 1.0f : 0.0f;
-    for (int e = tid; e <= NE; e += kRowThreads) sh_count[e] = 0;
+    for (int e = tid; e <= NE; e += threads) sh_count[e] = 0;
     __syncthreads();
   }
-  for (int64_t t0 = (int64_t)blockIdx.x * kRowThreads; t0 < a.T;
-       t0 += (int64_t)gridDim.x * kRowThreads) {
+  for (int64_t t0 = (int64_t)blockIdx.x * threads; t0 < a.T;
+       t0 += (int64_t)gridDim.x * threads) {
     const int64_t t = t0 + tid;
     const int64_t row = t < a.T ? t : a.T - 1;
     const bool in = t < a.T;
@@ -688,13 +702,12 @@ __global__ __launch_bounds__(kRowThreads) void k_route_rows(RouteArgs a, bool ve
       if (lane < 16) sh_prob[(w * NA + i) * 16 + lane] = s;
     }
     __syncthreads();
-    for (int e = tid; e <= E; e += kRowThreads) {
+    for (int e = tid; e <= E; e += threads) {
       float s = 0.0f;
       if (e < E) {
-#pragma unroll
-        for (int v = 0; v < W; ++v) s += sh_prob[v * NA * 16 + e];
+        for (int v = 0; v < threads / 64; ++v) s += sh_prob[v * NA * 16 + e];
       }
-      a.parts[(int64_t)blockIdx.x * (E + 1) + e] = RoutePart{s, sh_count[e < E ? e : NE]};
+      leave_stats(a, e, s, sh_count[e < E ? e : NE]);
     }
   }
 }
@@ -1078,29 +1091,65 @@ int route_waves(int64_t T, int rows_per_wave) {
   return need <= 1024 ? 4 : need <= 2048 ? 8 : kMaxWaves;
 }
 
-// Threads and workgroups of a launch over T rows: up to 32 wavefronts a compute unit.
-struct RouteShape {
+// How a launch takes its rows.
+enum RouteForm { kSingle, kNarrow, kWide };       // a thread, 16 lanes, a wavefront per row
+struct RoutePlan {
+  RouteForm form;
   unsigned grid, threads;
 };
-RouteShape route_shape(int64_t T, int E, int k, bool biased, bool backward) {
-  int waves, rows;
-  if (single(T, E, k, biased, backward)) {
-    waves = kRowThreads / 64;
+
+// Few enough rows for one workgroup, which then leaves the statistics
+// themselves: no partials and a launch fewer, of 3.3 us of the host's time
+// (with the loss, kernels alone: 1 x 384 8.8 -> 6.4 us, 512 x 8 7.1 -> 5.3).
+// More rounds of one workgroup lose: 128 x 64 would take 11.2 us for 8.5, 4096 x
+// 8 12.5 for 8.0.
+bool alone_any(int64_t T, int E) { return T <= kMaxWaves || (E <= 8 && T <= 1024); }
+
+RoutePlan route_plan(int64_t T, int E, int k, bool biased, bool stats) {
+  if (stats && E <= 8 && alone_any(T, E))
+    return RoutePlan{kSingle, 1, (unsigned)(T < 1024 ? (T + 63) / 64 * 64 : 1024)};
+  RoutePlan p{kWide, 0, 0};
+  int64_t rows = 0;
+  if (single(T, E, k, biased, false)) {
+    p.form = kSingle;
+    p.threads = kRowThreads;
     rows = kRowThreads;
   } else {
-    const int per_wave = narrow(T, E, k, biased, backward) ? 4 : 1;
-    waves = backward ? kWaves : route_waves(T, per_wave);
+    const int per_wave = narrow(T, E, k, biased, false) ? 4 : 1;
+    if (per_wave == 4) p.form = kNarrow;
+    const int waves = route_waves(T, per_wave);
+    if (stats && T <= kMaxWaves * per_wave)       // one round of one workgroup
+      return RoutePlan{p.form, 1, 64u * (unsigned)((T + per_wave - 1) / per_wave)};
+    p.threads = 64u * waves;
     rows = waves * per_wave;
   }
   const int64_t need = (T + rows - 1) / rows;
-  const int64_t most = (int64_t)device_cu_count() * 32 / waves;
-  return RouteShape{(unsigned)(need < most ? need : most), 64u * waves};
+  int64_t most = (int64_t)device_cu_count() * 2048 / p.threads;   // 32 wavefronts a compute unit
+  if (stats && most > kMaxRouteParts) most = kMaxRouteParts;
+  p.grid = (unsigned)(need < most ? need : most);
+  return p;
+}
+
+RoutePlan route_bwd_plan(int64_t T, int E, int k) {
+  RoutePlan p{kWide, 0, 64 * kWaves};
+  int64_t rows = kWaves;
+  if (single(T, E, k, false, true)) {
+    p = RoutePlan{kSingle, 0, kRowThreads};
+    rows = kRowThreads;
+  } else if (narrow(T, E, k, false, true)) {
+    p.form = kNarrow;
+    rows = 4 * kWaves;
+  }
+  const int64_t need = (T + rows - 1) / rows;
+  const int64_t most = (int64_t)device_cu_count() * 2048 / p.threads;
+  p.grid = (unsigned)(need < most ? need : most);
+  return p;
 }
 
 template <bool BF, bool SIG, bool BIAS, bool STATS>
-void route_nv(const RouteArgs& a, RouteShape at, hipStream_t s) {
+void route_nv(const RouteArgs& a, const RoutePlan& at, hipStream_t s) {
 #define NVFP4MOE_ROUTE(L, NV) k_route<BF, SIG, BIAS, STATS, L, NV><<<at.grid, at.threads, 0, s>>>(a)
-  if (single(a.T, a.E, a.k, BIAS, false)) {
+  if (at.form == kSingle) {
 #define NVFP4MOE_ROWS(NE) \
   k_route_rows<BF, SIG, BIAS, STATS, NE><<<at.grid, at.threads, 0, s>>>(a, whole_rows(a.logits, a.E, BF))
     if constexpr (BIAS) {
@@ -1114,7 +1163,7 @@ void route_nv(const RouteArgs& a, RouteShape at, hipStream_t s) {
 #undef NVFP4MOE_ROWS
     return;
   }
-  if (narrow(a.T, a.E, a.k, BIAS, false)) {
+  if (at.form == kNarrow) {
     if (a.E <= 16) NVFP4MOE_ROUTE(16, 1);
     else if (a.E <= 32) NVFP4MOE_ROUTE(16, 2);
     else if (BIAS || a.E <= 64) NVFP4MOE_ROUTE(16, 4);
@@ -1133,7 +1182,7 @@ void route_nv(const RouteArgs& a, RouteShape at, hipStream_t s) {
 }
 
 template <bool BF>
-void route_form(const RouteArgs& a, bool sigmoid, bool stats, RouteShape at, hipStream_t s) {
+void route_form(const RouteArgs& a, bool sigmoid, bool stats, const RoutePlan& at, hipStream_t s) {
   if (!sigmoid) {
     if (stats) route_nv<BF, false, false, true>(a, at, s);
     else route_nv<BF, false, false, false>(a, at, s);
@@ -1147,9 +1196,9 @@ void route_form(const RouteArgs& a, bool sigmoid, bool stats, RouteShape at, hip
 }
 
 template <bool BF, bool SIG, bool RENORM, bool BAL>
-void bwd_nv(const RouteBwdArgs& a, RouteShape at, hipStream_t s) {
+void bwd_nv(const RouteBwdArgs& a, const RoutePlan& at, hipStream_t s) {
 #define NVFP4MOE_BWD(L, NV) k_route_bwd<BF, SIG, RENORM, BAL, L, NV><<<at.grid, at.threads, 0, s>>>(a)
-  if (single(a.T, a.E, a.k, false, true)) {
+  if (at.form == kSingle) {
     const bool vec = whole_rows(a.logits, a.E, BF) && whole_rows(a.dlogits, a.E, BF);
 #define NVFP4MOE_ROWS(NE) \
   k_route_bwd_rows<BF, SIG, RENORM, BAL, NE><<<at.grid, at.threads, 0, s>>>(a, vec)
@@ -1157,7 +1206,7 @@ void bwd_nv(const RouteBwdArgs& a, RouteShape at, hipStream_t s) {
 #undef NVFP4MOE_ROWS
     return;
   }
-  if (narrow(a.T, a.E, a.k, false, true)) {
+  if (at.form == kNarrow) {
     if (a.E <= 16) NVFP4MOE_BWD(16, 1);
     else if (a.E <= 32) NVFP4MOE_BWD(16, 2);
     else if (a.E <= 64) NVFP4MOE_BWD(16, 4);
@@ -1176,7 +1225,7 @@ void bwd_nv(const RouteBwdArgs& a, RouteShape at, hipStream_t s) {
 }
 
 template <bool BF, bool SIG>
-void bwd_form(const RouteBwdArgs& a, bool renorm, RouteShape at, hipStream_t s) {
+void bwd_form(const RouteBwdArgs& a, bool renorm, const RoutePlan& at, hipStream_t s) {
   if (renorm) {
     if (a.counts) bwd_nv<BF, SIG, true, true>(a, at, s);
     else bwd_nv<BF, SIG, true, false>(a, at, s);
@@ -1189,7 +1238,8 @@ void bwd_form(const RouteBwdArgs& a, bool renorm, RouteShape at, hipStream_t s) 
 }  // namespace
 
 size_t route_workspace_bytes(int64_t T, int E) {
-  const int64_t need = (T + 3) / 4;           // workgroups have at least 4 rows
+  if (alone_any(T, E)) return 0;
+  const int64_t need = (T + 3) / 4;               // workgroups have at least 4 rows
   const int64_t parts = need < kMaxRouteParts ? need : kMaxRouteParts;
   return (size_t)(parts * ((int64_t)E + 1) * sizeof(RoutePart));
 }
@@ -1199,18 +1249,21 @@ hipError_t launch_route(const void* logits, bool bf16, int64_t T, int E, int k, 
                         int32_t* topk_ids, float* gate, int64_t* counts, float* prob_sum,
                         void* workspace, hipStream_t stream) {
   const bool stats = counts != nullptr;
-  RouteShape at = route_shape(T, E, k, bias != nullptr, false);
-  if (stats && at.grid > kMaxRouteParts) at.grid = (unsigned)kMaxRouteParts;
-  const RouteArgs a{logits, T, E, k, bias, token_mask, renorm, scale, topk_ids, gate,
-                    static_cast<RoutePart*>(workspace)};
+  RoutePart* parts = nullptr;
+  unsigned grid = 0;
   if (T > 0) {
+    const RoutePlan at = route_plan(T, E, k, bias != nullptr, stats);
+    grid = at.grid;
+    if (stats && grid > 1) parts = static_cast<RoutePart*>(workspace);
+    const RouteArgs a{logits, T, E, k, bias, token_mask, renorm, scale, topk_ids, gate, parts,
+                      counts, prob_sum};
     if (bf16) route_form<true>(a, sigmoid, stats, at, stream);
     else route_form<false>(a, sigmoid, stats, at, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (stats)
-    k_route_stats<<<(unsigned)(E / 16 + 1), 1024, 0, stream>>>(a.parts, (int)at.grid, E, counts,
+  if (stats && (parts || T == 0))
+    k_route_stats<<<(unsigned)(E / 16 + 1), 1024, 0, stream>>>(parts, (int)grid, E, counts,
                                                                prob_sum);
   return hipGetLastError();
 }
@@ -1227,7 +1280,7 @@ hipError_t launch_route_bwd(const void* logits, bool bf16, int64_t T, int E, int
                             hipStream_t stream) {
   if (T == 0) return hipSuccess;
   const RouteBwdArgs a{logits, T, E, k, topk_ids, dgate, scale, counts, alpha, dloss, dlogits};
-  const RouteShape at = route_shape(T, E, k, false, true);
+  const RoutePlan at = route_bwd_plan(T, E, k);
   if (bf16) {
     if (sigmoid) bwd_form<true, true>(a, renorm, at, stream);
     else bwd_form<true, false>(a, renorm, at, stream);

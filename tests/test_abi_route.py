@@ -44,10 +44,11 @@ def test_route_refusals(L):
     assert _route(L, bias=FAKE) == EUNSUP                        # softmax has no bias
     assert _route(L, logits=ODD) == EUNSUP
     assert _route(L, ids=ODD) == EUNSUP
-    assert _route(L, counts=FAKE, prob=FAKE) == EINVAL           # no workspace
-    need = L.nvfp4moe_route_workspace_size(64, 8)
+    assert _route(L, T=5000, counts=FAKE, prob=FAKE) == EINVAL   # no workspace
+    need = L.nvfp4moe_route_workspace_size(5000, 8)
     assert need > 0
-    assert _route(L, counts=FAKE, prob=FAKE, ws=FAKE, wsb=need - 1) == EWS
+    assert _route(L, T=5000, counts=FAKE, prob=FAKE, ws=FAKE, wsb=need - 1) == EWS
+    assert L.nvfp4moe_route_workspace_size(1, 384) == 0          # few rows need none
     assert _route(L, logits=None, T=0, ids=None, gate=None) == 0  # nothing to do
     assert L.nvfp4moe_route_workspace_size(-1, 8) == 0
     assert L.nvfp4moe_route_workspace_size(8, 0) == 0

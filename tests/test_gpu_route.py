@@ -155,6 +155,29 @@ def test_moe_route_bwd(nv, T, E, k, score, renorm, dtype, balance, closed):
                bound + (2.0 ** -8 * np.abs(ref) if dtype == "bf16" else 0.0), "dlogits of the loss")
 
 
+ALONE = [
+    # T, E, k on both sides of what one workgroup takes with its statistics
+    (16, 384, 8), (17, 384, 8), (15, 1024, 64), (33, 300, 9), (1024, 8, 8), (1025, 8, 2), (1000, 7, 3), (4097, 8, 2), (63, 3, 1),
+    (64, 64, 6), (65, 64, 6), (63, 33, 17), (64, 128, 4), (3, 5, 5), (2000, 1, 1),
+]
+
+
+@pytest.mark.parametrize("T,E,k", ALONE)
+@pytest.mark.parametrize("form", ["softmax", "sigmoid-bias"])
+def test_moe_route_few_rows(nv, T, E, k, form):
+    x = _logits(T, T, E, "f32", "normal", 0.2)
+    score = form.split("-")[0]
+    bias = (0.2 * np.random.default_rng(E).normal(size=E)).astype(np.float32) if score == "sigmoid" else None
+    o = nv.moe_route(to_dev(x), k, score=score, renorm=False, bias=None if bias is None else to_dev(bias),
+                     stats=True)
+    r = R.route(x, k, score, False, 1.0, bias)
+    assert np.array_equal(from_dev(o["topk_ids"]), r["topk_ids"])
+    assert np.array_equal(from_dev(o["counts"]), r["counts"])
+    rel = (6 * _spread(x, score) + E + 16) * U
+    _close(from_dev(o["gate"]), r["gate"], rel * r["gate"], "gate")
+    _close(from_dev(o["prob_sum"]), r["prob_sum"], (rel + T * U) * r["prob_sum"], "prob_sum")
+
+
 LONG = [
     # T, E, k, form, dtype: enough rows for one thread each, whole and odd row lengths
     (9001, 8, 2, "softmax", "bf16"), (6000, 5, 3, "softmax-sum", "f32"), (17000, 16, 4, "sigmoid", "f32"),
@@ -298,7 +321,8 @@ def test_moe_route_refuses(nv):
     with pytest.raises(nv.Nvfp4moeError):
         nv.moe_route(x, 17)
     with pytest.raises(nv.Nvfp4moeError):
-        nv.moe_route(x, 2, stats=True, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        nv.moe_route(x.repeat(1000, 1), 2, stats=True,
+                     workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     ids = torch.zeros((8, 2), dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError):
         nv.moe_route_bwd(x, ids, torch.zeros((8, 3), device="cuda"))
