@@ -365,3 +365,89 @@ def test_route_graphs_and_streams(nv):
         torch.cuda.synchronize()
         for o, r in zip(outs, ref):
             assert all(torch.equal(a, b) for a, b in zip(o, r))
+
+
+def test_route_past_32_bit_offsets(nv):
+    """More than 2^32 logits: rows at both ends against the oracle, equal rows
+    between (which go to the lowest experts) counted whole."""
+    import torch
+    T, E, k = 4_300_000, 1000, 2
+    tail = 70
+    x = torch.zeros((T, E), dtype=torch.bfloat16, device="cuda")
+    ends = _logits(11, 2 * tail, E, "bf16")
+    x[:tail], x[-tail:] = to_dev(ends[:tail]), to_dev(ends[tail:])
+    o = nv.moe_route(x, k, stats=True)
+    r = R.route(ends, k)
+    ids = o["topk_ids"]
+    assert np.array_equal(from_dev(torch.cat([ids[:tail], ids[-tail:]])), r["topk_ids"])
+    assert bool((ids[tail:-tail] == torch.arange(k, device="cuda", dtype=torch.int32)).all())
+    want = r["counts"].copy()
+    want[:k] += T - 2 * tail
+    want[E] = T
+    assert np.array_equal(from_dev(o["counts"]), want)
+    dg = torch.ones((T, k), device="cuda")
+    dg[:, 1] = -1.0
+    d = nv.moe_route_bwd(x, ids, dg, dlogits=x)                  # in place
+    ref, mag = R.route_bwd(ends, r["topk_ids"], np.tile([1.0, -1.0], (2 * tail, 1)))
+    got = R._vals(from_dev(torch.cat([d[:tail], d[-tail:]])))
+    _close(got, ref, 2 * (6 * _spread(ends, "softmax") + E + 16) * U * mag + 2.0 ** -8 * np.abs(ref), "ends")
+    assert bool((d[tail:-tail, 0] == 0.5).all()) and bool((d[tail:-tail, 1] == -0.5).all())
+    assert int(torch.count_nonzero(d[tail:-tail])) == 2 * (T - 2 * tail)
+
+
+def test_route_lowest_values_are_open(nv):
+    """The type's lowest value is a logit like any other: selected behind the
+    others, never in place of -inf; extreme spreads stay finite."""
+    lowest = np.finfo(np.float32).min
+    x = np.full((40, 70), lowest, np.float32)
+    x[1, 3] = 5
+    x[2, ::2] = -np.inf
+    x[3, 69] = np.finfo(np.float32).max
+    x[4] = np.linspace(-3e38, 3e38, 70, dtype=np.float32)
+    for k in (1, 8, 40):
+        for score in ("softmax", "sigmoid"):
+            o = nv.moe_route(to_dev(x), k, score=score, renorm=False, stats=True)
+            r = R.route(x, k, score, False)
+            assert np.array_equal(from_dev(o["topk_ids"]), r["topk_ids"])
+            assert np.array_equal(from_dev(o["counts"]), r["counts"])
+            assert np.allclose(from_dev(o["gate"]), r["gate"], rtol=1e-5, atol=1e-30)
+            d = from_dev(nv.moe_route_bwd(to_dev(x), o["topk_ids"], o["gate"], score=score,
+                                          renorm=False, counts=o["counts"], alpha=1.0))
+            assert np.isfinite(d).all()
+
+
+@pytest.mark.parametrize("E,k", [(12, 3), (100, 8), (384, 8)])
+def test_route_near_ties_under_a_bias(nv, E, k):
+    """Keys that float32 cannot tell apart: saturated scores, biases of one
+    float32 step, equal experts; infinite biases close or force an expert."""
+    T = 200
+    rng = np.random.default_rng(E)
+    x = (12 + 8 * rng.random((T, E))).astype(np.float32)         # sigmoid within 1e-5 of 1
+    x[::3] = np.round(x[::3])
+    bias = (1 + rng.integers(0, 4, size=E) * 2.0 ** -23).astype(np.float32)
+    bias[E - 1] = -np.inf
+    bias[E - 2] = np.inf
+    o = nv.moe_route(to_dev(x), k, score="sigmoid", bias=to_dev(bias))
+    ids = from_dev(o["topk_ids"])
+    assert np.array_equal(ids, R.select(R._vals(x), k, "sigmoid", bias))
+    assert (ids[:, 0] == E - 2).all() and not (ids == E - 1).any()
+    zero = np.zeros((T, E), np.float32)
+    same = nv.moe_route(to_dev(zero), k, score="sigmoid", bias=to_dev(np.zeros(E, np.float32)))
+    assert (from_dev(same["topk_ids"]) == np.arange(k)).all()
+
+
+def test_route_two_eager_streams(nv):
+    """Calls of two streams at once, each with its own workspace from torch."""
+    import torch
+    xs = [to_dev(_logits(30 + i, 20000, 130)) for i in range(2)]
+    ref = [nv.moe_route(x, 6, stats=True) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    outs = []
+    for _ in range(4):
+        for s, x in zip(streams, xs):
+            with torch.cuda.stream(s):
+                outs.append(nv.moe_route(x, 6, stats=True))
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert all(torch.equal(o[n], ref[i % 2][n]) for n in o)
