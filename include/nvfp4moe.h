@@ -576,8 +576,9 @@ NVFP4MOE_API int moe_route_bwd(const void* logits, int logits_dtype, int64_t T, 
                   const int64_t* counts, float alpha, const float* dloss, void* dlogits,
                   void* stream);
 
-/* Bytes of device workspace moe_grad_sumsq needs for a list of n tensors. */
-NVFP4MOE_API size_t nvfp4moe_grad_workspace_size(int n);
+/* Bytes of device workspace moe_grad_sumsq needs for a list of n tensors of
+ * these element counts (host array); 0 for short lists. */
+NVFP4MOE_API size_t nvfp4moe_grad_workspace_size(const int64_t* numels, int n);
 
 /*
  * Sum of the squares of every element of a list of gradients, in 64 bits.
@@ -587,6 +588,7 @@ NVFP4MOE_API size_t nvfp4moe_grad_workspace_size(int n);
  * NVFP4MOE_F32 or NVFP4MOE_BF16, element counts (0 allowed).
  * sumsq (device): the sum; 0 for an empty list. The same list gives the same
  * bits. Values of several devices may be added before moe_grad_clip.
+ * workspace: nvfp4moe_grad_workspace_size() bytes (NULL where that is 0).
  * Requires n <= 2^20 and at most 2^44 elements in all.
  */
 NVFP4MOE_API int moe_grad_sumsq(const void* const* grads, const int* dtypes, const int64_t* numels, int n,

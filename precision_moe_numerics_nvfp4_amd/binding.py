@@ -68,7 +68,7 @@ SIGNATURES = {
     "moe_balance_loss": ([_p, _p, _c_int, _c_int, _c_f32, _p, _p], _c_int),
     "moe_route_bwd": ([_p, _c_int, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_f32, _p, _p, _p,
                        _c_f32, _p, _p, _p], _c_int),
-    "nvfp4moe_grad_workspace_size": ([_c_int], _c_size),
+    "nvfp4moe_grad_workspace_size": ([_p, _c_int], _c_size),
     "moe_grad_sumsq": ([_p, _p, _p, _c_int, _p, _p, _c_size, _p], _c_int),
     "moe_grad_clip": ([_p, _p, _p, _p, _c_int, _p, _c_f32, _p, _p], _c_int),
 }
@@ -828,6 +828,7 @@ class GradList:
         self.device, self.spans, self.storages = dev, spans, storages
         self.starts, self.sizes, self.types = starts, sizes, codes
         self.ptrs, self.numels, self.codes = (_p * n)(*starts), (_c_i64 * n)(*sizes), (_c_int * n)(*codes)
+        self.workspace_size = int(lib().nvfp4moe_grad_workspace_size(self.numels, n))
 
     def __len__(self):
         return len(self.tensors)
@@ -857,9 +858,9 @@ def _overlap(a, b):
     return False
 
 
-@functools.lru_cache(maxsize=256)
-def grad_workspace_size(n):
-    return int(lib().nvfp4moe_grad_workspace_size(int(n)))
+def grad_workspace_size(grads):
+    """Bytes of workspace moe_grad_sumsq needs for a list (a GradList or tensors)."""
+    return _grad_list(grads).workspace_size
 
 
 def moe_grad_sumsq(grads, sumsq=None, workspace=None):
@@ -872,9 +873,10 @@ def moe_grad_sumsq(grads, sumsq=None, workspace=None):
             raise ValueError("an empty list needs sumsq (which device?)")
         dev = sumsq.device
     o = {"sumsq": sumsq}
-    ws, ws_bytes = _workspace(workspace, grad_workspace_size(len(g)), dev)
+    ws, ws_bytes = _workspace(workspace, g.workspace_size, dev)
     _launch(dev, "moe_grad_sumsq", g.ptrs, g.codes, g.numels, len(g),
-            _buf(o, "sumsq", torch.float64, (1,), dev), ws.data_ptr(), ws_bytes)
+            _buf(o, "sumsq", torch.float64, (1,), dev), None if ws is None else ws.data_ptr(),
+            ws_bytes)
     return o["sumsq"]
 
 

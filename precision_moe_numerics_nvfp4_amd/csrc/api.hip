@@ -28,12 +28,16 @@ inline hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
     if (!(cond)) return (code); \
   } while (0)
 
+// Bounds of a gradient list: its chunks are numbered in 32 bits.
+constexpr int kMaxGradTensors = 1 << 20;
+constexpr int64_t kMaxGradElems = (int64_t)1 << 44;
+
 // The list of tensors of the gradient calls: every entry of a known type, its
 // pointers aligned to that type, each output its own gradient or apart from it.
 int grad_list_status(const void* const* grads, void* const* outs, const int* dtypes,
                      const int64_t* numels, int n) {
   if (n > 0) REQUIRE(grads && dtypes && numels, NVFP4MOE_EINVAL);
-  REQUIRE(n <= 1 << 20, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(n <= kMaxGradTensors, NVFP4MOE_EUNSUPPORTED);
   int64_t total = 0;
   for (int i = 0; i < n; ++i) {
     REQUIRE(dtypes[i] == NVFP4MOE_F32 || dtypes[i] == NVFP4MOE_BF16, NVFP4MOE_EINVAL);
@@ -41,7 +45,7 @@ int grad_list_status(const void* const* grads, void* const* outs, const int* dty
     if (numels[i] == 0) continue;
     REQUIRE(grads[i] && (!outs || outs[i]), NVFP4MOE_EINVAL);
     const uintptr_t size = dtypes[i] == NVFP4MOE_F32 ? 4 : 2;
-    REQUIRE(numels[i] <= ((int64_t)1 << 44) - total, NVFP4MOE_EUNSUPPORTED);
+    REQUIRE(numels[i] <= kMaxGradElems - total, NVFP4MOE_EUNSUPPORTED);
     total += numels[i];
     const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]), bytes = size * (uintptr_t)numels[i];
     REQUIRE(g % size == 0, NVFP4MOE_EUNSUPPORTED);
@@ -497,14 +501,24 @@ int moe_route_bwd(const void* logits, int logits_dtype, int64_t T, int E, int k,
                                      as_stream(stream)));
 }
 
-size_t nvfp4moe_grad_workspace_size(int n) { return n < 0 ? 0 : grad_workspace_bytes(n); }
+size_t nvfp4moe_grad_workspace_size(const int64_t* numels, int n) {
+  if (n < 0 || n > kMaxGradTensors || (n > 0 && !numels)) return 0;
+  int64_t total = 0;
+  for (int i = 0; i < n; ++i) {
+    if (numels[i] < 0 || numels[i] > kMaxGradElems - total) return 0;
+    total += numels[i];
+  }
+  return grad_workspace_bytes(numels, n);
+}
 
 int moe_grad_sumsq(const void* const* grads, const int* dtypes, const int64_t* numels, int n,
                    double* sumsq, void* workspace, size_t workspace_bytes, void* stream) {
-  REQUIRE(n >= 0 && sumsq && workspace, NVFP4MOE_EINVAL);
+  REQUIRE(n >= 0 && sumsq, NVFP4MOE_EINVAL);
   const int bad = grad_list_status(grads, nullptr, dtypes, numels, n);
   if (bad != NVFP4MOE_OK) return bad;
-  REQUIRE(workspace_bytes >= grad_workspace_bytes(n), NVFP4MOE_EWORKSPACE);
+  const size_t need = grad_workspace_bytes(numels, n);
+  REQUIRE(need == 0 || workspace != nullptr, NVFP4MOE_EINVAL);
+  REQUIRE(workspace_bytes >= need, NVFP4MOE_EWORKSPACE);
   REQUIRE(aligned16(workspace) && aligned(sumsq, 8), NVFP4MOE_EUNSUPPORTED);
   return hip_status(launch_grad_sumsq(grads, dtypes, numels, n, sumsq, workspace,
                                       as_stream(stream)));

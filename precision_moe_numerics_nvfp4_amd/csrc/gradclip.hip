@@ -16,7 +16,8 @@ namespace nvfp4moe {
 
 namespace {
 
-constexpr int kSumTable = 280, kClipTable = 180;    // tensors per launch
+constexpr int kSumTable = 280, kClipTable = 180;    // tensors per launch, at most
+constexpr int kShortTable = 16;                     // of a short list: 0.4 KB of arguments, not 4
 constexpr int kThreads = 256;
 constexpr int kMaxParts = 2048;                     // workgroups, so partial sums, per launch
 constexpr int kAloneChunks = 8;                     // a list that one workgroup sums
@@ -178,10 +179,8 @@ __device__ __forceinline__ void scale_run(const void* base, void* out, int len, 
   if (tid < len - tail) put(tail + tid);
 }
 
-using SumTable = GradTable<kSumTable, false>;
-using ClipTable = GradTable<kClipTable, true>;
-
-__global__ __launch_bounds__(kThreads) void k_grad_sumsq(SumTable t, uint32_t per,
+template <int N>
+__global__ __launch_bounds__(kThreads) void k_grad_sumsq(GradTable<N, false> t, uint32_t per,
                                                          double* __restrict__ parts) {
   const uint32_t all = t.first[t.n];
   const uint32_t c0 = blockIdx.x * per, c1 = c0 + per < all ? c0 + per : all;
@@ -208,7 +207,8 @@ __global__ __launch_bounds__(kThreads) void k_grad_join(const double* __restrict
 // Each workgroup goes through its run backwards: what the sum read last is still
 // in the 256 MB Infinity Cache (604M float32 elements: 1314 -> 1295 us for both
 // passes; non-temporal loads and stores, against plain ones, 1362 -> 1295).
-__global__ __launch_bounds__(kThreads) void k_grad_clip(ClipTable t, uint32_t per,
+template <int N>
+__global__ __launch_bounds__(kThreads) void k_grad_clip(GradTable<N, true> t, uint32_t per,
                                                         const double* __restrict__ sumsq,
                                                         float max_norm, float* __restrict__ norm) {
   const double root = sqrt(*sumsq);
@@ -267,36 +267,32 @@ int fill_table(GradTable<N, OUT>& t, int shift, int at, const void* const* grads
 
 uint32_t per_workgroup(uint32_t chunks) { return (chunks + kMaxParts - 1) / kMaxParts; }
 
-}  // namespace
-
-size_t grad_workspace_bytes(int n) {
-  return (size_t)(n / kSumTable + 1) * kMaxParts * sizeof(double);
+int64_t chunks_of(const int64_t* numels, int n, int shift) {
+  int64_t all = 0;
+  for (int i = 0; i < n; ++i) all += (numels[i] + ((int64_t)1 << shift) - 1) >> shift;
+  return all;
 }
 
-hipError_t launch_grad_sumsq(const void* const* grads, const int* dtypes, const int64_t* numels,
-                             int n, double* sumsq, void* workspace, hipStream_t stream) {
-  const int shift = chunk_shift(numels, n);
-  // A list of a few chunks: one workgroup leaves the sum itself (a launch fewer,
-  // 3.3 us of the host's time).
-  int64_t all = 0;
-  for (int i = 0; i < n && all <= kAloneChunks; ++i)
-    all += (numels[i] + ((int64_t)1 << shift) - 1) >> shift;
-  if (n > 0 && n <= kSumTable && all > 0 && all <= kAloneChunks) {
-    SumTable t;
-    fill_table(t, shift, 0, grads, nullptr, dtypes, numels, n);
-    k_grad_sumsq<<<1, kThreads, 0, stream>>>(t, t.first[t.n], sumsq);
-    return hipGetLastError();
-  }
-  double* parts = static_cast<double*>(workspace);
+// A list of a few chunks: one workgroup leaves the sum itself (no partials, and
+// a launch fewer of 3.3 us of the host's time).
+bool alone(int64_t chunks, int n) { return chunks > 0 && chunks <= kAloneChunks && n <= kShortTable; }
+
+template <int N>
+hipError_t sumsq_launches(const void* const* grads, const int* dtypes, const int64_t* numels, int n,
+                          int shift, double* sumsq, double* parts, hipStream_t stream) {
   int used = 0;
   for (int at = 0; at < n;) {
-    SumTable t;
+    GradTable<N, false> t;
     at = fill_table(t, shift, at, grads, nullptr, dtypes, numels, n);
     if (t.n == 0) break;
     const uint32_t chunks = t.first[t.n];
+    if (!parts) {
+      k_grad_sumsq<N><<<1, kThreads, 0, stream>>>(t, chunks, sumsq);
+      return hipGetLastError();
+    }
     const uint32_t per = per_workgroup(chunks);
     const unsigned grid = (chunks + per - 1) / per;
-    k_grad_sumsq<<<grid, kThreads, 0, stream>>>(t, per, parts + used);
+    k_grad_sumsq<N><<<grid, kThreads, 0, stream>>>(t, per, parts + used);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     used += (int)grid;
@@ -305,24 +301,53 @@ hipError_t launch_grad_sumsq(const void* const* grads, const int* dtypes, const 
   return hipGetLastError();
 }
 
-hipError_t launch_grad_clip(const void* const* grads, void* const* outs, const int* dtypes,
-                            const int64_t* numels, int n, const double* sumsq, float max_norm,
-                            float* norm, hipStream_t stream) {
-  const int shift = chunk_shift(numels, n);
+template <int N>
+hipError_t clip_launches(const void* const* grads, void* const* outs, const int* dtypes,
+                         const int64_t* numels, int n, int shift, const double* sumsq,
+                         float max_norm, float* norm, hipStream_t stream) {
   int at = 0;
   do {
-    ClipTable t;
+    GradTable<N, true> t;
     at = fill_table(t, shift, at, grads, outs, dtypes, numels, n);
     if (t.n == 0 && norm == nullptr) break;
     const uint32_t chunks = t.first[t.n];
     const uint32_t per = chunks ? per_workgroup(chunks) : 1;
     const unsigned grid = chunks ? (chunks + per - 1) / per : 1;
-    k_grad_clip<<<grid, kThreads, 0, stream>>>(t, per, sumsq, max_norm, norm);
+    k_grad_clip<N><<<grid, kThreads, 0, stream>>>(t, per, sumsq, max_norm, norm);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     norm = nullptr;                       // the first launch writes it
   } while (at < n);
   return hipSuccess;
+}
+
+}  // namespace
+
+size_t grad_workspace_bytes(const int64_t* numels, int n) {
+  const int64_t chunks = chunks_of(numels, n, chunk_shift(numels, n));
+  if (alone(chunks, n)) return 0;
+  const int64_t most = (int64_t)(n / kSumTable + 1) * kMaxParts;
+  return (size_t)((chunks < most ? chunks : most) + 1) * sizeof(double);
+}
+
+hipError_t launch_grad_sumsq(const void* const* grads, const int* dtypes, const int64_t* numels,
+                             int n, double* sumsq, void* workspace, hipStream_t stream) {
+  const int shift = chunk_shift(numels, n);
+  double* parts = alone(chunks_of(numels, n, shift), n) ? nullptr : static_cast<double*>(workspace);
+  if (n <= kShortTable)
+    return sumsq_launches<kShortTable>(grads, dtypes, numels, n, shift, sumsq, parts, stream);
+  return sumsq_launches<kSumTable>(grads, dtypes, numels, n, shift, sumsq, parts, stream);
+}
+
+hipError_t launch_grad_clip(const void* const* grads, void* const* outs, const int* dtypes,
+                            const int64_t* numels, int n, const double* sumsq, float max_norm,
+                            float* norm, hipStream_t stream) {
+  const int shift = chunk_shift(numels, n);
+  if (n <= kShortTable)
+    return clip_launches<kShortTable>(grads, outs, dtypes, numels, n, shift, sumsq, max_norm, norm,
+                                      stream);
+  return clip_launches<kClipTable>(grads, outs, dtypes, numels, n, shift, sumsq, max_norm, norm,
+                                   stream);
 }
 
 }  // namespace nvfp4moe

@@ -104,7 +104,7 @@ hipError_t launch_route_bwd(const void* logits, bool bf16, int64_t T, int E, int
                             hipStream_t stream);
 
 // gradclip.hip
-size_t grad_workspace_bytes(int n);
+size_t grad_workspace_bytes(const int64_t* numels, int n);
 hipError_t launch_grad_sumsq(const void* const* grads, const int* dtypes, const int64_t* numels,
                              int n, double* sumsq, void* workspace, hipStream_t stream);
 hipError_t launch_grad_clip(const void* const* grads, void* const* outs, const int* dtypes,

@@ -234,7 +234,7 @@ class RoutedFFNStep:
         self.route_ws = e(B.route_workspace_size(T, n), dt=torch.uint8)
         self.grads = B.GradList([self.ffn.dw1, self.ffn.dw2])
         self.sumsq, self.norm = e(1, dt=torch.float64), e(1)
-        self.grad_ws = e(B.grad_workspace_size(len(self.grads)), dt=torch.uint8)
+        self.grad_ws = e(B.grad_workspace_size(self.grads), dt=torch.uint8)
 
     def route(self, logits, bias=None, token_mask=None):
         B.moe_route(logits, self.k, bias=bias, token_mask=token_mask, stats=True,

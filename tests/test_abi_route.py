@@ -89,14 +89,19 @@ def _list(ptrs, types, sizes):
 
 
 def test_gradient_list_refusals(L):
-    need = L.nvfp4moe_grad_workspace_size(1)
-    assert L.nvfp4moe_grad_workspace_size(-1) == 0
+    size = lambda sizes, n=None: L.nvfp4moe_grad_workspace_size(
+        (ctypes.c_int64 * len(sizes))(*sizes), len(sizes) if n is None else n)
+    need = size([1 << 20])
+    assert need > 0 and size([4]) == 0                            # a short list needs none
+    assert size([4], -1) == 0 and size([-4]) == 0
+    assert L.nvfp4moe_grad_workspace_size(None, 1) == 0
+    assert size([1 << 40] * 2) < 1 << 16 and size([1 << 62] * 4) == 0
 
     def s(ptrs, types, sizes, out=FAKE, ws=FAKE, wsb=1 << 30, n=None):
         p, t, m, k = _list(ptrs, types, sizes)
         return L.moe_grad_sumsq(p, t, m, k if n is None else n, out, ws, wsb, None)
     assert s([0x10000], [0], [4], out=None) == EINVAL
-    assert s([0x10000], [0], [4], ws=None) == EINVAL
+    assert s([0x10000], [0], [1 << 20], ws=None) == EINVAL
     assert s([0x10000], [0], [4], n=-1) == EINVAL
     assert s([0x10000], [2], [4]) == EINVAL
     assert s([0x10000], [0], [-4]) == EINVAL
@@ -105,7 +110,7 @@ def test_gradient_list_refusals(L):
     assert s([0x10001], [1], [4]) == EUNSUP
     assert s([0x10000], [0], [(1 << 44) + 1]) == EUNSUP
     assert s([0x10000, 0x10000], [0, 0], [1 << 43, (1 << 43) + 1]) == EUNSUP
-    assert s([0x10000], [0], [4], wsb=need - 1) == EWS
+    assert s([0x10000], [0], [1 << 20], wsb=need - 1) == EWS
     assert L.moe_grad_sumsq(None, None, None, 1, FAKE, FAKE, 1 << 30, None) == EINVAL
 
     def c(ptrs, outs, sizes, sumsq=FAKE, max_norm=1.0, norm=FAKE):

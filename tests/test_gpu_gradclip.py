@@ -42,7 +42,8 @@ def _check(got, ref, bits, what):
 
 
 LISTS = [
-    [1], [0, 3, 0], [4096, 17], [16384], [16385, 1, 16383], [100000, 7, 65536, 3],
+    [1], [0, 3, 0], [4096, 17], [16384], [16385], [2048] * 8, [2048] * 8 + [1], [100] * 16, [100] * 17,
+    [16385, 1, 16383], [100000, 7, 65536, 3],
     [3] * 95, [3] * 96, [5, 0] * 97, [1000 + 37 * i for i in range(200)], [3000001],
 ]
 
@@ -181,7 +182,8 @@ def test_refusals(nv):
     with pytest.raises(nv.Nvfp4moeError):
         nv.moe_grad_clip([a], s, -1.0)
     with pytest.raises(nv.Nvfp4moeError):
-        nv.moe_grad_sumsq([a], workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        nv.moe_grad_sumsq([torch.ones(1 << 20, device="cuda")],
+                          workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
 
 
 def test_graph_replays(nv):
