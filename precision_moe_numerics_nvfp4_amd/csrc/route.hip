@@ -30,13 +30,24 @@ __device__ __forceinline__ float load1(const void* p, bool bf16, int64_t i) {
   return bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 
-// The element at a byte offset from a row's start (32 bits unsigned: the row's
-// address can stay in scalar registers).
+// The element at a byte offset from a row's start. The offset is kept opaque in
+// 32 bits: the row's address stays in scalar registers and the load adds them,
+// where a 64-bit sum per load would take a vector instruction.
+template <class T>
+__device__ __forceinline__ T read_at(const void* row, uint32_t byte) {
+  asm volatile("" : "+v"(byte));
+  return *reinterpret_cast<const T*>(static_cast<const char*>(row) + byte);
+}
 template <bool BF>
 __device__ __forceinline__ float load_at(const void* row, uint32_t byte) {
-  const char* p = static_cast<const char*>(row) + byte;
-  if constexpr (BF) return bf16_to_f32(*reinterpret_cast<const uint16_t*>(p));
-  else return *reinterpret_cast<const float*>(p);
+  if constexpr (BF) return bf16_to_f32(read_at<uint16_t>(row, byte));
+  else return read_at<float>(row, byte);
+}
+template <class T>
+__device__ __forceinline__ void store_at(T* row, uint32_t i, T v) {
+  uint32_t byte = i * (uint32_t)sizeof(T);
+  asm volatile("" : "+v"(byte));
+  *reinterpret_cast<T*>(reinterpret_cast<char*>(row) + byte) = v;
 }
 
 template <bool BF>
@@ -405,6 +416,7 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
   const int l = lane & (L - 1), g = L == 64 ? 0 : lane / L;
   const int E = a.E, k = a.k, waves = blockDim.x >> 6;
   const bool renorm = a.renorm;
+  const uint32_t T = (uint32_t)a.T;         // rows: below 2^31, like T k
   float bias[BIAS ? NV : 1];
   if constexpr (BIAS) {
 #pragma unroll
@@ -425,26 +437,30 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
   // without a mask any byte is loaded (of the logits) and not looked at
   const bool masked = a.token_mask != nullptr;
   const uint8_t* mask_bytes = masked ? a.token_mask : static_cast<const uint8_t*>(a.logits);
-  const auto load = [&](int64_t t, float (&v)[NV], uint32_t& mask) {
-    const int64_t row = t < a.T ? t : a.T - 1;
+  const auto load = [&](uint32_t t, float (&v)[NV], uint32_t& mask) {
+    const uint32_t row = t < T ? t : T - 1;
     mask = mask_bytes[row];
-    const void* p = row_of<BF>(a.logits, row * E);
+    const void* p = row_of<BF>(a.logits, (uint64_t)row * (uint32_t)E);
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = load_at<BF>(p, off[i]);
   };
-  const int64_t stride = (int64_t)gridDim.x * waves * R;
-  int64_t t0 = ((int64_t)blockIdx.x * waves + w) * R;
+  const uint32_t stride = gridDim.x * waves * R;
+  uint32_t t0 = (blockIdx.x * waves + w) * R;
   float next[NV];
   uint32_t next_mask;
   load(t0 + g, next, next_mask);
-  for (; t0 < a.T; t0 += stride) {
-    const int64_t t = t0 + g;
-    bool on = t < a.T && (!masked || next_mask != 0);
+  for (; t0 < T; t0 += stride) {
+    const uint32_t t = t0 + g;
+    bool on = t < T && (!masked || next_mask != 0);
     float x[NV];
     if constexpr (L == 64) {
       on = !masked || __builtin_amdgcn_readfirstlane(next_mask) != 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) x[i] = i * L + l < E ? next[i] : kNegInf;
+      for (int i = 0; i < NV; ++i) x[i] = next[i];
+      if (E != NV * L) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) x[i] = i * L + l < E ? x[i] : kNegInf;
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i) x[i] = on && i * L + l < E ? next[i] : kNegInf;
@@ -452,8 +468,8 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
     load(t + stride, next, next_mask);
     if (L == 64 && !on) {                    // padding: the wavefront has nothing to select
       if (l < k) {
-        a.topk_ids[t * k + l] = -1;
-        a.gate[t * k + l] = 0.0f;
+        store_at(a.topk_ids + (uint64_t)t * (uint32_t)k, l, -1);
+        store_at(a.gate + (uint64_t)t * (uint32_t)k, l, 0.0f);
       }
       continue;
     }
@@ -499,7 +515,7 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
     if constexpr (STATS) {
       const float r = live && total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) psum[i] += p[i] * r;
+      for (int i = 0; i < NV; ++i) psum[i] = __fmaf_rn(p[i], r, psum[i]);
       if (l < k && id >= 0) atomicAdd(&sh_count[id], 1);
       if (l == 0 && live) atomicAdd(&sh_count[E], 1);
     }
@@ -518,9 +534,9 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
       const float sum = L == 64 && k <= 16 ? group_sum<16>(gate) : group_sum<L>(gate);
       gate = sum > 0.0f ? gate * __builtin_amdgcn_rcpf(sum) : 0.0f;
     }
-    if (l < k && t < a.T) {
-      a.topk_ids[t * k + l] = id;
-      a.gate[t * k + l] = gate * a.scale;
+    if (l < k && t < T) {
+      store_at(a.topk_ids + (uint64_t)t * (uint32_t)k, l, id);
+      store_at(a.gate + (uint64_t)t * (uint32_t)k, l, gate * a.scale);
     }
   }
   if constexpr (STATS) {
@@ -796,6 +812,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
   const int l = lane & (L - 1), g = L == 64 ? 0 : lane / L;
   float* sh = sh_all[w * R + g];
   const int E = a.E, k = a.k;
+  const uint32_t T = (uint32_t)a.T;         // rows: below 2^31, like T k
   float coef[BAL ? NV : 1];
   if constexpr (BAL) {
     const double n = (double)a.counts[E];
@@ -812,23 +829,26 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) off[i] = (uint32_t)(i * L + l < E ? i * L + l : E - 1) * (BF ? 2 : 4);
   const int slot = l < k ? l : k - 1;
-  const auto load = [&](int64_t t, float (&v)[NV], int& id, float& dg) {
-    const int64_t row = t < a.T ? t : a.T - 1;
-    id = a.topk_ids[row * k + slot];
-    dg = a.dgate ? a.dgate[row * k + slot] : 0.0f;
-    const void* p = row_of<BF>(a.logits, row * E);
+  // without dgate the ids are read in its place and not looked at
+  const void* dgate = a.dgate ? static_cast<const void*>(a.dgate) : a.topk_ids;
+  const auto load = [&](uint32_t t, float (&v)[NV], int& id, float& dg) {
+    const uint32_t row = t < T ? t : T - 1;
+    const uint64_t first = (uint64_t)row * (uint32_t)k * 4;
+    id = read_at<int32_t>(reinterpret_cast<const char*>(a.topk_ids) + first, slot * 4);
+    dg = read_at<float>(static_cast<const char*>(dgate) + first, slot * 4);
+    const void* p = row_of<BF>(a.logits, (uint64_t)row * (uint32_t)E);
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = load_at<BF>(p, off[i]);
   };
-  const int64_t stride = (int64_t)gridDim.x * kWaves * R;
-  int64_t t0 = ((int64_t)blockIdx.x * kWaves + w) * R;
+  const uint32_t stride = gridDim.x * kWaves * R;
+  uint32_t t0 = (blockIdx.x * kWaves + w) * R;
   float next[NV], next_dg;
   int next_id;
   load(t0 + g, next, next_id, next_dg);
-  for (; t0 < a.T; t0 += stride) {
-    const int64_t t = t0 + g;
-    const int id = l < k && t < a.T && next_id >= 0 && next_id < E ? next_id : -1;
-    const float dg = id >= 0 ? next_dg * a.scale : 0.0f;
+  for (; t0 < T; t0 += stride) {
+    const uint32_t t = t0 + g;
+    const int id = l < k && t < T && next_id >= 0 && next_id < E ? next_id : -1;
+    const float dg = id >= 0 && a.dgate ? next_dg * a.scale : 0.0f;
     float x[NV], d[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) x[i] = i * L + l < E ? next[i] : kNegInf;
@@ -914,13 +934,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
         d[i] = RENORM ? d[i] + dp : dp;
       }
     }
+    const uint64_t at = (uint64_t)t * (uint32_t)E;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = i * L + l;
-      if (e < E && t < a.T) {
+      if (e < E && t < T) {
         const float y = live ? d[i] : 0.0f;
-        if constexpr (BF) static_cast<uint16_t*>(a.dlogits)[t * E + e] = (uint16_t)pk_bf16(y, 0.0f);
-        else static_cast<float*>(a.dlogits)[t * E + e] = y;
+        if constexpr (BF) store_at(static_cast<uint16_t*>(a.dlogits) + at, e, (uint16_t)pk_bf16(y, 0.0f));
+        else store_at(static_cast<float*>(a.dlogits) + at, e, y);
       }
     }
   }
