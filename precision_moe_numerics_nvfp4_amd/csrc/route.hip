@@ -75,9 +75,23 @@ __device__ __forceinline__ double across(double v) {
   return __longlong_as_double((int64_t)r);
 }
 
+// A value joined over the four rows of 16 lanes, lane by lane: the two halves of
+// each pair of rows, then of the wavefront, meet in the results of a row swap.
+template <class T, class Op>
+__device__ __forceinline__ T join_rows(T v, Op op) {
+  static_assert(sizeof(T) == 4);
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t r0 = r[0], r1 = r[1];
+  v = op(__builtin_bit_cast(T, r0), __builtin_bit_cast(T, r1));
+  const uint32_t x = __builtin_bit_cast(uint32_t, v);
+  const auto q = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  const uint32_t q0 = q[0], q1 = q[1];
+  return op(__builtin_bit_cast(T, q0), __builtin_bit_cast(T, q1));
+}
+
 // A value joined over the group of L lanes, in every lane: four DPP steps make
-// rows of 16 uniform; the two halves of each pair of rows, then of the
-// wavefront, meet in the results of a row swap.
+// rows of 16 uniform, the row swaps join them.
 template <int L, class T, class Op>
 __device__ __forceinline__ T group_join(T v, Op op) {
   v = op(v, across<0>(v));
@@ -86,14 +100,7 @@ __device__ __forceinline__ T group_join(T v, Op op) {
   v = op(v, across<3>(v));
   if constexpr (L == 64) {
     if constexpr (sizeof(T) == 4) {
-      const uint32_t u = __builtin_bit_cast(uint32_t, v);
-      const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-      const uint32_t r0 = r[0], r1 = r[1];
-      v = op(__builtin_bit_cast(T, r0), __builtin_bit_cast(T, r1));
-      const uint32_t x = __builtin_bit_cast(uint32_t, v);
-      const auto q = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-      const uint32_t q0 = q[0], q1 = q[1];
-      v = op(__builtin_bit_cast(T, q0), __builtin_bit_cast(T, q1));
+      v = join_rows(v, op);
     } else {
       v = op(v, __shfl_xor(v, 16, 64));
       v = op(v, __shfl_xor(v, 32, 64));
@@ -244,16 +251,12 @@ __device__ __forceinline__ float k_reached(float v, int k) {
   return unordered(low);
 }
 
-struct Candidate {
-  float x;
-  int e;
-};
-
-// LDS of a wavefront's selection.
+// LDS of a wavefront's selection: its candidates in expert order, then its slots.
 template <bool BIAS>
 struct Candidates {
-  Candidate of[64];
-  float key[BIAS ? 64 : 1];
+  alignas(16) float key[64];
+  int e[64];
+  float x[BIAS ? 64 : 1];                      // without a bias the key is the logit
 };
 
 // The float32 keys of a lane's experts.
@@ -324,33 +327,52 @@ __device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g
     const int at = base + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(hit[i] >> 32),
                                                          __builtin_amdgcn_mbcnt_lo((uint32_t)hit[i], 0));
     if (key[i] >= cut) {
-      list.of[at] = Candidate{x[i], i * 64 + lane};
-      if constexpr (BIAS) list.key[at] = key[i];
+      list.key[at] = key[i];
+      list.e[at] = i * 64 + lane;
+      if constexpr (BIAS) list.x[at] = x[i];
     }
     base += __popcll(hit[i]);
   }
-  wave_lds_fence();
-  const Candidate c = lane < n ? list.of[lane] : Candidate{kNegInf, 0};
-  float mine32 = c.x;
-  if constexpr (BIAS) mine32 = lane < n ? list.key[lane] : kNegInf;
-  wave_lds_fence();
-  // one unsigned comparison: the key, then the earlier place in the list
-  const uint32_t u = ordered(mine32 + 0.0f);
-  const uint64_t mine = ((uint64_t)u << 32) | (uint32_t)(63 - lane);
+  // Each candidate counts the keys ahead of it, equal ones of lower experts
+  // among them. Up to 16 candidates: lane 16 q + c compares candidate c with
+  // candidates 4 q .. 4 q + 3 (one 16-byte read), the row swaps add the quarters.
   int rank = 0;
-  for (int j = 0; j < n; ++j) {
-    const uint64_t other =
-        ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)u, j) << 32) | (uint32_t)(63 - j);
-    rank += other > mine;
+  const int c = n <= 16 ? lane & 15 : lane;
+  if (n <= 16) {
+    if (lane >= n && lane < 16) list.key[lane] = kNegInf;
+    wave_lds_fence();
+    const int q = lane >> 4;
+    const float mine = list.key[c];
+    const float4 other = *reinterpret_cast<const float4*>(&list.key[4 * q]);
+    const float o[4] = {other.x, other.y, other.z, other.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rank += o[i] > mine || (o[i] == mine && 4 * q + i < c);
+    rank = join_rows(rank, [](int u, int v) { return u + v; });
+  } else {
+    wave_lds_fence();
+    // one unsigned comparison: the key, then the earlier place in the list
+    const uint32_t u = ordered((lane < n ? list.key[lane] : kNegInf) + 0.0f);
+    const uint64_t mine = ((uint64_t)u << 32) | (uint32_t)(63 - lane);
+    for (int j = 0; j < n; ++j) {
+      const uint64_t other =
+          ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)u, j) << 32) | (uint32_t)(63 - j);
+      rank += other > mine;
+    }
   }
+  const bool holds = lane < n;                 // (c is the lane there)
+  const float mykey = holds ? list.key[c] : kNegInf;
+  const int myexpert = holds ? list.e[c] : 0;
+  float myx = mykey;
+  if constexpr (BIAS) myx = holds ? list.x[c] : kNegInf;
+  wave_lds_fence();
   if constexpr (BIAS) {
-    if (lane < n) list.key[rank] = mine32;
+    if (holds) list.key[rank] = mykey;
     wave_lds_fence();
     const bool near = lane < k && lane + 1 < n &&
                       list.key[lane] - list.key[lane + 1] <= key_margin(list.key[lane]);
     wave_lds_fence();
     if (__any(near)) {
-      const double key64 = lane < n ? biased_key(c.x, bias_g[c.e]) : (double)kNegInf;
+      const double key64 = holds ? biased_key(myx, bias_g[myexpert]) : (double)kNegInf;
       const uint64_t bits = __double_as_longlong(key64);
       rank = 0;
       for (int j = 0; j < n; ++j) {
@@ -361,12 +383,14 @@ __device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g
       }
     }
   }
-  if (lane < n && rank < k) list.of[rank] = c;
+  if (holds && rank < k) {
+    list.e[rank] = myexpert;
+    list.key[rank] = myx;
+  }
   wave_lds_fence();
   if (lane < k && lane < n) {
-    const Candidate slot = list.of[lane];
-    id = slot.e;
-    sx = slot.x;
+    id = list.e[lane];
+    sx = list.key[lane];
   }
   wave_lds_fence();
 }
