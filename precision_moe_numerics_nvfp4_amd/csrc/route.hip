@@ -9,11 +9,22 @@
 //           p the scores of a row summing to one;
 //   loss    alpha * E * sum_e counts[e] / (N k) * prob_sum[e] / N.
 //
-// A group of L lanes takes a row, lane l its experts l, l + L, ...: every load
-// and store is one run of lanes, a lane meets the same experts in every row
-// (their probability sums and loss gradients stay in registers), and the k
-// results sit in the group's first k lanes. L is the wavefront, or 16 (four
-// rows to a wavefront, joined by DPP operands alone) up to 64 experts.
+// Three forms, by the rows and experts at hand (route_plan, route_bwd_plan):
+//   wide    a wavefront per row, lane l its experts l, l + 64, ...: every load
+//           and store is one run of lanes, a lane meets the same experts in
+//           every row (their probability sums and loss gradients stay in
+//           registers), and the k results sit in the first k lanes;
+//   narrow  the same with 16 lanes per row, four rows to a wavefront, joined by
+//           DPP operands alone;
+//   single  a thread per row, its logits in registers, for many rows of few
+//           experts.
+// What bounds them (MI355X, kernels back to back, statistics and loss apart):
+// 32768 x 384 top-8 takes 15.9 us for 50.3 MB of logits (3.2 TB/s; at the rate
+// of a copy, 5.1 TB/s, 10.2 us) and as long in bfloat16: vector and scalar issue,
+// some 200 and 150 instructions a row. 262144 x 64 top-6 single takes 22.7 us
+// for 79.7 MB (3.5 TB/s). The backward streams: 32768 x 384 23.9 us for 102.8 MB
+// (4.3 TB/s), 262144 x 64 33.5 us for 146.8 MB (4.4 TB/s). Below some thousand
+// rows a launch costs 2.5 to 4 us whatever it does.
 #include "codecs.hpp"
 #include "internal.hpp"
 
@@ -426,9 +437,9 @@ __device__ __forceinline__ void leave_stats(const RouteArgs& a, int e, float pro
   }
 }
 
-// Eight wavefronts a SIMD where the registers allow it (share of 32768 x 384
-// 17.1 us against 18.6 without the attribute; the biased form, with its 64-bit
-// path, 42 against 26).
+// Eight wavefronts a SIMD where the registers allow it (32768 x 384 top-8 15.9
+// us against 17.0 without the attribute; the biased form, with its 64-bit path,
+// would spill: 42 against 26).
 template <bool BF, bool SIG, bool BIAS, bool STATS, int L, int NV>
 __global__ __launch_bounds__(64 * kMaxWaves)
 __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) void k_route(RouteArgs a) {
@@ -826,8 +837,14 @@ struct RouteBwdArgs {
   void* dlogits;
 };
 
-// The selected experts' part of a row's gradient is computed one slot per
-// lane and reaches the lanes that own the experts through LDS.
+// The selected experts' part of a row's gradient is computed one slot per lane
+// and reaches the lanes that own the experts through LDS. With s the scores, u
+// the gradient of the selected ones, a the loss's of p:
+//   softmax            dx = p (u + a - sum p (u + a));
+//   renormalised       q = s over its sum: the slots add q (u - sum q u), the
+//                      loss p (a - sum p a);
+//   sigmoid            dx = s' (u + (a - sum p a) / sum s), renormalised u
+//                      (u - sum q u) / sum of the selected.
 template <bool BF, bool SIG, bool RENORM, bool BAL, int L, int NV>
 __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
   constexpr int R = 64 / L;
@@ -1097,21 +1114,22 @@ __global__ __launch_bounds__(kRowThreads) void k_route_bwd_rows(RouteBwdArgs a, 
   }
 }
 
-// Whether rows go to groups of 16 lanes. A round of the selection costs each of
-// four rows less than the wavefront's form costs one, up to some k; measured
-// against it at 131072 rows of 128 experts: top-2 18 against 45 us, top-8 44
-// against 51, top-16 82 against 62; backward 35 against 48 us, but 4.5 against
-// 3.2 us at 512 rows.
+// Whether rows go to groups of 16 lanes: a round of the selection there serves
+// four rows, but every slot takes one, where the wide form's cost hardly grows
+// with k. Narrow against wide: 32768 x 64 top-6 8.1 and 13.5 us, top-16 16.5
+// and 18.1 (512 rows top-6: 3.6 and 2.8); 131072 x 128 top-2 18.2 and 48.3,
+// top-8 46.6 and 47.6, top-16 84 and 63; backward 131072 x 128 33.9 and 45.4,
+// 32768 rows 12.2 and 14.0, 512 rows 4.6 and 3.1.
 bool narrow(int64_t T, int E, int k, bool biased, bool backward) {
   if (k > kNarrowK || E > 128) return false;
   return E <= 64 || (backward ? T >= 32768 : !biased && k <= 4);
 }
 
 // Whether rows go to single threads: rows enough to fill the device, few enough
-// experts for the registers. Against groups of 16 lanes, both at the bound and
-// at 262144 rows: 8 experts 2.4 against 2.7 us (at 4096) and 3.5 against 18.3,
-// 64 experts top-6 12 against 14 and 22 against 50; backward and biased, 8
-// experts, 4.2 against 4.6 and 9.0 against 17.
+// experts for the registers. Single against narrow, at the bound and at 262144
+// rows: 8 experts top-2 2.5 and 2.5 us (4096 rows), 3.7 and 18.9; 64 experts
+// top-6 12.2 and 14.7 (65536 rows), 22.7 and 52.1; 8 experts backward 4.1 and
+// 4.3 (32768 rows), 8.7 and 16.9; biased 4.0 and 4.5, 7.8 and 21.1.
 bool single(int64_t T, int E, int k, bool biased, bool backward) {
   if (k > kNarrowK || E > (biased || backward ? 8 : 64)) return false;
   return T >= (biased || backward ? 32768 : 1024 * E);
@@ -1129,8 +1147,9 @@ int lanes_experts(int E) {
 }
 
 // Wavefronts of a forward workgroup: few while the rows do not fill the device
-// (512 x 384 biased: 3.9 us with 4, 4.0 with 8, 4.7 with 16), many when they do,
-// for fewer statistics partials (32768 x 384: 31.4, 28.1, 26.5 us).
+// (512 x 384 biased: 3.8 us with 4, 4.6 with 16), many when they do, for fewer
+// statistics partials (32768 x 384 with statistics and loss: 37.9 us with 4,
+// 25.8 with 16; without them 16.1 and 16.0).
 int route_waves(int64_t T, int rows_per_wave) {
   const int64_t need = (T + rows_per_wave - 1) / rows_per_wave;
   return need <= 1024 ? 4 : need <= 2048 ? 8 : kMaxWaves;
