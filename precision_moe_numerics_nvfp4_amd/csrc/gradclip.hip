@@ -10,9 +10,9 @@
 // kernel arguments (no copy to the device, nothing to keep alive): up to 280
 // tensors a launch for the sum, 180 for the scaling, within 4 KiB.
 //
-// Memory bounds large lists (604M float32 elements: the sum 403 us, 6.0 TB/s,
-// the scaling 888 us, 5.4 TB/s; a copy reaches 5.1), launches the short ones
-// (1.6M elements: 4.3 + 3.0 + 5.2 us of kernels).
+// Memory bounds large lists (604M float32 elements: the sum 405 us, 6.0 TB/s,
+// the scaling 890 us, 5.4 TB/s; a copy reaches 5.1), launches the short ones
+// (1.6M elements: 3.8 + 3.0 + 4.8 us of kernels).
 #include "codecs.hpp"
 #include "internal.hpp"
 
