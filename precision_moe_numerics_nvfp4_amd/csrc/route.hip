@@ -19,7 +19,7 @@
 //   single  a thread per row, its logits in registers, for many rows of few
 //           experts.
 // What bounds them (MI355X, kernels back to back, statistics and loss apart):
-// 32768 x 384 top-8 takes 15.9 us for 50.3 MB of logits (3.2 TB/s; at the rate
+// 32768 x 384 top-8 takes 15.4 us for 50.3 MB of logits (3.3 TB/s; at the rate
 // of a copy, 5.1 TB/s, 10.2 us) and as long in bfloat16: vector and scalar issue,
 // some 200 and 150 instructions a row. 262144 x 64 top-6 single takes 22.7 us
 // for 79.7 MB (3.5 TB/s). The backward streams: 32768 x 384 23.9 us for 102.8 MB
@@ -265,9 +265,9 @@ __device__ __forceinline__ float k_reached(float v, int k) {
 // LDS of a wavefront's selection: its candidates in expert order, then its slots.
 template <bool BIAS>
 struct Candidates {
-  alignas(16) float key[64];
-  int e[64];
-  float x[BIAS ? 64 : 1];                      // without a bias the key is the logit
+  alignas(16) float key[128];                  // the upper halves: what is no candidate
+  int e[128];
+  float x[BIAS ? 128 : 1];                     // without a bias the key is the logit
 };
 
 // The float32 keys of a lane's experts.
@@ -337,11 +337,10 @@ __device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g
   for (int i = 0; i < NV; ++i) {
     const int at = base + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(hit[i] >> 32),
                                                          __builtin_amdgcn_mbcnt_lo((uint32_t)hit[i], 0));
-    if (key[i] >= cut) {
-      list.key[at] = key[i];
-      list.e[at] = i * 64 + lane;
-      if constexpr (BIAS) list.x[at] = x[i];
-    }
+    const int to = key[i] >= cut ? at : 64 + lane;
+    list.key[to] = key[i];
+    list.e[to] = i * 64 + lane;
+    if constexpr (BIAS) list.x[to] = x[i];
     base += __popcll(hit[i]);
   }
   // Each candidate counts the keys ahead of it, equal ones of lower experts
@@ -357,7 +356,8 @@ __device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g
     const float4 other = *reinterpret_cast<const float4*>(&list.key[4 * q]);
     const float o[4] = {other.x, other.y, other.z, other.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) rank += o[i] > mine || (o[i] == mine && 4 * q + i < c);
+    for (int i = 0; i < 4; ++i)
+      rank += (int)(o[i] > mine) | ((int)(o[i] == mine) & (int)(4 * q + i < c));
     rank = join_rows(rank, [](int u, int v) { return u + v; });
   } else {
     wave_lds_fence();
@@ -371,10 +371,10 @@ __device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g
     }
   }
   const bool holds = lane < n;                 // (c is the lane there)
-  const float mykey = holds ? list.key[c] : kNegInf;
-  const int myexpert = holds ? list.e[c] : 0;
+  const float mykey = list.key[c];
+  const int myexpert = list.e[c];
   float myx = mykey;
-  if constexpr (BIAS) myx = holds ? list.x[c] : kNegInf;
+  if constexpr (BIAS) myx = list.x[c];
   wave_lds_fence();
   if constexpr (BIAS) {
     if (holds) list.key[rank] = mykey;
@@ -399,10 +399,11 @@ __device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g
     list.key[rank] = myx;
   }
   wave_lds_fence();
-  if (lane < k && lane < n) {
-    id = list.e[lane];
-    sx = list.key[lane];
-  }
+  const bool slot = lane < k && lane < n;
+  const int e = list.e[lane];
+  const float v = list.key[lane];
+  id = slot ? e : -1;
+  sx = slot ? v : kNegInf;
   wave_lds_fence();
 }
 
