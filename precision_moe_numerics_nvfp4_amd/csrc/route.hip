@@ -149,14 +149,23 @@ __device__ __forceinline__ float exp_neg(float x) {
   return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f);
 }
 
-// sigmoid(x) and its derivative s (1 - s), both from z = exp(-|x|) so that
-// neither cancels: s = 1 / (1 + z) or z / (1 + z), s' = z / (1 + z)^2.
-__device__ __forceinline__ void sigmoid(float x, float& s, float& ds) {
+// sigmoid(x) and 1 - sigmoid(x), both from z = exp(-|x|) so that neither
+// cancels: 1 / (1 + z) and z / (1 + z), the first for the sign of x.
+__device__ __forceinline__ void sigmoid(float x, float& s, float& rest) {
   const float z = exp_neg(-fabsf(x));
   const float r = __builtin_amdgcn_rcpf(1.0f + z);
   s = x >= 0.0f ? r : z * r;
-  ds = z * r * r;
+  rest = x >= 0.0f ? z * r : r;
 }
+__device__ __forceinline__ float sigmoid(float x) {
+  float s, rest;
+  sigmoid(x, s, rest);
+  return s;
+}
+
+// Backward sums over sigmoid scores are formed scaled by this, an exact step, so
+// that products of scores near 2^-126 keep their bits.
+constexpr float kScaleUp = 0x1p64f;
 
 // The key experts compete with where a bias is given. 64 bits: two scores that
 // differ by less than a float32 step are told apart, and the choice does not
@@ -277,9 +286,7 @@ __device__ __forceinline__ void keys32(const float (&x)[NV], const float* bias, 
   for (int i = 0; i < NV; ++i) {
     key[i] = x[i];
     if constexpr (BIAS) {
-      float s, ds;
-      sigmoid(x[i], s, ds);
-      key[i] = x[i] > kNegInf ? s + bias[i] : kNegInf;
+      key[i] = x[i] > kNegInf ? sigmoid(x[i]) + bias[i] : kNegInf;
     }
   }
 }
@@ -538,12 +545,8 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
       if constexpr (!SIG) top = first;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        if constexpr (SIG) {
-          float ds;
-          sigmoid(x[i], p[i], ds);
-        } else {
-          p[i] = exp_neg(x[i] - top);
-        }
+        if constexpr (SIG) p[i] = sigmoid(x[i]);
+        else p[i] = exp_neg(x[i] - top);
         total += p[i];
       }
       total = group_sum<L>(total);
@@ -558,8 +561,7 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
     // gates of the selected, one per lane
     float gate = 0.0f;
     if constexpr (SIG) {
-      float ds;
-      sigmoid(sx, gate, ds);               // 0 in empty slots, whose logit is -inf
+      gate = sigmoid(sx);                  // 0 in empty slots, whose logit is -inf
     } else if (renorm) {
       gate = exp_neg(sx - first);
     } else {
@@ -668,10 +670,8 @@ __global__ __launch_bounds__(row_threads(NE)) void k_route_rows(RouteArgs a, boo
     const bool open = top > kNegInf;
     top = open ? top : 0.0f;
     const auto score = [&](float v) {
-      float s, ds;
-      if constexpr (SIG) sigmoid(v, s, ds);   // 0 for -inf
-      else s = exp_neg(v - top);
-      return s;
+      if constexpr (SIG) return sigmoid(v);   // 0 for -inf
+      else return exp_neg(v - top);
     };
     float total = 0.0f;
     if (STATS || (!SIG && !renorm)) {
@@ -844,8 +844,10 @@ struct RouteBwdArgs {
 //   softmax            dx = p (u + a - sum p (u + a));
 //   renormalised       q = s over its sum: the slots add q (u - sum q u), the
 //                      loss p (a - sum p a);
-//   sigmoid            dx = s' (u + (a - sum p a) / sum s), renormalised u
-//                      (u - sum q u) / sum of the selected.
+//   sigmoid            dx = (1 - s) (s u + p (a - sum p a)), p = s over the row's
+//                      sum; renormalised q (u - sum q u) in the place of s u, q
+//                      = s over the selected's (quotients of at most 1: no 1 / s
+//                      leaves the range).
 template <bool BF, bool SIG, bool RENORM, bool BAL, int L, int NV>
 __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
   constexpr int R = 64 / L;
@@ -913,16 +915,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
     if constexpr (RENORM) {
       float q;
       if constexpr (SIG) {
-        float ds;
-        sigmoid(sx, q, ds);                // 0 in empty slots, whose logit is -inf
+        q = sigmoid(sx) * kScaleUp;        // 0 in empty slots, whose logit is -inf
       } else {
         const float m = group_max<L>(sx);
         q = exp_neg(sx - (m > kNegInf ? m : 0.0f));
       }
       const float sum = group_sum<L>(q), dot = group_sum<L>(q * u);
       const float r = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
-      u = (u - dot * r) * r;
-      if constexpr (!SIG) u *= q;
+      u = (u - dot * r) * (q * r);
     }
     wave_lds_fence();
     if (id >= 0) atomicAdd(&sh[id], u);
@@ -933,11 +933,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
     if (id >= 0) sh[id] = 0.0f;
     // per expert
     if constexpr (SIG) {
-      float s[NV], ds[NV], total = 0.0f, dot = 0.0f;
+      float s[NV], rest[NV], total = 0.0f, dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        sigmoid(x[i], s[i], ds[i]);
+        sigmoid(x[i], s[i], rest[i]);
+        if constexpr (!RENORM) d[i] *= s[i];
         if constexpr (BAL) {
+          s[i] *= kScaleUp;
           total += s[i];
           dot += s[i] * coef[i];
         }
@@ -947,10 +949,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
         dot = group_sum<L>(dot);
         const float r = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) d[i] += (coef[i] - dot * r) * r;
+        for (int i = 0; i < NV; ++i) d[i] += (coef[i] - dot * r) * (s[i] * r);
       }
 #pragma unroll
-      for (int i = 0; i < NV; ++i) d[i] *= ds[i];
+      for (int i = 0; i < NV; ++i) d[i] *= rest[i];
     } else if constexpr (BAL || !RENORM) {
       float top = kNegInf, total = 0.0f, dot = 0.0f, p[NV];
 #pragma unroll
@@ -1022,12 +1024,8 @@ __global__ __launch_bounds__(kRowThreads) void k_route_bwd_rows(RouteBwdArgs a, 
         float v = kNegInf;
 #pragma unroll
         for (int e = 0; e < NE; ++e) v = e == id ? x[e] : v;
-        if constexpr (SIG) {
-          float ds;
-          sigmoid(v, q, ds);
-        } else {
-          q = exp_neg(v - top);
-        }
+        if constexpr (SIG) q = sigmoid(v) * kScaleUp;
+        else q = exp_neg(v - top);
       }
     };
     if constexpr (RENORM) {
@@ -1044,34 +1042,31 @@ __global__ __launch_bounds__(kRowThreads) void k_route_bwd_rows(RouteBwdArgs a, 
       int id;
       float u, q;
       slot(j, id, u, q);
-      if constexpr (RENORM) {
-        u = (u - dot * r) * r;
-        if constexpr (!SIG) u *= q;
-      }
+      if constexpr (RENORM) u = (u - dot * r) * (q * r);
       live = live || id >= 0;
 #pragma unroll
       for (int e = 0; e < NE; ++e) d[e] += e == id ? u : 0.0f;
     }
     // per expert
     if constexpr (SIG) {
-      float s[BAL ? NE : 1], ds[NE], total = 0.0f, all = 0.0f;
+      float s[NE], rest[NE], total = 0.0f, all = 0.0f;
 #pragma unroll
       for (int e = 0; e < NE; ++e) {
-        float v;
-        sigmoid(x[e], v, ds[e]);
+        sigmoid(x[e], s[e], rest[e]);
+        if constexpr (!RENORM) d[e] *= s[e];
         if constexpr (BAL) {
-          s[e] = v;
-          total += v;
-          all += v * coef[e];
+          s[e] *= kScaleUp;
+          total += s[e];
+          all += s[e] * coef[e];
         }
       }
       if constexpr (BAL) {
         const float rt = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
 #pragma unroll
-        for (int e = 0; e < NE; ++e) d[e] += (coef[e] - all * rt) * rt;
+        for (int e = 0; e < NE; ++e) d[e] += (coef[e] - all * rt) * (s[e] * rt);
       }
 #pragma unroll
-      for (int e = 0; e < NE; ++e) d[e] *= ds[e];
+      for (int e = 0; e < NE; ++e) d[e] *= rest[e];
     } else if constexpr (BAL || !RENORM) {
       float total = 0.0f, all = 0.0f, p[NE];
 #pragma unroll

@@ -451,3 +451,26 @@ def test_route_two_eager_streams(nv):
     torch.cuda.synchronize()
     for i, o in enumerate(outs):
         assert all(torch.equal(o[n], ref[i % 2][n]) for n in o)
+
+
+@pytest.mark.parametrize("T,E,k", [(40, 7, 2), (40, 60, 5), (40, 300, 8), (33000, 8, 2)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_tiny_sigmoid_scores(nv, T, E, k, renorm):
+    """Scores down to 2^-126: their quotients and gradients are those of any
+    other row's, though 1 / (a sum of them) squared is far out of range. A
+    product of scores that is below 2^-126 may be 0: 2^-126 times the gradient
+    and the loss's coefficient, absolute."""
+    rng = np.random.default_rng(T + E)
+    x = (-86 + 4 * rng.random((T, E))).astype(np.float32)
+    x[::2] += 60
+    dg = (50 * rng.normal(size=(T, k))).astype(np.float32)
+    o = nv.moe_route(to_dev(x), k, score="sigmoid", renorm=renorm, stats=True)
+    r = R.route(x, k, "sigmoid", renorm)
+    assert np.array_equal(from_dev(o["topk_ids"]), r["topk_ids"])
+    rel = (6 * _spread(x, "sigmoid") + E + 16) * U
+    _close(from_dev(o["gate"]), r["gate"], rel * r["gate"], "gate")
+    _close(from_dev(o["prob_sum"]), r["prob_sum"], (rel + T * U) * r["prob_sum"], "prob_sum")
+    got = from_dev(nv.moe_route_bwd(to_dev(x), o["topk_ids"], to_dev(dg), score="sigmoid", renorm=renorm,
+                                    counts=o["counts"], alpha=float(T)))
+    ref, mag = R.route_bwd(x, r["topk_ids"], dg, "sigmoid", renorm, 1.0, r["counts"], float(T))
+    _close(got, ref, 2 * rel * mag + 2.0 ** -126 * 200, "dlogits")
