@@ -748,11 +748,11 @@ def moe_route(logits, k, score="softmax", renorm=True, scale=1.0, bias=None, tok
     if bias is not None:
         bias = _on(bias, "bias", torch.float32, (E,), dev)
     if token_mask is not None:
-        if token_mask.dtype == torch.bool:
+        if isinstance(token_mask, torch.Tensor) and token_mask.dtype == torch.bool:
             token_mask = token_mask.view(torch.uint8)
         token_mask = _on(token_mask, "token_mask", torch.uint8, (T,), dev)
     _launch(dev, "moe_route", logits.data_ptr(), _in_dtype(logits), T, E, k, _score(score),
-            1 if renorm else 0, scale, bias, token_mask, ids, gate, counts, prob_sum,
+            1 if renorm else 0, float(scale), bias, token_mask, ids, gate, counts, prob_sum,
             None if ws is None else ws.data_ptr(), ws_bytes)
     return o
 
@@ -765,7 +765,7 @@ def moe_balance_loss(counts, prob_sum, k, alpha, loss=None):
     dev, E = prob_sum.device, prob_sum.shape[0]
     o = {"loss": loss}
     _launch(dev, "moe_balance_loss", _on(counts, "counts", torch.int64, (E + 1,), dev),
-            prob_sum.data_ptr(), E, int(k), alpha, _buf(o, "loss", torch.float32, (1,), dev))
+            prob_sum.data_ptr(), E, int(k), float(alpha), _buf(o, "loss", torch.float32, (1,), dev))
     return o["loss"]
 
 
@@ -788,8 +788,8 @@ def moe_route_bwd(logits, topk_ids, dgate=None, score="softmax", renorm=True, sc
     if dloss is not None:
         dloss = _on(dloss, "dloss", torch.float32, (1,), dev)
     _launch(dev, "moe_route_bwd", logits.data_ptr(), _in_dtype(logits), T, E, k, _score(score),
-            1 if renorm else 0, scale, _on(topk_ids, "topk_ids", torch.int32, (T, k), dev), dgate,
-            counts, alpha, dloss, _buf(o, "dlogits", logits.dtype, (T, E), dev))
+            1 if renorm else 0, float(scale), _on(topk_ids, "topk_ids", torch.int32, (T, k), dev),
+            dgate, counts, float(alpha), dloss, _buf(o, "dlogits", logits.dtype, (T, E), dev))
     return o["dlogits"]
 
 
@@ -900,6 +900,6 @@ def moe_grad_clip(grads, sumsq, max_norm, outs=None, norm=None):
         raise ValueError(f"sumsq is on {dev}, the gradients or outs elsewhere")
     res = {"norm": norm}
     _launch(dev, "moe_grad_clip", g.ptrs, o.ptrs, g.codes, g.numels, len(g),
-            _on(sumsq, "sumsq", torch.float64, (1,), dev), max_norm,
+            _on(sumsq, "sumsq", torch.float64, (1,), dev), float(max_norm),
             _buf(res, "norm", torch.float32, (1,), dev))
     return res["norm"]

@@ -316,6 +316,9 @@ def test_moe_route_refuses(nv):
         nv.moe_route(x, 2, token_mask=torch.ones(7, dtype=torch.bool, device="cuda"))
     with pytest.raises(ValueError):
         nv.moe_route(x, 2, out={"gate": torch.empty((8, 3), device="cuda")})
+    with pytest.raises(TypeError):
+        nv.moe_route(x, 2, token_mask=[True] * 8)
+    nv.moe_route(x, 2, scale=np.float32(2.5))                            # any number
     with pytest.raises(nv.Nvfp4moeError):
         nv.moe_route(x, 2, bias=torch.zeros(16, device="cuda"))          # softmax
     with pytest.raises(nv.Nvfp4moeError):
