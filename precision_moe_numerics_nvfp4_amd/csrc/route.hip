@@ -164,7 +164,7 @@ __device__ __forceinline__ float sigmoid(float x) {
 }
 
 // Backward sums over sigmoid scores are formed scaled by this, an exact step, so
-// that products of scores near 2^-126 keep their bits.
+// that the reciprocal of a sum near 2^-126 stays in range.
 constexpr float kScaleUp = 0x1p64f;
 
 // The key experts compete with where a bias is given. 64 bits: two scores that
@@ -920,9 +920,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
         const float m = group_max<L>(sx);
         q = exp_neg(sx - (m > kNegInf ? m : 0.0f));
       }
-      const float sum = group_sum<L>(q), dot = group_sum<L>(q * u);
-      const float r = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
-      u = (u - dot * r) * (q * r);
+      const float sum = group_sum<L>(q);
+      q *= sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
+      u = (u - group_sum<L>(q * u)) * q;
     }
     wave_lds_fence();
     if (id >= 0) atomicAdd(&sh[id], u);
@@ -933,7 +933,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
     if (id >= 0) sh[id] = 0.0f;
     // per expert
     if constexpr (SIG) {
-      float s[NV], rest[NV], total = 0.0f, dot = 0.0f;
+      float s[NV], rest[NV], total = 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         sigmoid(x[i], s[i], rest[i]);
@@ -941,15 +941,20 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
         if constexpr (BAL) {
           s[i] *= kScaleUp;
           total += s[i];
-          dot += s[i] * coef[i];
         }
       }
       if constexpr (BAL) {
         total = group_sum<L>(total);
-        dot = group_sum<L>(dot);
         const float r = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+        float dot = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) d[i] += (coef[i] - dot * r) * (s[i] * r);
+        for (int i = 0; i < NV; ++i) {
+          s[i] *= r;
+          dot += s[i] * coef[i];
+        }
+        dot = group_sum<L>(dot);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) d[i] += (coef[i] - dot) * s[i];
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) d[i] *= rest[i];
@@ -1034,22 +1039,31 @@ __global__ __launch_bounds__(kRowThreads) void k_route_bwd_rows(RouteBwdArgs a, 
         float u, q;
         slot(j, id, u, q);
         sum += q;
-        dot += q * u;
+        if constexpr (!SIG) dot += q * u;
       }
     }
     const float r = RENORM && sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
+    if constexpr (RENORM && !SIG) dot *= r;
+    if constexpr (RENORM && SIG) {         // scaled scores: quotients first, to stay in range
+      for (int j = 0; j < k; ++j) {
+        int id;
+        float u, q;
+        slot(j, id, u, q);
+        dot += q * r * u;
+      }
+    }
     for (int j = 0; j < k; ++j) {
       int id;
       float u, q;
       slot(j, id, u, q);
-      if constexpr (RENORM) u = (u - dot * r) * (q * r);
+      if constexpr (RENORM) u = (u - dot) * (q * r);
       live = live || id >= 0;
 #pragma unroll
       for (int e = 0; e < NE; ++e) d[e] += e == id ? u : 0.0f;
     }
     // per expert
     if constexpr (SIG) {
-      float s[NE], rest[NE], total = 0.0f, all = 0.0f;
+      float s[NE], rest[NE], total = 0.0f;
 #pragma unroll
       for (int e = 0; e < NE; ++e) {
         sigmoid(x[e], s[e], rest[e]);
@@ -1057,13 +1071,18 @@ __global__ __launch_bounds__(kRowThreads) void k_route_bwd_rows(RouteBwdArgs a, 
         if constexpr (BAL) {
           s[e] *= kScaleUp;
           total += s[e];
-          all += s[e] * coef[e];
         }
       }
       if constexpr (BAL) {
         const float rt = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+        float all = 0.0f;
 #pragma unroll
-        for (int e = 0; e < NE; ++e) d[e] += (coef[e] - all * rt) * (s[e] * rt);
+        for (int e = 0; e < NE; ++e) {
+          s[e] *= rt;
+          all += s[e] * coef[e];
+        }
+#pragma unroll
+        for (int e = 0; e < NE; ++e) d[e] += (coef[e] - all) * s[e];
       }
 #pragma unroll
       for (int e = 0; e < NE; ++e) d[e] *= rest[e];

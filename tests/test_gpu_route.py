@@ -477,3 +477,19 @@ def test_route_tiny_sigmoid_scores(nv, T, E, k, renorm):
                                     counts=o["counts"], alpha=float(T)))
     ref, mag = R.route_bwd(x, r["topk_ids"], dg, "sigmoid", renorm, 1.0, r["counts"], float(T))
     _close(got, ref, 2 * rel * mag + 2.0 ** -126 * 200, "dlogits")
+
+
+@pytest.mark.parametrize("T,E,k", [(100, 384, 8), (300, 64, 6), (40000, 8, 2)])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_bwd_scales_with_its_gradients(nv, T, E, k, renorm, score):
+    """The backward is linear in dgate and alpha: 2^80 times both (exact in
+    every product and sum, and far inside the range) gives 2^80 times the bits."""
+    rng = np.random.default_rng(T + E)
+    x = to_dev((2 * rng.normal(size=(T, E))).astype(np.float32))
+    dg = rng.normal(size=(T, k)).astype(np.float32)
+    o = nv.moe_route(x, k, score=score, renorm=renorm, stats=True)
+    got = [from_dev(nv.moe_route_bwd(x, o["topk_ids"], to_dev(dg * np.float32(c)), score=score,
+                                     renorm=renorm, counts=o["counts"], alpha=float(T) * c))
+           for c in (1.0, 2.0 ** 80)]
+    assert np.array_equal(got[0] * np.float32(2.0 ** 80), got[1])
