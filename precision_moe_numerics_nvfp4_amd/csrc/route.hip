@@ -20,7 +20,7 @@
 //           experts.
 // What bounds them (MI355X, kernels back to back, statistics and loss apart):
 // 32768 x 384 top-8 takes 15.4 us for 50.3 MB of logits (3.3 TB/s; at the rate
-// of a copy, 5.1 TB/s, 10.2 us) and as long in bfloat16: vector and scalar issue,
+// of a copy, 5.1 TB/s, 10.2 us) and 14.5 in bfloat16: vector and scalar issue,
 // some 200 and 150 instructions a row. 262144 x 64 top-6 single takes 22.7 us
 // for 79.7 MB (3.5 TB/s). The backward streams: 32768 x 384 23.9 us for 102.8 MB
 // (4.3 TB/s), 262144 x 64 33.5 us for 146.8 MB (4.4 TB/s). Below some thousand
