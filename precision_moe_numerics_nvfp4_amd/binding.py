@@ -9,6 +9,7 @@ import functools
 import os
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4moe.so")
+TENSORS_LIB_PATH = os.path.join(os.path.dirname(LIB_PATH), "libnvfp4moe_tensors.so")
 
 NVFP4MOE_F32 = 0
 NVFP4MOE_BF16 = 1
@@ -793,12 +794,27 @@ def moe_route_bwd(logits, topk_ids, dgate=None, score="softmax", renorm=True, sc
     return o["dlogits"]
 
 
+@functools.lru_cache(maxsize=None)
+def _tensors_lib():
+    """libnvfp4moe_tensors.so, whose calls keep the interpreter's lock."""
+    _torch()                                    # the libraries it is linked to
+    if not os.path.exists(TENSORS_LIB_PATH):
+        raise RuntimeError(
+            f"{TENSORS_LIB_PATH} is missing: build it with "
+            "`python -m precision_moe_numerics_nvfp4_amd.build` (or __graft_entry__.build())")
+    L = ctypes.PyDLL(TENSORS_LIB_PATH)
+    for f in (L.nvfp4moe_tensors_look, L.nvfp4moe_tensors_same):
+        f.argtypes, f.restype = [ctypes.py_object, _p, _c_i64], _c_int
+    return L
+
+
 class GradList:
     """The gradients (or their clipped copies) of one device as the calls
     below take them: contiguous bf16|f32 tensors of any alignment that do not
     overlap. Made once of buffers that live on, it keeps the tensors and their
-    memory; a tensor given other memory since (``t.data = ...``) is looked at
-    again in the next call, but sizes must not be changed in place."""
+    memory; every call looks whether a tensor has other memory, another size,
+    type or order since (``t.data = ...``, ``resize_``), and checks and takes
+    the whole list anew where one has."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
@@ -806,7 +822,11 @@ class GradList:
 
     def _look(self):
         torch = _torch()
-        ts = self.tensors
+        ts = self.tensors = list(self.tensors)
+        n = len(ts)
+        # before all else: what changes from here on is seen by the next call
+        seen = (_c_i64 * (3 * n))()
+        known = _tensors_lib().nvfp4moe_tensors_look(ts, seen, n)
         dev = None
         for i, t in enumerate(ts):
             if not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous()):
@@ -824,8 +844,9 @@ class GradList:
         for (_, end), (start, _) in zip(spans, spans[1:]):
             if start < end:
                 raise ValueError("tensors overlap (or one is listed twice)")
-        n = len(ts)
-        self.device, self.spans, self.storages = dev, spans, storages
+        if not known:
+            raise ValueError("tensors without memory of their own")
+        self.seen, self.device, self.spans, self.storages = seen, dev, spans, storages
         self.starts, self.sizes, self.types = starts, sizes, codes
         self.ptrs, self.numels, self.codes = (_p * n)(*starts), (_c_i64 * n)(*sizes), (_c_int * n)(*codes)
         self.workspace_size = int(lib().nvfp4moe_grad_workspace_size(self.numels, n))
@@ -834,7 +855,7 @@ class GradList:
         return len(self.tensors)
 
     def current(self):
-        if list(map(_torch().Tensor.data_ptr, self.tensors)) != self.starts:
+        if not _tensors_lib().nvfp4moe_tensors_same(self.tensors, self.seen, len(self.starts)):
             self._look()
         return self
 

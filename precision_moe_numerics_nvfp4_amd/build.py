@@ -1,4 +1,5 @@
-"""Build libnvfp4moe.so (HIP, gfx950) in-tree.
+"""Build libnvfp4moe.so (HIP, gfx950) in-tree, and beside it
+libnvfp4moe_tensors.so (C++, what a list of torch tensors points to).
 
 Usage: python -m precision_moe_numerics_nvfp4_amd.build [--jobs N]
 
@@ -19,12 +20,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libnvfp4moe.so")
+TENSORS_LIB = os.path.join(PKG, "libnvfp4moe_tensors.so")
 ARCH = "gfx950"
 
 FLAGS = [
@@ -52,12 +55,33 @@ def _compile(src):
     return obj
 
 
+def _build_tensors():
+    """Host code against the torch that is installed: no GPU compiler."""
+    import torch
+    top = os.path.dirname(torch.__file__)
+    tmp = TENSORS_LIB + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(top, "include"),
+           "-isystem", os.path.join(top, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_path("include"),
+           os.path.join(CSRC, "tensors.cpp"), "-o", tmp,
+           "-L" + os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TENSORS_LIB)
+
+
 def build(jobs=None, verbose=False):
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
-    jobs = jobs or min(8, len(srcs))
+    jobs = jobs or min(8, len(srcs) + 1)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        tensors = ex.submit(_build_tensors)
         objs = list(ex.map(_compile, srcs))
+        tensors.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", f"--offload-arch={ARCH}", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -65,7 +89,7 @@ def build(jobs=None, verbose=False):
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB}, {TENSORS_LIB}")
     return LIB
 
 

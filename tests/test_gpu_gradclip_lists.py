@@ -1,0 +1,70 @@
+"""Gradient lists on the GPU beyond single launches and single looks: tensors
+that change under a handle. Bounds as derived in test_gpu_gradclip."""
+
+import numpy as np
+import pytest
+
+from helpers import ensure_built, from_dev, to_dev
+from oracle import route as R
+from workloads import gen
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def nv():
+    ensure_built()
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import precision_moe_numerics_nvfp4_amd as nv
+    return nv
+
+
+def test_handle_of_a_tensor_cut_short(nv):
+    """The same address with fewer elements: the sum leaves out what is no
+    longer the tensor's, and a clip in place leaves it as it is."""
+    import torch
+    m = torch.full((5000,), 3.0, device="cuda")
+    t = m[:]
+    h = nv.GradList([t])
+    assert from_dev(nv.moe_grad_sumsq(h))[0] == 9.0 * 5000
+    t.data = m[:16]
+    s = nv.moe_grad_sumsq(h)
+    assert from_dev(s)[0] == 9.0 * 16
+    nv.moe_grad_clip(h, s, 6.0)                               # norm 12: halved
+    assert from_dev(m[:16]) == pytest.approx([1.5] * 16, rel=1e-6)
+    assert (from_dev(m[16:]) == 3.0).all()
+
+
+def test_handle_of_a_tensor_of_another_type(nv):
+    """The same address as the other type, in the sum and as an output."""
+    import torch
+    bits = gen.to_bf16_bits(np.random.default_rng(1).normal(size=6000).astype(np.float32))
+    m = to_dev(bits)                                          # pairs of them are finite float32 too
+    t = m.view(torch.float32)
+    h = nv.GradList([t])
+    nv.moe_grad_sumsq(h)
+    t.data = m[:3000]
+    s = nv.moe_grad_sumsq(h)
+    assert from_dev(s)[0] == pytest.approx(R.sumsq([bits[:3000]]), rel=2.0 ** -52 * 3008)
+    f = torch.zeros(3000, device="cuda")
+    with pytest.raises(ValueError):                           # float32 gradients, bfloat16 outputs
+        nv.moe_grad_clip([f], s, 1.0, outs=h)
+
+
+def test_handle_within_a_graph_keeps_what_was_captured(nv):
+    """A replay uses what the capture took; the next eager call what is there."""
+    import torch
+    m = torch.full((100,), 2.0, device="cuda")
+    t = m[:]
+    h = nv.GradList([t])
+    nv.moe_grad_sumsq(h)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s = nv.moe_grad_sumsq(h)
+    t.data = m[:10]
+    for _ in range(3):
+        s.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert from_dev(s)[0] == 400.0 and from_dev(nv.moe_grad_sumsq(h))[0] == 40.0
