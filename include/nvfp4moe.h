@@ -598,8 +598,9 @@ NVFP4MOE_API int moe_grad_sumsq(const void* const* grads, const int* dtypes, con
  * Gradients clipped by their global norm, sqrt(*sumsq):
  *   outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6)),
  * a float32 product rounded to the tensor's type; a norm of infinity gives a
- * factor of 0, NaN a factor of NaN. norm (device float32) gets the norm before clipping,
- * unless NULL. outs[i] is grads[i] (in place; left as it is when the factor is
+ * factor of 0, NaN a factor of NaN. A max_norm of infinity (no bound: the norm
+ * alone is wanted) gives a factor of 1, with a norm of infinity too, NaN with
+ * NaN. norm (device float32) gets the norm before clipping, unless NULL. outs[i] is grads[i] (in place; left as it is when the factor is
  * 1) or apart from every gradient; outputs must not overlap one another.
  * Host arrays, types and limits as moe_grad_sumsq; max_norm >= 0.
  */

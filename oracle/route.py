@@ -15,7 +15,8 @@ at work"); the formulas are readings:
   the N tokens with an expert of the row's normalised score; f is a constant
   of the gradient;
 * norm sqrt(sum of squares of all gradients); clipped = g * min(1, max_norm /
-  (norm + 1e-6)).
+  (norm + 1e-6)); an infinite max_norm bounds nothing, an infinite norm
+  included.
 """
 
 import numpy as np
@@ -142,5 +143,10 @@ def sumsq(grads):
 def clip(grads, total, max_norm):
     """(norm, clipped copies in float64)."""
     norm = float(np.sqrt(total))
-    coef = min(1.0, max_norm / (norm + 1e-6))
+    if np.isnan(norm):
+        coef = np.nan
+    elif np.isinf(max_norm):                 # no bound, whatever the norm
+        coef = 1.0
+    else:
+        coef = min(1.0, max_norm / (norm + 1e-6))
     return norm, [_vals(g) * coef for g in grads]

@@ -905,7 +905,8 @@ def moe_grad_clip(grads, sumsq, max_norm, outs=None, norm=None):
     """Scale a list of gradients by min(1, max_norm / (norm + 1e-6)), norm =
     sqrt(sumsq) of moe_grad_sumsq (or a sum of several ranks' values): in
     place, or into ``outs`` (same types and sizes, apart from the gradients).
-    Returns norm f32 [1], the norm before clipping."""
+    max_norm infinity leaves them as they are. Returns norm f32 [1], the norm
+    before clipping."""
     torch = _torch()
     _dev(sumsq, "sumsq", torch.float64)
     g = _grad_list(grads)

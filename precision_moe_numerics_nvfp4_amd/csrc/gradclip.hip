@@ -2,7 +2,7 @@
 //
 //   sumsq = sum over tensors and elements of g^2 (64-bit products and sums: no
 //           overflow or lost small terms whatever the gradients' scale);
-//   out   = g * min(1, max_norm / (sqrt(sumsq) + 1e-6)).
+//   out   = g * min(1, max_norm / (sqrt(sumsq) + 1e-6)), g for an infinite max_norm.
 //
 // Both passes stream: the tensors are cut into chunks, each workgroup takes a
 // contiguous run of chunks of the whole list, so a list of many small tensors
@@ -217,7 +217,9 @@ __global__ __launch_bounds__(kThreads) void k_grad_clip(GradTable<N, true> t, ui
                                                         float max_norm, float* __restrict__ norm) {
   const double root = sqrt(*sumsq);
   const double share = (double)max_norm / (root + 1e-6);
-  const float coef = share >= 1.0 ? 1.0f : (float)share;     // a NaN norm stays NaN
+  // no bound leaves the gradients as they are, infinite ones too; a NaN norm stays NaN
+  const bool whole = share >= 1.0 || (max_norm == __builtin_huge_valf() && root == root);
+  const float coef = whole ? 1.0f : (float)share;
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)root;
   if (t.n == 0) return;
   const uint32_t all = t.first[t.n];

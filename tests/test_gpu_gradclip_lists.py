@@ -68,3 +68,32 @@ def test_handle_within_a_graph_keeps_what_was_captured(nv):
         g.replay()
         torch.cuda.synchronize()
         assert from_dev(s)[0] == 400.0 and from_dev(nv.moe_grad_sumsq(h))[0] == 40.0
+
+
+@pytest.mark.parametrize("bad", [None, "inf", "-inf", "nan"])
+@pytest.mark.parametrize("max_norm", ["inf", "1e300", "1.0", "0.0"])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_infinite_bound_and_norm(nv, bad, max_norm, in_place):
+    """No bound leaves every gradient its bits, with a norm of infinity too (a
+    bound past float32 is one of infinity there); a NaN norm makes all NaN."""
+    import torch
+    host = [np.array([3.0, -4.0, 0.0], np.float32), gen.to_bf16_bits(np.full(9, 2.0, np.float32))]
+    if bad:
+        host[0][2] = float(bad)
+    ts = [to_dev(h) for h in host]
+    outs = ts if in_place else [torch.empty_like(t) for t in ts]
+    s = nv.moe_grad_sumsq(ts)
+    norm = nv.moe_grad_clip(ts, s, float(max_norm), outs=None if in_place else outs)
+    total = R.sumsq(host)
+    with np.errstate(invalid="ignore"):                       # infinity by a factor of 0
+        ref_norm, ref = R.clip(host, total, float(max_norm))
+    assert np.array_equal(from_dev(norm), np.array([ref_norm], np.float32), equal_nan=True)
+    for o, r, h in zip(outs, ref, host):
+        got = R._vals(from_dev(o))
+        if float(max_norm) > 1e30 and bad != "nan":
+            assert np.array_equal(from_dev(o), h)
+        else:
+            assert np.array_equal(np.isnan(got), np.isnan(r))
+            ok = ~np.isnan(r)
+            eps = 3 * 2.0 ** -24 + (2.0 ** -8 if h.dtype == np.uint16 else 0.0)
+            assert (np.abs(got[ok] - r[ok]) <= eps * np.abs(r[ok]) + 1e-37).all()

@@ -120,3 +120,16 @@ def test_unchanged_tensors_are_not_looked_at_again(B, monkeypatch):
     monkeypatch.setattr(B.GradList, "_look", lambda self: pytest.fail("looked at again"))
     assert h.current() is h
     assert B.GradList.current(h) is h
+
+
+def test_oracle_of_infinite_bounds_and_norms():
+    """The definition the GPU is compared with: no bound is a factor of 1, an
+    infinite norm under a bound one of 0, a NaN norm one of NaN."""
+    import numpy as np
+    from oracle import route as R
+    g = [np.array([2.0, 1.0])]
+    inf = float("inf")
+    for total, bound, want in [(inf, inf, 1.0), (5.0, inf, 1.0), (inf, 3.0, 0.0), (0.0, inf, 1.0)]:
+        assert np.array_equal(R.clip(g, total, bound)[1][0], want * g[0])
+    for bound in (inf, 3.0):
+        assert np.isnan(R.clip(g, float("nan"), bound)[1][0]).all()
