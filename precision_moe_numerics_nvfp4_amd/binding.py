@@ -731,13 +731,15 @@ def moe_route(logits, k, score="softmax", renorm=True, scale=1.0, bias=None, tok
 
     score 'softmax' or 'sigmoid'; renorm: gates divided by their sum; bias f32
     [E] ('sigmoid' only) shifts the choice, not the gates; token_mask bool or
-    uint8 [T], False for padding; ``out`` may hold any of the results' buffers."""
+    uint8 [T], False for padding; ``out`` may hold any of the results' buffers
+    (others in it are left alone and not returned)."""
     torch = _torch()
     _dev(logits, "logits", ndim=2)
     T, E = logits.shape
     k = int(k)
     dev = logits.device
-    o = {} if out is None else dict(out)
+    names = ("topk_ids", "gate", "counts", "prob_sum") if stats else ("topk_ids", "gate")
+    o = {} if out is None else {n: out[n] for n in names if n in out}
     ids = _buf(o, "topk_ids", torch.int32, (T, k), dev)
     gate = _buf(o, "gate", torch.float32, (T, k), dev)
     counts = prob_sum = ws = None
