@@ -16,6 +16,7 @@ NVFP4MOE_BF16 = 1
 _OUTER_PER_ROW, _OUTER_PER_GROUP = 0, 1
 _LAYOUT_TRANSPOSED, _LAYOUT_PER_GROUP = 0, 1
 _ROWWISE, _COLWISE_GROUPED = 0, 1
+_EINVAL, _EUNSUPPORTED = 1, 2
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 _c_i64 = ctypes.c_int64
@@ -717,6 +718,15 @@ def _score(score):
     return _SCORES[score]
 
 
+def _route_sizes(fn, T, E, k):
+    """The library's bounds, before an output of these sizes is made (and in
+    whole numbers: 2^32 + 2 slots are not the two that a C int would hold)."""
+    if E < 1 or k < 1:
+        _check(fn, _EINVAL)
+    if E > 1024 or k > 64 or k > E or T * k > 0x7FFFFFFF:
+        _check(fn, _EUNSUPPORTED)
+
+
 @functools.lru_cache(maxsize=256)
 def route_workspace_size(T, E):
     return int(lib().nvfp4moe_route_workspace_size(int(T), int(E)))
@@ -737,6 +747,7 @@ def moe_route(logits, k, score="softmax", renorm=True, scale=1.0, bias=None, tok
     _dev(logits, "logits", ndim=2)
     T, E = logits.shape
     k = int(k)
+    _route_sizes("moe_route", T, E, k)
     dev = logits.device
     names = ("topk_ids", "gate", "counts", "prob_sum") if stats else ("topk_ids", "gate")
     o = {} if out is None else {n: out[n] for n in names if n in out}
@@ -766,9 +777,11 @@ def moe_balance_loss(counts, prob_sum, k, alpha, loss=None):
     torch = _torch()
     _dev(prob_sum, "prob_sum", torch.float32, 1)
     dev, E = prob_sum.device, prob_sum.shape[0]
+    k = int(k)
+    _route_sizes("moe_balance_loss", 0, E, k)
     o = {"loss": loss}
     _launch(dev, "moe_balance_loss", _on(counts, "counts", torch.int64, (E + 1,), dev),
-            prob_sum.data_ptr(), E, int(k), float(alpha), _buf(o, "loss", torch.float32, (1,), dev))
+            prob_sum.data_ptr(), E, k, float(alpha), _buf(o, "loss", torch.float32, (1,), dev))
     return o["loss"]
 
 
@@ -782,6 +795,7 @@ def moe_route_bwd(logits, topk_ids, dgate=None, score="softmax", renorm=True, sc
     _dev(topk_ids, "topk_ids", torch.int32, 2)
     T, E = logits.shape
     k = topk_ids.shape[1]
+    _route_sizes("moe_route_bwd", T, E, k)
     dev = logits.device
     o = {"dlogits": dlogits}
     if dgate is not None:
