@@ -718,6 +718,16 @@ def _score(score):
     return _SCORES[score]
 
 
+def _number(v, name, kind=float):
+    """A host number of any type. A GPU tensor is refused: to read it the call
+    would have to wait for the device (and could not be captured)."""
+    if v.__class__ is kind:
+        return v
+    if isinstance(v, _torch().Tensor) and v.is_cuda:
+        raise ValueError(f"{name} must be a host number (got a tensor on {v.device})")
+    return kind(v)
+
+
 def _route_sizes(fn, T, E, k):
     """The library's bounds, before an output of these sizes is made (and in
     whole numbers: 2^32 + 2 slots are not the two that a C int would hold)."""
@@ -746,7 +756,7 @@ def moe_route(logits, k, score="softmax", renorm=True, scale=1.0, bias=None, tok
     torch = _torch()
     _dev(logits, "logits", ndim=2)
     T, E = logits.shape
-    k = int(k)
+    k = _number(k, "k", int)
     _route_sizes("moe_route", T, E, k)
     dev = logits.device
     names = ("topk_ids", "gate", "counts", "prob_sum") if stats else ("topk_ids", "gate")
@@ -766,7 +776,7 @@ def moe_route(logits, k, score="softmax", renorm=True, scale=1.0, bias=None, tok
             token_mask = token_mask.view(torch.uint8)
         token_mask = _on(token_mask, "token_mask", torch.uint8, (T,), dev)
     _launch(dev, "moe_route", logits.data_ptr(), _in_dtype(logits), T, E, k, _score(score),
-            1 if renorm else 0, float(scale), bias, token_mask, ids, gate, counts, prob_sum,
+            1 if renorm else 0, _number(scale, "scale"), bias, token_mask, ids, gate, counts, prob_sum,
             None if ws is None else ws.data_ptr(), ws_bytes)
     return o
 
@@ -777,11 +787,11 @@ def moe_balance_loss(counts, prob_sum, k, alpha, loss=None):
     torch = _torch()
     _dev(prob_sum, "prob_sum", torch.float32, 1)
     dev, E = prob_sum.device, prob_sum.shape[0]
-    k = int(k)
+    k = _number(k, "k", int)
     _route_sizes("moe_balance_loss", 0, E, k)
     o = {"loss": loss}
     _launch(dev, "moe_balance_loss", _on(counts, "counts", torch.int64, (E + 1,), dev),
-            prob_sum.data_ptr(), E, k, float(alpha), _buf(o, "loss", torch.float32, (1,), dev))
+            prob_sum.data_ptr(), E, k, _number(alpha, "alpha"), _buf(o, "loss", torch.float32, (1,), dev))
     return o["loss"]
 
 
@@ -805,8 +815,8 @@ def moe_route_bwd(logits, topk_ids, dgate=None, score="softmax", renorm=True, sc
     if dloss is not None:
         dloss = _on(dloss, "dloss", torch.float32, (1,), dev)
     _launch(dev, "moe_route_bwd", logits.data_ptr(), _in_dtype(logits), T, E, k, _score(score),
-            1 if renorm else 0, float(scale), _on(topk_ids, "topk_ids", torch.int32, (T, k), dev),
-            dgate, counts, float(alpha), dloss, _buf(o, "dlogits", logits.dtype, (T, E), dev))
+            1 if renorm else 0, _number(scale, "scale"), _on(topk_ids, "topk_ids", torch.int32, (T, k), dev),
+            dgate, counts, _number(alpha, "alpha"), dloss, _buf(o, "dlogits", logits.dtype, (T, E), dev))
     return o["dlogits"]
 
 
@@ -938,6 +948,6 @@ def moe_grad_clip(grads, sumsq, max_norm, outs=None, norm=None):
         raise ValueError(f"sumsq is on {dev}, the gradients or outs elsewhere")
     res = {"norm": norm}
     _launch(dev, "moe_grad_clip", g.ptrs, o.ptrs, g.codes, g.numels, len(g),
-            _on(sumsq, "sumsq", torch.float64, (1,), dev), float(max_norm),
+            _on(sumsq, "sumsq", torch.float64, (1,), dev), _number(max_norm, "max_norm"),
             _buf(res, "norm", torch.float32, (1,), dev))
     return res["norm"]

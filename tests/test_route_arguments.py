@@ -63,3 +63,34 @@ def test_backward_and_loss_sizes(B, monkeypatch):
         with pytest.raises(B.Nvfp4moeError) as e:
             call()
         assert e.value.status == EINVAL
+
+
+def test_numbers_on_the_device_are_refused(B, monkeypatch):
+    """Reading one would make the call wait for the GPU."""
+    x, one = _posing(8, 16), _posing()
+    for get in ("__float__", "__int__", "item"):
+        monkeypatch.setattr(_Posing, get, lambda self: pytest.fail("waited for the device"), raising=False)
+    ids, f = _posing(8, 2, dtype=torch.int32), dict(dtype=torch.float64)
+    h = B.GradList([])
+    for call in (lambda: B.moe_route(x, one), lambda: B.moe_route(x, 2, scale=one, out=_out()),
+                 lambda: B.moe_balance_loss(_posing(17, dtype=torch.int64), _posing(16), one, 0.1),
+                 lambda: B.moe_balance_loss(_posing(17, dtype=torch.int64), _posing(16), 2, one, loss=_posing(1)),
+                 lambda: B.moe_route_bwd(x, ids, scale=one, dlogits=_posing(8, 16)),
+                 lambda: B.moe_route_bwd(x, ids, alpha=one, dlogits=_posing(8, 16)),
+                 lambda: B.moe_grad_clip(h, _posing(1, **f), one, norm=_posing(1))):
+        with pytest.raises(ValueError, match="host number"):
+            call()
+
+
+def _out():
+    return {"topk_ids": _posing(8, 2, dtype=torch.int32), "gate": _posing(8, 2)}
+
+
+def test_host_numbers_of_any_type(B):
+    import numpy as np
+    from fractions import Fraction
+    for v in (2.5, 2, True, np.float32(2.5), np.int64(2), Fraction(5, 2), torch.tensor(2.5)):
+        assert B._number(v, "scale") == float(v)
+    assert B._number(np.int32(3), "k", int) == 3 and B._number(torch.tensor(3), "k", int) == 3
+    with pytest.raises((TypeError, ValueError)):
+        B._number("two", "scale")
