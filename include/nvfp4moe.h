@@ -101,7 +101,9 @@ enum nvfp4moe_layout { NVFP4MOE_LAYOUT_TRANSPOSED = 0, NVFP4MOE_LAYOUT_PER_GROUP
 /* Scores of the router (moe_route). */
 enum nvfp4moe_score { NVFP4MOE_SCORE_SOFTMAX = 0, NVFP4MOE_SCORE_SIGMOID = 1 };
 
-/* Version of this ABI (NVFP4MOE_ABI_VERSION). */
+/* Version of this ABI (NVFP4MOE_ABI_VERSION): raised when a call that was there
+ * changes. Calls that join leave it as it is; a library without them does not
+ * resolve their symbols. */
 NVFP4MOE_API int nvfp4moe_abi_version(void);
 
 /* Static string naming a status code; never NULL. */

@@ -95,7 +95,11 @@ def lib():
                 "`python -m precision_moe_numerics_nvfp4_amd.build` (or __graft_entry__.build())")
         L = ctypes.CDLL(LIB_PATH)
         for name, (args, res) in SIGNATURES.items():
-            f = getattr(L, name)
+            f = getattr(L, name, None)
+            if f is None:
+                raise RuntimeError(
+                    f"{LIB_PATH} lacks {name}: it is older than this package, build it again with "
+                    "`python -m precision_moe_numerics_nvfp4_amd.build` (or __graft_entry__.build())")
             f.argtypes = args
             f.restype = res
         _LIB = L
