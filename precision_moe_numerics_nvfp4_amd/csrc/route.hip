@@ -414,7 +414,15 @@ __device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g
   wave_lds_fence();
 }
 
-// One workgroup's share of an expert's statistics.
+// Rows whose probabilities a lane adds up in 32 bits before they go to a sum in
+// 64 (in LDS), so that the error of the statistics does not grow with the rows:
+// 4.2 million equal rows of 20 experts were off by 26 units of 2^-24 in 32 bits
+// throughout. 64-bit sums that every launch of at least this many rows a lane
+// pays for (32768 x 384 with statistics and loss 25.0 -> 25.3 us, a million rows
+// of 64 114.0 -> 115.2).
+constexpr int kHeldRows = 16;
+
+// One workgroup's share of an expert's statistics: a sum in 64 bits, rounded once.
 struct alignas(8) RoutePart {
   float prob;
   int32_t count;
@@ -433,14 +441,15 @@ struct RouteArgs {
   RoutePart* parts;      // [grid, E + 1], the last one's count the tokens
   int64_t* counts;       // of a workgroup that is the only one: the sums themselves
   float* prob_sum;
+  bool deep;             // a lane may take kHeldRows rows or more
 };
 
 // A workgroup's statistics of expert e (e = E: its tokens) on their way out.
-__device__ __forceinline__ void leave_stats(const RouteArgs& a, int e, float prob, int32_t count) {
+__device__ __forceinline__ void leave_stats(const RouteArgs& a, int e, double prob, int32_t count) {
   if (a.parts) {
-    a.parts[(int64_t)blockIdx.x * (a.E + 1) + e] = RoutePart{prob, count};
+    a.parts[(int64_t)blockIdx.x * (a.E + 1) + e] = RoutePart{(float)prob, count};
   } else {
-    if (e < a.E) a.prob_sum[e] = prob;
+    if (e < a.E) a.prob_sum[e] = (float)prob;
     a.counts[e] = count;
   }
 }
@@ -452,9 +461,14 @@ template <bool BF, bool SIG, bool BIAS, bool STATS, int L, int NV>
 __global__ __launch_bounds__(64 * kMaxWaves)
 __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) void k_route(RouteArgs a) {
   constexpr int R = 64 / L;                // rows of a wavefront
-  __shared__ float sh_prob[STATS ? kMaxWaves * 64 * NV : 1];
+  // the lanes' probability sums, each lane its own NV: in 64 bits where a lane
+  // takes kHeldRows rows or more, else the 32-bit ones on their way to the join
+  extern __shared__ double sh_prob[];
   __shared__ int32_t sh_count[STATS ? NV * L + 1 : 1];
   __shared__ Candidates<BIAS> list[L == 64 ? kMaxWaves : 1];
+  static_assert((STATS ? kMaxWaves * 64 * NV * sizeof(double) + 4 * (NV * L + 1) : 0) + sizeof(list) <=
+                    160 * 1024,
+                "LDS of a compute unit");
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & (L - 1), g = L == 64 ? 0 : lane / L;
   const int E = a.E, k = a.k, waves = blockDim.x >> 6;
@@ -466,9 +480,15 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
     for (int i = 0; i < NV; ++i) bias[i] = i * L + l < E ? a.bias[i * L + l] : 0.0f;
   }
   float psum[STATS ? NV : 1];
+  int held = 0;                            // rows in psum
+  const int own = (w * R + g) * NV * L + l;
   if constexpr (STATS) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) psum[i] = 0.0f;
+    if (a.deep) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) sh_prob[own + i * L] = 0.0;
+    }
     for (int e = threadIdx.x; e <= E; e += 64 * waves) sh_count[e] = 0;
     __syncthreads();
   }
@@ -555,6 +575,14 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
       const float r = live && total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) psum[i] = __fmaf_rn(p[i], r, psum[i]);
+      if (++held == kHeldRows) {
+        held = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          sh_prob[own + i * L] += (double)psum[i];
+          psum[i] = 0.0f;
+        }
+      }
       if (l < k && id >= 0) atomicAdd(&sh_count[id], 1);
       if (l == 0 && live) atomicAdd(&sh_count[E], 1);
     }
@@ -578,15 +606,25 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
     }
   }
   if constexpr (STATS) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) sh_prob[(w * R + g) * NV * L + i * L + l] = psum[i];
-    __syncthreads();
-    for (int e = threadIdx.x; e <= E; e += 64 * waves) {
-      float s = 0.0f;
-      if (e < E) {
-        for (int v = 0; v < waves * R; ++v) s += sh_prob[v * NV * L + e];
+    const auto join = [&](auto* sums) {
+      __syncthreads();
+      for (int e = threadIdx.x; e <= E; e += 64 * waves) {
+        double s = 0.0;
+        if (e < E) {
+          for (int v = 0; v < waves * R; ++v) s += (double)sums[v * NV * L + e];
+        }
+        leave_stats(a, e, s, sh_count[e]);
       }
-      leave_stats(a, e, s, sh_count[e]);
+    };
+    if (a.deep) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) sh_prob[own + i * L] += (double)psum[i];
+      join(sh_prob);
+    } else {
+      float* few = reinterpret_cast<float*>(sh_prob);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) few[own + i * L] = psum[i];
+      join(few);
     }
   }
 }
@@ -632,22 +670,39 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 // One row per thread. The statistics' sums over rows are matrix products: the
 // wavefront's values for expert e are the 16 x 4 operand, the other one is 1 in
 // column e (mod 16), so that expert's sums land in that column of the
-// accumulator, which stays over all rows (four registers for 16 experts). The
-// matrix instruction reads every lane: lanes past the rows hold zeros.
+// accumulator (four registers for 16 experts), four rows to an element at a
+// time; every kHeldRows of them it is added to sums in 64 bits. The matrix
+// instruction reads every lane: lanes past the rows hold zeros.
 template <bool BF, bool SIG, bool BIAS, bool STATS, int NE>
 __global__ __launch_bounds__(row_threads(NE)) void k_route_rows(RouteArgs a, bool vec) {
   constexpr int most = row_threads(NE), NA = (NE + 15) / 16, slots = NE < kNarrowK ? NE : kNarrowK;
   __shared__ float chosen[slots][most];             // the selected logits of each row
-  __shared__ float sh_prob[STATS ? most / 64 * NA * 16 : 1];
+  __shared__ double sh_prob[STATS ? most / 64 * NA * 16 : 1];    // each wavefront its own
   __shared__ int32_t sh_count[STATS ? NE + 1 : 1];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int E = a.E, k = a.k, threads = blockDim.x;
   const bool renorm = a.renorm;
   f32x4_t acc[STATS ? NA : 1];
   float column[STATS ? 16 : 1];
+  int held = 0;                                     // rows in an element of acc
+  // a lane's accumulator: four rows of column (lane mod 16)
+  const auto put_by = [&]() {
+    held = 0;
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      float s = (acc[i][0] + acc[i][1]) + (acc[i][2] + acc[i][3]);
+      s += __shfl_xor(s, 16, 64);
+      s += __shfl_xor(s, 32, 64);
+      if (lane < 16) sh_prob[(w * NA + i) * 16 + lane] += (double)s;
+      acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+  };
   if constexpr (STATS) {
 #pragma unroll
-    for (int i = 0; i < NA; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < NA; ++i) {
+      acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      if (lane < 16) sh_prob[(w * NA + i) * 16 + lane] = 0.0;
+    }
 #pragma unroll
     for (int c = 0; c < 16; ++c) column[c] = (lane & 15) == c ? 1.0f : 0.0f;
     for (int e = tid; e <= NE; e += threads) sh_count[e] = 0;
@@ -693,6 +748,8 @@ __global__ __launch_bounds__(row_threads(NE)) void k_route_rows(RouteArgs a, boo
         acc[e / 16] = __builtin_amdgcn_mfma_f32_16x16x4f32(score(x[e]) * r, column[e % 16],
                                                            acc[e / 16], 0, 0, 0);
       if (counts) atomicAdd(&sh_count[NE], 1);
+      held += 4;
+      if (held == kHeldRows) put_by();
     }
     // k rounds of the largest remaining key, the lowest expert among equals
     float sum = 0.0f;
@@ -745,17 +802,10 @@ __global__ __launch_bounds__(row_threads(NE)) void k_route_rows(RouteArgs a, boo
     }
   }
   if constexpr (STATS) {
-    // a lane's accumulator: four rows of column (lane mod 16)
-#pragma unroll
-    for (int i = 0; i < NA; ++i) {
-      float s = (acc[i][0] + acc[i][1]) + (acc[i][2] + acc[i][3]);
-      s += __shfl_xor(s, 16, 64);
-      s += __shfl_xor(s, 32, 64);
-      if (lane < 16) sh_prob[(w * NA + i) * 16 + lane] = s;
-    }
+    put_by();
     __syncthreads();
     for (int e = tid; e <= E; e += threads) {
-      float s = 0.0f;
+      double s = 0.0;
       if (e < E) {
         for (int v = 0; v < threads / 64; ++v) s += sh_prob[v * NA * 16 + e];
       }
@@ -1175,6 +1225,11 @@ enum RouteForm { kSingle, kNarrow, kWide };       // a thread, 16 lanes, a wavef
 struct RoutePlan {
   RouteForm form;
   unsigned grid, threads;
+  // A lane of the wide and narrow forms takes kHeldRows rows or more.
+  bool deep(int64_t T) const {
+    const int64_t at_once = (int64_t)grid * (threads / 64) * (form == kNarrow ? 4 : 1);
+    return (T + at_once - 1) / at_once >= kHeldRows;
+  }
 };
 
 // Few enough rows for one workgroup, which then leaves the statistics
@@ -1227,7 +1282,9 @@ RoutePlan route_bwd_plan(int64_t T, int E, int k) {
 
 template <bool BF, bool SIG, bool BIAS, bool STATS>
 void route_nv(const RouteArgs& a, const RoutePlan& at, hipStream_t s) {
-#define NVFP4MOE_ROUTE(L, NV) k_route<BF, SIG, BIAS, STATS, L, NV><<<at.grid, at.threads, 0, s>>>(a)
+  const size_t word = !STATS ? 0 : a.deep ? sizeof(double) : sizeof(float);
+#define NVFP4MOE_ROUTE(L, NV) \
+  k_route<BF, SIG, BIAS, STATS, L, NV><<<at.grid, at.threads, at.threads * NV * word, s>>>(a)
   if (at.form == kSingle) {
 #define NVFP4MOE_ROWS(NE) \
   k_route_rows<BF, SIG, BIAS, STATS, NE><<<at.grid, at.threads, 0, s>>>(a, whole_rows(a.logits, a.E, BF))
@@ -1335,7 +1392,7 @@ hipError_t launch_route(const void* logits, bool bf16, int64_t T, int E, int k, 
     grid = at.grid;
     if (stats && grid > 1) parts = static_cast<RoutePart*>(workspace);
     const RouteArgs a{logits, T, E, k, bias, token_mask, renorm, scale, topk_ids, gate, parts,
-                      counts, prob_sum};
+                      counts, prob_sum, stats && at.deep(T)};
     if (bf16) route_form<true>(a, sigmoid, stats, at, stream);
     else route_form<false>(a, sigmoid, stats, at, stream);
     const hipError_t e = hipGetLastError();
