@@ -97,3 +97,73 @@ def test_infinite_bound_and_norm(nv, bad, max_norm, in_place):
             ok = ~np.isnan(r)
             eps = 3 * 2.0 ** -24 + (2.0 ** -8 if h.dtype == np.uint16 else 0.0)
             assert (np.abs(got[ok] - r[ok]) <= eps * np.abs(r[ok]) + 1e-37).all()
+
+
+# Tables hold 280 tensors of a sum's launch, 180 of a scaling's, 16 of a short
+# list's; chunks have 2^11 elements up to 2^23 of them in all, then 2^12, 2^13
+# and 2^14; above 2048 chunks a workgroup goes through several, of several
+# tensors where those are short.
+LONG = {
+    "180": [700 + i for i in range(180)],
+    "181": [700 + i for i in range(181)],
+    "280": [300 + i % 7 for i in range(280)],
+    "281": [300 + i % 7 for i in range(281)],
+    "600-with-empty": [(i * 977) % 5003 * (i % 5 > 0) for i in range(600)],
+    "561-of-one": [1] * 561,
+    "runs-over-tensors": [50000 + i for i in range(120)],
+    "runs-over-short-ones": [3] * 100 + [7_000_000] + [5] * 60,
+    "chunks-of-2^12": [6_000_001, 1, 4097, 3_000_000, 70_000],
+    "chunks-of-2^13": [9_000_000, 0, 8_191, 8_192, 8_193, 12_000_001],
+    "chunks-of-2^14": [30_000_001] + [2, 16384, 0, 16385] * 10 + [20_000_003],
+    "three-chunks-a-run": [60_000_000] + [1, 2, 3] * 20 + [45_000_001, 16_383] + [9] * 17,
+}
+
+
+@pytest.mark.parametrize("name", LONG)
+@pytest.mark.parametrize("types", ["f32", "mixed"])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_long_lists(nv, name, types, in_place):
+    """The sum and every element, against 64-bit torch: random values without
+    zeros (a chunk left out or scaled twice shows), tensors one element off the
+    16-byte grid, memory between them left as it is."""
+    import torch
+    sizes = LONG[name]
+    kinds = [torch.bfloat16 if types == "mixed" and i % 2 else torch.float32 for i in range(len(sizes))]
+    gen_ = torch.Generator(device="cuda").manual_seed(len(sizes))
+
+    def flat(t, fill):
+        n = sum(m + 1 for m, u in zip(sizes, kinds) if u == t) + 1
+        if not fill:
+            return torch.full((n,), 7.0, dtype=t, device="cuda")
+        f = torch.rand(n, generator=gen_, device="cuda") + 0.5
+        return (f * torch.where(torch.rand(n, generator=gen_, device="cuda") < 0.5, -1e-2, 1e-2)).to(t)
+
+    def views(buf):
+        at, out = dict.fromkeys(buf, 1), []
+        for m, t in zip(sizes, kinds):
+            out.append(buf[t][at[t]:at[t] + m])
+            at[t] += m + 1
+        return out
+
+    buf = {t: flat(t, True) for t in dict.fromkeys(kinds)}
+    obuf = buf if in_place else {t: flat(t, False) for t in buf}
+    before = {t: b.clone() for t, b in buf.items()}
+    used = {t: torch.zeros(b.numel(), dtype=torch.bool, device="cuda") for t, b in buf.items()}
+    for v in views(used):
+        v.fill_(True)
+    grads, outs = nv.GradList(views(buf)), nv.GradList(views(obuf))
+    s = nv.moe_grad_sumsq(grads)
+    total = sum(float(b[used[t]].double().square().sum()) for t, b in before.items())
+    assert float(s) == pytest.approx(total, rel=2.0 ** -52 * (sum(sizes) + 8))
+    bound = 0.3 * np.sqrt(total)
+    norm = nv.moe_grad_clip(grads, s, bound, outs=outs)
+    assert float(norm) == pytest.approx(np.sqrt(total), rel=2.0 ** -23)
+    coef = bound / (np.sqrt(total) + 1e-6)
+    for t, b in obuf.items():
+        want = before[t][used[t]].double() * coef
+        eps = 3 * 2.0 ** -24 + (2.0 ** -8 if t == torch.bfloat16 else 0.0)
+        assert bool(((b[used[t]].double() - want).abs() <= eps * want.abs()).all())
+        rest = before[t][~used[t]] if in_place else torch.full_like(b[~used[t]], 7.0)
+        assert torch.equal(b[~used[t]], rest)
+        if not in_place:
+            assert torch.equal(buf[t], before[t])
