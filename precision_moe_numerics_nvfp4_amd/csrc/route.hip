@@ -163,6 +163,26 @@ __device__ __forceinline__ float sigmoid(float x) {
   return s;
 }
 
+// 1 / d within half a unit of its last place (the instruction's is one off), 0
+// for 0: what a row's probabilities are multiplied by.
+__device__ __forceinline__ float inverse(float d) {
+  const float r = __builtin_amdgcn_rcpf(d);
+  return d > 0.0f ? __fmaf_rn(__fmaf_rn(-d, r, 1.0f), r, r) : 0.0f;
+}
+
+// n / d, r the instruction's 1 / d: the product mended by its exact remainder.
+// The quotient of a number by itself is 1, so that one expert's share of
+// itself, and with it the gradient of a row that has a single one, leaves no
+// rounding behind: n * r leaves 2^-24 of the gradients that should cancel.
+__device__ __forceinline__ float quotient(float n, float d, float r) {
+  const float q = n * r;
+  return __fmaf_rn(__fmaf_rn(-q, d, n), r, q);
+}
+// 1 / d for quotient(), 0 for 0.
+__device__ __forceinline__ float estimate(float d) {
+  return d > 0.0f ? __builtin_amdgcn_rcpf(d) : 0.0f;
+}
+
 // Backward sums over sigmoid scores are formed scaled by this, an exact step, so
 // that the reciprocal of a sum near 2^-126 stays in range.
 constexpr float kScaleUp = 0x1p64f;
@@ -572,7 +592,7 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
       total = group_sum<L>(total);
     }
     if constexpr (STATS) {
-      const float r = live && total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+      const float r = live ? inverse(total) : 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) psum[i] = __fmaf_rn(p[i], r, psum[i]);
       if (++held == kHeldRows) {
@@ -593,12 +613,12 @@ __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) voi
     } else if (renorm) {
       gate = exp_neg(sx - first);
     } else {
-      gate = total > 0.0f ? exp_neg(sx - top) * __builtin_amdgcn_rcpf(total) : 0.0f;
+      gate = quotient(exp_neg(sx - top), total, estimate(total));
     }
     if (renorm) {
       // up to 16 slots lie in the first 16 lanes, whose sum is all that they need
       const float sum = L == 64 && k <= 16 ? group_sum<16>(gate) : group_sum<L>(gate);
-      gate = sum > 0.0f ? gate * __builtin_amdgcn_rcpf(sum) : 0.0f;
+      gate = quotient(gate, sum, estimate(sum));
     }
     if (l < k && t < T) {
       store_at(a.topk_ids + (uint64_t)t * (uint32_t)k, l, id);
@@ -742,7 +762,7 @@ __global__ __launch_bounds__(row_threads(NE)) void k_route_rows(RouteArgs a, boo
         for (int e = 0; e < NE; ++e)
           counts = counts || (x[e] > kNegInf && a.bias[e < E ? e : E - 1] > kNegInf);
       }
-      const float r = counts && total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+      const float r = counts ? inverse(total) : 0.0f;
 #pragma unroll
       for (int e = 0; e < NE; ++e)
         acc[e / 16] = __builtin_amdgcn_mfma_f32_16x16x4f32(score(x[e]) * r, column[e % 16],
@@ -794,10 +814,10 @@ __global__ __launch_bounds__(row_threads(NE)) void k_route_rows(RouteArgs a, boo
       }
     }
     const float den = renorm ? sum : SIG ? 1.0f : total;
-    const float r = den > 0.0f ? __builtin_amdgcn_rcpf(den) : 0.0f;
+    const float r = estimate(den);
     for (int j = 0; j < k; ++j) {
       float g = score(chosen[j][tid]);
-      if (!SIG || renorm) g *= r;
+      if (!SIG || renorm) g = quotient(g, den, r);
       if (in) a.gate[t * k + j] = g * a.scale;
     }
   }
@@ -971,7 +991,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
         q = exp_neg(sx - (m > kNegInf ? m : 0.0f));
       }
       const float sum = group_sum<L>(q);
-      q *= sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
+      q = quotient(q, sum, estimate(sum));
       u = (u - group_sum<L>(q * u)) * q;
     }
     wave_lds_fence();
@@ -995,11 +1015,11 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
       }
       if constexpr (BAL) {
         total = group_sum<L>(total);
-        const float r = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+        const float r = estimate(total);
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          s[i] *= r;
+          s[i] = quotient(s[i], total, r);
           dot += s[i] * coef[i];
         }
         dot = group_sum<L>(dot);
@@ -1024,12 +1044,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
       }
       total = group_sum<L>(total);
       dot = group_sum<L>(dot);
-      const float r = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+      const float r = inverse(total), mean = quotient(dot, total, r);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float v = RENORM ? 0.0f : d[i];
         if constexpr (BAL) v += coef[i];
-        const float dp = p[i] * r * (v - dot * r);
+        const float dp = p[i] * r * (v - mean);
         d[i] = RENORM ? d[i] + dp : dp;
       }
     }
@@ -1092,21 +1112,21 @@ __global__ __launch_bounds__(kRowThreads) void k_route_bwd_rows(RouteBwdArgs a, 
         if constexpr (!SIG) dot += q * u;
       }
     }
-    const float r = RENORM && sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
-    if constexpr (RENORM && !SIG) dot *= r;
+    const float r = RENORM ? estimate(sum) : 0.0f;
+    if constexpr (RENORM && !SIG) dot = quotient(dot, sum, r);
     if constexpr (RENORM && SIG) {         // scaled scores: quotients first, to stay in range
       for (int j = 0; j < k; ++j) {
         int id;
         float u, q;
         slot(j, id, u, q);
-        dot += q * r * u;
+        dot += quotient(q, sum, r) * u;
       }
     }
     for (int j = 0; j < k; ++j) {
       int id;
       float u, q;
       slot(j, id, u, q);
-      if constexpr (RENORM) u = (u - dot) * (q * r);
+      if constexpr (RENORM) u = (u - dot) * quotient(q, sum, r);
       live = live || id >= 0;
 #pragma unroll
       for (int e = 0; e < NE; ++e) d[e] += e == id ? u : 0.0f;
@@ -1124,11 +1144,11 @@ __global__ __launch_bounds__(kRowThreads) void k_route_bwd_rows(RouteBwdArgs a, 
         }
       }
       if constexpr (BAL) {
-        const float rt = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+        const float rt = estimate(total);
         float all = 0.0f;
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
-          s[e] *= rt;
+          s[e] = quotient(s[e], total, rt);
           all += s[e] * coef[e];
         }
 #pragma unroll
@@ -1146,12 +1166,12 @@ __global__ __launch_bounds__(kRowThreads) void k_route_bwd_rows(RouteBwdArgs a, 
         total += p[e];
         all += p[e] * v;
       }
-      const float rt = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+      const float rt = inverse(total), mean = quotient(all, total, rt);
 #pragma unroll
       for (int e = 0; e < NE; ++e) {
         float v = RENORM ? 0.0f : d[e];
         if constexpr (BAL) v += coef[e];
-        const float dp = p[e] * rt * (v - all * rt);
+        const float dp = p[e] * rt * (v - mean);
         d[e] = RENORM ? d[e] + dp : dp;
       }
     }
