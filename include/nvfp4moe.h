@@ -514,6 +514,9 @@ NVFP4MOE_API int moe_bwd_wgrad_nvfp4(const uint8_t* dyT_codes, const uint8_t* dy
  * Trains a 594B Model in 68 Hours" (hermes-ai), section "594B weights, 17B at
  * work": 8 of 384 experts); the formulas are the ones written here. Pointers of
  * these calls need the alignment of their elements only (workspaces 16 bytes).
+ * scale, alpha and max_norm are float32 numbers (0.001 is its nearest float32).
+ * A workspace belongs to one call at a time: calls that may run at once, on two
+ * streams or as replays of two graphs, need one each.
  * ------------------------------------------------------------------------- */
 
 /* Bytes of device workspace moe_route needs for its statistics (0 for few rows;

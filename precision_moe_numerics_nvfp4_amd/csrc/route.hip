@@ -19,12 +19,14 @@
 //   single  a thread per row, its logits in registers, for many rows of few
 //           experts.
 // What bounds them (MI355X, kernels back to back, statistics and loss apart):
-// 32768 x 384 top-8 takes 15.4 us for 50.3 MB of logits (3.3 TB/s; at the rate
-// of a copy, 5.1 TB/s, 10.2 us) and 14.5 in bfloat16: vector and scalar issue,
-// some 200 and 150 instructions a row. 262144 x 64 top-6 single takes 22.7 us
-// for 79.7 MB (3.5 TB/s). The backward streams: 32768 x 384 23.9 us for 102.8 MB
-// (4.3 TB/s), 262144 x 64 33.5 us for 146.8 MB (4.4 TB/s). Below some thousand
-// rows a launch costs 2.5 to 4 us whatever it does.
+// 32768 x 384 top-8 takes 15.5 us for 52.4 MB (3.4 TB/s; at the rate of a copy,
+// 5.1 TB/s, 10.2 us) and 14.6 in bfloat16 for half of the bytes: issue, 165
+// vector and 138 scalar instructions a row in both. 262144 x 64 top-6 single
+// takes 22.2 us for 79.7 MB (3.6 TB/s): vector issue too, 16 us of it, with 198
+// scalar registers (a comparison's mask per expert) in lanes of vector ones.
+// The backward streams: 32768 x 384 24.4 us for 102.8 MB (4.2 TB/s), 262144 x 64
+// 33.6 us for 146.8 MB (4.4 TB/s); in bfloat16 19.5 and 25.5, issue bound. Below
+// some thousand rows a launch costs 2.5 to 4 us whatever it does.
 #include "codecs.hpp"
 #include "internal.hpp"
 
@@ -436,10 +438,9 @@ __device__ __forceinline__ void select(const float (&x)[NV], const float* bias_g
 
 // Rows whose probabilities a lane adds up in 32 bits before they go to a sum in
 // 64 (in LDS), so that the error of the statistics does not grow with the rows:
-// 4.2 million equal rows of 20 experts were off by 26 units of 2^-24 in 32 bits
-// throughout. 64-bit sums that every launch of at least this many rows a lane
-// pays for (32768 x 384 with statistics and loss 25.0 -> 25.3 us, a million rows
-// of 64 114.0 -> 115.2).
+// in 32 bits throughout, 4.2 million equal rows of 20 experts were off by 26
+// units of 2^-24. Joins and comparison together cost 1% (32768 x 384 with
+// statistics and loss 25.0 -> 25.3 us, a million rows of 64 114.0 -> 115.2).
 constexpr int kHeldRows = 16;
 
 // One workgroup's share of an expert's statistics: a sum in 64 bits, rounded once.
@@ -474,9 +475,13 @@ __device__ __forceinline__ void leave_stats(const RouteArgs& a, int e, double pr
   }
 }
 
-// Eight wavefronts a SIMD where the registers allow it (32768 x 384 top-8 15.9
-// us against 17.0 without the attribute; the biased form, with its 64-bit path,
-// would spill: 42 against 26).
+// Eight wavefronts a SIMD where the registers allow it (32768 x 384 top-8 15.5
+// us against 16.8 without the attribute, 14.7 and 16.9 in bfloat16, 25.5 and 28.4
+// with statistics and loss; the biased form, with its 64-bit path, 28.9 with eight
+// and 21.1 with four). Workgroups of 16 wavefronts hold every form to 128
+// registers: biased with 16 experts a lane 39 of them (73 with statistics) live
+// in scratch (32768 x 1000 94 us). Of the scalar registers 16 (32) are kept in
+// lanes of vector ones at 6 experts a lane.
 template <bool BF, bool SIG, bool BIAS, bool STATS, int L, int NV>
 __global__ __launch_bounds__(64 * kMaxWaves)
 __attribute__((amdgpu_waves_per_eu(!BIAS && NV <= 6 ? 8 : NV <= 8 ? 4 : 2))) void k_route(RouteArgs a) {
@@ -1201,10 +1206,13 @@ __global__ __launch_bounds__(kRowThreads) void k_route_bwd_rows(RouteBwdArgs a, 
 
 // Whether rows go to groups of 16 lanes: a round of the selection there serves
 // four rows, but every slot takes one, where the wide form's cost hardly grows
-// with k. Narrow against wide: 32768 x 64 top-6 8.1 and 13.5 us, top-16 16.5
-// and 18.1 (512 rows top-6: 3.6 and 2.8); 131072 x 128 top-2 18.2 and 48.3,
-// top-8 46.6 and 47.6, top-16 84 and 63; backward 131072 x 128 33.9 and 45.4,
-// 32768 rows 12.2 and 14.0, 512 rows 4.6 and 3.1.
+// with k. Narrow against wide: 32768 x 64 top-6 8.3 and 12.7 us, top-16 16.6
+// and 19.6; 131072 x 128 top-2 18.1 and 44.1, top-4 27.2 and 43.7, top-8 45.6 and
+// 42.8, top-16 82.6 and 66.3; backward 131072 x 128 33.9 and 45.7, 32768 rows
+// 12.6 and 14.3. The rule does not look at few rows, which pay up to 1 us for it
+// (512 x 64 top-6 3.6 and 2.8, backward 3.5 and 2.9, biased 4.9 and 2.9; top-2
+// 2.7 and 2.8, 32 experts top-8 3.4 and 4.1) in a call of 7 us of the host's
+// time; the two meet at some 4096 rows.
 bool narrow(int64_t T, int E, int k, bool biased, bool backward) {
   if (k > kNarrowK || E > 128) return false;
   return E <= 64 || (backward ? T >= 32768 : !biased && k <= 4);
@@ -1212,9 +1220,9 @@ bool narrow(int64_t T, int E, int k, bool biased, bool backward) {
 
 // Whether rows go to single threads: rows enough to fill the device, few enough
 // experts for the registers. Single against narrow, at the bound and at 262144
-// rows: 8 experts top-2 2.5 and 2.5 us (4096 rows), 3.7 and 18.9; 64 experts
-// top-6 12.2 and 14.7 (65536 rows), 22.7 and 52.1; 8 experts backward 4.1 and
-// 4.3 (32768 rows), 8.7 and 16.9; biased 4.0 and 4.5, 7.8 and 21.1.
+// rows: 8 experts top-2 2.5 and 2.7 us (8192 rows), 3.7 and 18.9; 64 experts
+// top-6 11.7 and 14.4 (65536 rows), 22.2 and 49.7; 8 experts backward 4.2 and
+// 4.5 (32768 rows), 9.1 and 17.2; biased 4.0 and 4.5, 7.7 and 20.4.
 bool single(int64_t T, int E, int k, bool biased, bool backward) {
   if (k > kNarrowK || E > (biased || backward ? 8 : 64)) return false;
   return T >= (biased || backward ? 32768 : 1024 * E);
@@ -1232,9 +1240,9 @@ int lanes_experts(int E) {
 }
 
 // Wavefronts of a forward workgroup: few while the rows do not fill the device
-// (512 x 384 biased: 3.8 us with 4, 4.6 with 16), many when they do, for fewer
-// statistics partials (32768 x 384 with statistics and loss: 37.9 us with 4,
-// 25.8 with 16; without them 16.1 and 16.0).
+// (512 x 384 biased: 3.7 us with 4, 4.5 with 16), many when they do, for fewer
+// statistics partials (32768 x 384 with statistics and loss: 36.7 us with 4, 28.0
+// with 8, 25.7 with 16; without them 15.5, 15.5 and 15.3).
 int route_waves(int64_t T, int rows_per_wave) {
   const int64_t need = (T + rows_per_wave - 1) / rows_per_wave;
   return need <= 1024 ? 4 : need <= 2048 ? 8 : kMaxWaves;
@@ -1254,7 +1262,8 @@ struct RoutePlan {
 
 // Few enough rows for one workgroup, which then leaves the statistics
 // themselves: no partials and a launch fewer, of 3.3 us of the host's time
-// (with the loss, kernels alone: 1 x 384 8.8 -> 6.4 us, 512 x 8 7.1 -> 5.3).
+// (with the loss, kernels alone: 16 x 384 8.9 -> 6.5 us, 512 x 8 7.2 -> 5.3,
+// 1024 x 8 7.6 -> 6.3).
 // More rounds of one workgroup lose: 128 x 64 would take 11.2 us for 8.5, 4096 x
 // 8 12.5 for 8.0.
 bool alone_any(int64_t T, int E) { return T <= kMaxWaves || (E <= 8 && T <= 1024); }
