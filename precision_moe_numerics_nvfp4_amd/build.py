@@ -17,6 +17,7 @@ import argparse
 import concurrent.futures as cf
 import glob
 import os
+import shlex
 import shutil
 import subprocess
 import sys
@@ -56,18 +57,22 @@ def _compile(src):
 
 
 def _build_tensors():
-    """Host code against the torch that is installed: no GPU compiler."""
-    import torch
+    """Host code against the torch that is installed (without one there are no
+    tensors to look at): no GPU compiler."""
+    try:
+        import torch
+    except ImportError:
+        return
     top = os.path.dirname(torch.__file__)
     tmp = TENSORS_LIB + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-           "-fvisibility=hidden", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-isystem", os.path.join(top, "include"),
-           "-isystem", os.path.join(top, "include", "torch", "csrc", "api", "include"),
-           "-isystem", sysconfig.get_path("include"),
-           os.path.join(CSRC, "tensors.cpp"), "-o", tmp,
-           "-L" + os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    cmd = shlex.split(os.environ.get("CXX") or "g++") + [
+        "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        "-isystem", os.path.join(top, "include"),
+        "-isystem", os.path.join(top, "include", "torch", "csrc", "api", "include"),
+        "-isystem", sysconfig.get_path("include"),
+        os.path.join(CSRC, "tensors.cpp"), "-o", tmp,
+        "-L" + os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
