@@ -544,8 +544,9 @@ NVFP4MOE_API size_t nvfp4moe_route_workspace_size(int64_t T, int E);
  * counts [E + 1] int64, prob_sum [E] float32 (both or neither NULL):
  * counts[e] = selected pairs of expert e, counts[E] = tokens with at least one
  * expert; prob_sum[e] = sum over those tokens of s_te (SIGMOID: of
- * s_te / sum_i s_ti), sums of more than 16 rows formed in 64 bits and rounded
- * at the end. Both are overwritten, and the same inputs give the same bits. Sums over ranks may replace them before the calls below.
+ * s_te / sum_i s_ti), sums of more than 16 rows in 64 bits, rounded once for
+ * each workgroup and once at the end. Both are overwritten, and the same inputs
+ * give the same bits. Sums over ranks may replace them before the calls below.
  * workspace: nvfp4moe_route_workspace_size() bytes when counts is given (NULL
  * where that is 0).
  * Requires E <= 1024, k <= 64, k <= E, T * k < 2^31. T may be 0.
