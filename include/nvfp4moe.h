@@ -49,7 +49,10 @@
  *     NVFP4-backward variants, the one-pass dual dY quantizer,
  *     moe_permute_noalloc, and what trains around the layer: the router's
  *     selection with its statistics and backward, the balance loss, and the
- *     global gradient norm with clipping.
+ *     global gradient norm with clipping;
+ *   - MXFP4, the 4-bit format the matrix units multiply as it is stored:
+ *     quantizer, grouped forward GEMM, the backward's re-quantization; the
+ *     grouping without rows; and the whole expert layer for a few tokens.
  *
  * Formats (NVFP4 and MXFP8 as named on "Inkling 2 Small uses four-bit
  * training ..." (ai-primer), section "Block scales and per-token activations"):
@@ -62,6 +65,10 @@
  *   MXFP8  elems  uint8 [rows, cols]: OCP E4M3FN;
  *          scales uint8 [rows, cols/32]: E8M0 (2^(c-127)), one per 32
  *                 consecutive elements of a row.
+ *   MXFP4  codes  uint8 [rows, cols/2]: E2M1, in NVFP4's nibble order;
+ *          scales uint8 [rows, cols/32]: E8M0, as MXFP8's.
+ *          value = e2m1 * 2^(c-127). No call writes c = 255 (OCP's NaN); what
+ *          it gives where it is read is not defined.
  */
 #ifndef NVFP4MOE_H
 #define NVFP4MOE_H
@@ -100,6 +107,11 @@ enum nvfp4moe_layout { NVFP4MOE_LAYOUT_TRANSPOSED = 0, NVFP4MOE_LAYOUT_PER_GROUP
 
 /* Scores of the router (moe_route). */
 enum nvfp4moe_score { NVFP4MOE_SCORE_SOFTMAX = 0, NVFP4MOE_SCORE_SIGMOID = 1 };
+
+/* 4-bit format of weights, and the activation between the projections
+ * (moe_ffn_tokens): v, max(v, 0)^2, v / (1 + exp(-v)). */
+enum nvfp4moe_format { NVFP4MOE_NVFP4 = 0, NVFP4MOE_MXFP4 = 1 };
+enum nvfp4moe_act { NVFP4MOE_ACT_NONE = 0, NVFP4MOE_ACT_RELU2 = 1, NVFP4MOE_ACT_SILU = 2 };
 
 /* Version of this ABI (NVFP4MOE_ABI_VERSION): raised when a call that was there
  * changes. Calls that join leave it as it is; a library without them does not
@@ -613,6 +625,113 @@ NVFP4MOE_API int moe_grad_sumsq(const void* const* grads, const int* dtypes, con
 NVFP4MOE_API int moe_grad_clip(const void* const* grads, void* const* outs, const int* dtypes,
                   const int64_t* numels, int n, const double* sumsq, float max_norm, float* norm,
                   void* stream);
+
+/* ---------------------------------------------------------------------------
+ * MXFP4. The pages' recipe quantizes the forward to NVFP4, whose E4M3 block
+ * scales this GPU's block-scaled matrix instruction cannot take; MXFP4's powers
+ * of two it takes as they are. The calls below are the forward's and the
+ * backward's counterparts in MXFP4 of nvfp4_quantize, moe_fwd_grouped_gemm and
+ * mxfp8_requant_sr, whose rules (rounding, grouping, stochastic rounding,
+ * draws) are theirs; gradients go on in MXFP8 through moe_bwd_dgrad and
+ * moe_bwd_wgrad.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * x [rows, cols] float32 or bfloat16 -> codes [rows, cols/2], scales
+ * [rows, cols/32]. Block of 32 along a row: e = the smallest exponent with
+ * max|x_block| <= 6 * 2^e, clamped to [-127, 127]; scale byte e + 127;
+ * codes E2M1_RNE(x * 2^-e) (sign kept). From 3.5 * 2^126 on the nearest value
+ * is 2^128, which is not a float32.
+ * n_live (device, NULL: all rows): only rows r < *n_live are quantized, later
+ * rows of the outputs untouched.
+ * Requires cols % 32 == 0, rows * cols < 2^35.
+ */
+NVFP4MOE_API int mxfp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols,
+                   const int64_t* n_live, uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * Back to values: out [rows, cols] float32 or bfloat16 = element * 2^(c-127),
+ * of MXFP4 codes [rows, cols/2] or MXFP8 elements [rows, cols], scales
+ * [rows, cols/32]. Exact in float32, in bfloat16 too but for MXFP8 values below
+ * 2^-130 (rounded to nearest even). Requires cols % 32 == 0, rows * cols < 2^35.
+ */
+NVFP4MOE_API int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                     int64_t cols, void* out, int out_dtype, void* stream);
+NVFP4MOE_API int mxfp8_dequantize(const uint8_t* e4m3, const uint8_t* e8m0, int64_t rows, int64_t cols,
+                     void* out, int out_dtype, void* stream);
+
+/*
+ * moe_permute's grouping without its gather: offsets, padded_offsets, row_token,
+ * row_slot and pair_row (may be NULL) as there, no rows moved (the calls below
+ * read rows through row_token). Workspace and bounds as moe_permute's.
+ */
+NVFP4MOE_API int moe_group(const int32_t* topk_ids, int64_t T, int k, int e0, int n_local,
+              int64_t* offsets, int64_t* padded_offsets, int32_t* row_token, int32_t* row_slot,
+              int32_t* pair_row, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * MXFP4 forward grouped GEMM.
+ * a_*: activations MXFP4 [a_rows, K]; row_token[m_cap] int32 or NULL: the row
+ *   of a_* that row r < offsets[G] reads (NULL: row r itself, a_rows >= m_cap).
+ *   Entries outside [0, a_rows) read some row of a_*; none past it is touched.
+ * b_*: W MXFP4 stored [G, N, K]; offsets[G+1] (device).
+ * y[r, n] = sum_k a[row, k] * b[g, n, k] for rows r of group g; y [m_cap, N]
+ *   float32 or bfloat16 (round to nearest even). Products and the sums of a
+ *   block of 32 are exact, the blocks are added in float32. Rows >= offsets[G]
+ *   untouched. Requires N % 128 == 0, K % 128 == 0, K < 2^23, G <= 4095,
+ *   m_cap < 2^31, a_rows < 2^31, scales 4-byte aligned.
+ */
+NVFP4MOE_API int moe_fwd_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a_rows,
+                               const int32_t* row_token, const uint8_t* b_codes,
+                               const uint8_t* b_scales, const int64_t* offsets, int G,
+                               int64_t m_cap, int64_t N, int64_t K, void* y, int y_dtype,
+                               void* stream);
+
+/*
+ * mxfp8_requant_sr of a saved MXFP4 tensor [rows, cols] (values are exact, so
+ * only the stochastic rounding rounds). rows_per_group == 0: activations, out
+ * [cols, P]; > 0: weights, one block per group (offsets = padded_offsets =
+ * {0, rows_per_group, ...}), both as mxfp8_requant_sr writes them.
+ * row_token int32 or NULL (activations only): the row of codes/scales that
+ * grouped row r reads; entries outside [0, rows) are taken as rows of zeros.
+ * Requires cols % 128 == 0, P % 32 == 0.
+ */
+NVFP4MOE_API int mxfp8_requant_sr_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                           int64_t cols, const int32_t* row_token, int64_t rows_per_group,
+                           const int64_t* offsets, const int64_t* padded_offsets, int G, int64_t P,
+                           uint64_t seed, uint32_t tag, uint8_t* out_e4m3, uint8_t* out_e8m0,
+                           void* stream);
+
+/* Bytes of device workspace moe_ffn_tokens needs (0 for sizes it refuses). */
+NVFP4MOE_API size_t nvfp4moe_ffn_tokens_workspace_size(int64_t T, int k, int64_t F);
+
+/*
+ * The whole expert layer for a few tokens (decoding): routing, both
+ * projections, the weighted sum.
+ *
+ * x [T, K] bfloat16 (not quantized); logits, score, renorm, scale, bias,
+ * token_mask, topk_ids, gate: as moe_route, whose results topk_ids and gate
+ * are. Weights of the local experts [e0, e0 + n_local) in `format`: NVFP4 with
+ * an outer scale per expert (w*_outer [n_local]) or MXFP4 (w*_outer NULL);
+ * w1 [n_local, F, K], or gated != 0 [n_local, 2 F, K] (an expert's first F
+ * rows make a, its last F rows b); w2 [n_local, K, F].
+ *   h = act(W1[e] x[t]), gated: act(a) * b
+ *   out[t] = sum over slots j with a local expert of gate[t, j] * W2[e] h
+ * out [T, K] bfloat16 or float32, zero for a token without local experts.
+ * Products are exact, sums float32; h, times its gate, is carried in 16
+ * significant bits.
+ * workspace: nvfp4moe_ffn_tokens_workspace_size() bytes, one call's at a time.
+ * Requires T <= 64, k <= 16, T * k <= 512, k <= E <= 1024, n_local <= 1024,
+ * K % 128 == 0, F % 128 == 0, K, F <= 2^20; x, codes, scales, out and
+ * workspace 16-byte aligned. T may be 0.
+ */
+NVFP4MOE_API int moe_ffn_tokens(const void* x, const void* logits, int logits_dtype, int64_t T, int E, int k,
+                   int score, int renorm, float scale, const float* bias,
+                   const uint8_t* token_mask, int format, const uint8_t* w1_codes,
+                   const uint8_t* w1_scales, const float* w1_outer, const uint8_t* w2_codes,
+                   const uint8_t* w2_scales, const float* w2_outer, int e0, int n_local, int64_t K,
+                   int64_t F, int act, int gated, int32_t* topk_ids, float* gate, void* out,
+                   int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -33,7 +33,7 @@ examples or independent library routines. Philox4x32-10 is pinned against the
 rocRAND source header's host implementation and known-answer vectors.
 """
 
-from . import formats, philox, nvfp4, mxfp8, permute, gemm, ffn, nvfp4_bwd, route  # noqa: F401
+from . import formats, philox, nvfp4, mxfp8, permute, gemm, ffn, nvfp4_bwd, route, mxfp4  # noqa: F401
 
 __all__ = ["formats", "philox", "nvfp4", "mxfp8", "permute", "gemm", "ffn", "nvfp4_bwd",
-           "route"]
+           "route", "mxfp4"]

@@ -15,6 +15,7 @@ from .binding import (  # noqa: F401
     NVFP4MOE_F32,
     Nvfp4moeError,
     abi_version,
+    ffn_tokens_workspace_size,
     grad_workspace_size,
     lib,
     moe_balance_loss,
@@ -24,18 +25,25 @@ from .binding import (  # noqa: F401
     moe_combine_bwd,
     moe_fwd_grouped_gemm,
     moe_bwd_wgrad_nvfp4,
+    moe_ffn_tokens,
+    moe_fwd_grouped_gemm_mxfp4,
     moe_fwd_grouped_gemm_mxfp8,
     moe_grad_clip,
     moe_grad_sumsq,
+    moe_group,
     moe_padded_offsets,
     moe_permute,
     moe_permute_noalloc,
     moe_route,
     moe_route_bwd,
+    mxfp4_dequantize,
+    mxfp4_quantize,
+    mxfp8_dequantize,
     mxfp8_gather_rows,
     mxfp8_quantize,
     mxfp8_quantize_dual,
     mxfp8_requant_sr,
+    mxfp8_requant_sr_mxfp4,
     nvfp4_quantize,
     nvfp4_quantize_live,
     nvfp4_quantize_sr,

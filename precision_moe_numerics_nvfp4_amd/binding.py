@@ -18,6 +18,8 @@ _LAYOUT_TRANSPOSED, _LAYOUT_PER_GROUP = 0, 1
 _ROWWISE, _COLWISE_GROUPED = 0, 1
 _EINVAL, _EUNSUPPORTED = 1, 2
 _SCORES = {"softmax": 0, "sigmoid": 1}
+_FORMATS = {3: 0, 2: 1}                 # parts of a weight: NVFP4 (with outer scales), MXFP4
+_ACTS = {"none": 0, "relu2": 1, "silu": 2}
 
 _c_i64 = ctypes.c_int64
 _c_int = ctypes.c_int
@@ -73,6 +75,18 @@ SIGNATURES = {
     "nvfp4moe_grad_workspace_size": ([_p, _c_int], _c_size),
     "moe_grad_sumsq": ([_p, _p, _p, _c_int, _p, _p, _c_size, _p], _c_int),
     "moe_grad_clip": ([_p, _p, _p, _p, _c_int, _p, _c_f32, _p, _p], _c_int),
+    "mxfp4_quantize": ([_p, _c_int, _c_i64, _c_i64, _p, _p, _p, _p], _c_int),
+    "mxfp4_dequantize": ([_p, _p, _c_i64, _c_i64, _p, _c_int, _p], _c_int),
+    "mxfp8_dequantize": ([_p, _p, _c_i64, _c_i64, _p, _c_int, _p], _c_int),
+    "moe_group": ([_p, _c_i64, _c_int, _c_int, _c_int, _p, _p, _p, _p, _p, _p, _c_size, _p], _c_int),
+    "moe_fwd_grouped_gemm_mxfp4": ([_p, _p, _c_i64, _p, _p, _p, _p, _c_int, _c_i64, _c_i64, _c_i64,
+                                    _p, _c_int, _p], _c_int),
+    "mxfp8_requant_sr_mxfp4": ([_p, _p, _c_i64, _c_i64, _p, _c_i64, _p, _p, _c_int, _c_i64, _c_u64,
+                                _c_u32, _p, _p, _p], _c_int),
+    "nvfp4moe_ffn_tokens_workspace_size": ([_c_i64, _c_int, _c_i64], _c_size),
+    "moe_ffn_tokens": ([_p, _p, _c_int, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_f32, _p, _p,
+                        _c_int, _p, _p, _p, _p, _p, _p, _c_int, _c_int, _c_i64, _c_i64, _c_int,
+                        _c_int, _p, _p, _p, _c_int, _p, _c_size, _p], _c_int),
 }
 
 _LIB = None
@@ -955,3 +969,271 @@ def moe_grad_clip(grads, sumsq, max_norm, outs=None, norm=None):
             _on(sumsq, "sumsq", torch.float64, (1,), dev), _number(max_norm, "max_norm"),
             _buf(res, "norm", torch.float32, (1,), dev))
     return res["norm"]
+
+
+# ------------------------------------------ MXFP4, and the layer for a few tokens
+
+def _c_size_of(v, name, bits=64):
+    """A whole number that the C argument holds."""
+    v = _number(v, name, int)
+    if not -(1 << (bits - 1)) <= v < 1 << (bits - 1):
+        raise ValueError(f"{name} is out of range (got {v})")
+    return v
+
+
+def _mxfp4_pair(codes, scales, name, dev):
+    """Addresses, rows and columns of an MXFP4 tensor (any leading dimensions)."""
+    torch = _torch()
+    _dev(codes, f"{name} codes", torch.uint8)
+    if codes.dim() < 2:
+        raise ValueError(f"{name} codes must have at least 2 dimensions (got {codes.dim()})")
+    half = codes.shape[-1]
+    rows = codes.numel() // half if half else 0
+    if half % 16:
+        raise ValueError(f"{name} codes must hold whole blocks of 32 (got {2 * half} columns)")
+    if codes.device != dev:
+        raise ValueError(f"{name} codes must be on {dev} (got {codes.device})")
+    _dev(scales, f"{name} scales", torch.uint8)
+    if scales.device != dev or scales.numel() != rows * (half // 16) or scales.shape[-1] != half // 16:
+        raise ValueError(f"{name} scales must hold {half // 16} bytes for each of {rows} rows on {dev} "
+                         f"(got {tuple(scales.shape)} on {scales.device})")
+    return codes.data_ptr(), scales.data_ptr(), rows, 2 * half
+
+
+def mxfp4_quantize(x, offsets=None, codes=None, scales=None):
+    """x [rows, cols] float32|bfloat16 -> MXFP4 (codes [rows, cols/2] u8, scales
+    [rows, cols/32] u8). With ``offsets`` (moe_group's) only the routed rows
+    r < offsets[-1]; later rows of the outputs untouched."""
+    torch = _torch()
+    _dev(x, "x", ndim=2)
+    rows, cols = x.shape
+    dev, live = x.device, None
+    if cols % 32:
+        _check("mxfp4_quantize", _EUNSUPPORTED)
+    if offsets is not None:
+        _dev(offsets, "offsets", torch.int64, 1)
+        if offsets.device != dev or offsets.numel() < 1:
+            raise ValueError(f"offsets must hold a row count on {dev}")
+        live = offsets.data_ptr() + 8 * (offsets.numel() - 1)
+    o = dict(codes=codes, scales=scales)
+    _launch(dev, "mxfp4_quantize", x.data_ptr(), _in_dtype(x), rows, cols, live,
+            _buf(o, "codes", torch.uint8, (rows, cols // 2), dev),
+            _buf(o, "scales", torch.uint8, (rows, cols // 32), dev))
+    return o["codes"], o["scales"]
+
+
+def _dequantize(fn, q, scales, rows, cols, dev, out_dtype, out):
+    torch = _torch()
+    o = {"out": out}
+    dtype = out.dtype if out is not None else (out_dtype or torch.float32)
+    code = _out_dtype(dtype)
+    _launch(dev, fn, q, scales, rows, cols, _buf(o, "out", dtype, (rows, cols), dev), code)
+    return o["out"]
+
+
+def mxfp4_dequantize(codes, scales, out_dtype=None, out=None):
+    """Values [rows, cols] (float32|bfloat16) of MXFP4 codes [rows, cols/2]."""
+    _dev(codes, "codes", ndim=2)
+    q, e, rows, cols = _mxfp4_pair(codes, scales, "mxfp4", codes.device)
+    return _dequantize("mxfp4_dequantize", q, e, rows, cols, codes.device, out_dtype, out)
+
+
+def mxfp8_dequantize(e4m3, e8m0, out_dtype=None, out=None):
+    """Values [rows, cols] (float32|bfloat16) of MXFP8 elements [rows, cols]."""
+    torch = _torch()
+    _dev(e4m3, "e4m3", torch.uint8, 2)
+    rows, cols = e4m3.shape
+    if cols % 32:
+        _check("mxfp8_dequantize", _EUNSUPPORTED)
+    e = _on(e8m0, "e8m0", torch.uint8, (rows, cols // 32), e4m3.device)
+    return _dequantize("mxfp8_dequantize", e4m3.data_ptr(), e, rows, cols, e4m3.device, out_dtype, out)
+
+
+def moe_group(topk_ids, e0, n_local, workspace=None, out=None):
+    """moe_permute's grouping without moving rows: a dict with offsets,
+    padded_offsets (int64 [n_local+1]), row_token, row_slot (int32 [T*k]; rows
+    >= offsets[-1] untouched) and pair_row (int32 [T, k]; an ``out`` dict
+    without it asks for none)."""
+    torch = _torch()
+    _dev(topk_ids, "topk_ids", torch.int32, 2)
+    T, k = topk_ids.shape
+    e0, n_local = _c_size_of(e0, "e0", 32), _c_size_of(n_local, "n_local", 32)
+    if n_local < 1:
+        _check("moe_group", _EINVAL)
+    if n_local > 1024 or k > 64 or T * k > 0x7FFFFFFF:
+        _check("moe_group", _EUNSUPPORTED)
+    dev, i32, i64 = topk_ids.device, torch.int32, torch.int64
+    o = dict(out or {})
+    if out is None:
+        o["pair_row"] = torch.empty((T, k), dtype=i32, device=dev)
+    pair = o.get("pair_row")
+    ws, ws_bytes = _workspace(workspace, permute_workspace_size(T, k, n_local), dev)
+    _launch(dev, "moe_group", topk_ids.data_ptr(), T, k, e0, n_local,
+            _buf(o, "offsets", i64, (n_local + 1,), dev), _buf(o, "padded_offsets", i64, (n_local + 1,), dev),
+            _buf(o, "row_token", i32, (T * k,), dev), _buf(o, "row_slot", i32, (T * k,), dev),
+            None if pair is None else _on(pair, "pair_row", i32, (T, k), dev), ws.data_ptr(), ws_bytes)
+    return o
+
+
+def _row_map(row_token, dev):
+    """Address and length of a map from grouped rows to source rows."""
+    _dev(row_token, "row_token", _torch().int32, 1)
+    if row_token.device != dev:
+        raise ValueError(f"row_token must be on {dev} (got {row_token.device})")
+    return row_token.data_ptr(), row_token.shape[0]
+
+
+def moe_fwd_grouped_gemm_mxfp4(a_codes, a_scales, b_codes, b_scales, offsets, row_token=None,
+                               out_dtype=None, y=None):
+    """y [m_cap, N] = grouped MXFP4 GEMM of activations [rows, K] with weights
+    [G*N, K] or [G, N, K]; offsets int64 [G+1] on the device. With ``row_token``
+    (int32 [m_cap], moe_group's) row r reads activation row row_token[r], else
+    row r. Rows >= offsets[-1] of y are untouched."""
+    torch = _torch()
+    _dev(a_codes, "a codes", ndim=2)
+    dev = a_codes.device
+    ac, as_, rows, K = _mxfp4_pair(a_codes, a_scales, "a", dev)
+    bc, bs, b_rows, b_cols = _mxfp4_pair(b_codes, b_scales, "b", dev)
+    _dev(offsets, "offsets", torch.int64, 1)
+    G = offsets.shape[0] - 1
+    if offsets.device != dev or G < 0:
+        raise ValueError(f"offsets must hold G + 1 row counts on {dev}")
+    if b_cols != K or (b_rows % G if G else b_rows):
+        raise ValueError(f"b must hold G = {G} weights of {K} columns (got {b_rows} rows of {b_cols})")
+    N = b_rows // G if G else 0
+    tok, m_cap = (None, rows) if row_token is None else _row_map(row_token, dev)
+    o = {"y": y}
+    dtype = y.dtype if y is not None else (out_dtype or torch.float32)
+    code = _out_dtype(dtype)
+    _launch(dev, "moe_fwd_grouped_gemm_mxfp4", ac, as_, rows, tok, bc, bs, offsets.data_ptr(), G, m_cap,
+            N, K, _buf(o, "y", dtype, (m_cap, N), dev), code)
+    return o["y"]
+
+
+def mxfp8_requant_sr_mxfp4(codes, scales, offsets, padded_offsets, P, seed, tag, rows_per_group=None,
+                           row_token=None, out=None, out_e8=None):
+    """Saved MXFP4 [rows, cols] -> MXFP8 with stochastic rounding, grouped
+    transpose, as mxfp8_requant_sr: activations [cols, P] (+ E8M0 [cols, P/32]),
+    read through ``row_token`` where it is given; weights (rows_per_group)
+    per-expert blocks [G * cols, rows_per_group], P = G * rows_per_group."""
+    torch = _torch()
+    _dev(codes, "codes", ndim=2)
+    dev = codes.device
+    q, e, rows, cols = _mxfp4_pair(codes, scales, "mxfp4", dev)
+    _dev(offsets, "offsets", torch.int64, 1)
+    G = offsets.shape[0] - 1
+    if offsets.device != dev or G < 0:
+        raise ValueError(f"offsets must hold G + 1 row counts on {dev}")
+    P = _c_size_of(P, "P")
+    if P < 0 or P % 32:
+        _check("mxfp8_requant_sr_mxfp4", _EINVAL if P < 0 else _EUNSUPPORTED)
+    tok, n = (None, rows) if row_token is None else _row_map(row_token, dev)
+    if rows_per_group is None:
+        rpg, shape = 0, (cols, P)
+    else:
+        rpg = _c_size_of(rows_per_group, "rows_per_group")
+        if rpg < 1 or P != G * rpg or rows != P:
+            raise ValueError("mxfp8_requant_sr_mxfp4: weights need P == rows == G * rows_per_group")
+        if tok is not None:
+            raise ValueError("mxfp8_requant_sr_mxfp4: row_token goes with activations only")
+        if rpg % 32:
+            _check("mxfp8_requant_sr_mxfp4", _EUNSUPPORTED)
+        shape = (G * cols, rpg)
+    o = dict(out=out, out_e8=out_e8)
+    _launch(dev, "mxfp8_requant_sr_mxfp4", q, e, rows, cols, tok, rpg, offsets.data_ptr(),
+            _on(padded_offsets, "padded_offsets", torch.int64, (G + 1,), dev), G, P,
+            int(seed) & 0xFFFFFFFFFFFFFFFF, int(tag) & 0xFFFFFFFF,
+            _buf(o, "out", torch.uint8, shape, dev),
+            _buf(o, "out_e8", torch.uint8, (shape[0], shape[1] // 32), dev))
+    return o["out"], o["out_e8"]
+
+
+@functools.lru_cache(maxsize=256)
+def ffn_tokens_workspace_size(T, k, F):
+    return int(lib().nvfp4moe_ffn_tokens_workspace_size(int(T), int(k), int(F)))
+
+
+def _weight(w, name, dev):
+    """Parts of a 4-bit weight: MXFP4 (codes, scales) or NVFP4 (codes, scales,
+    outer [n_local]), its addresses, rows and columns."""
+    torch = _torch()
+    if not isinstance(w, (tuple, list)) or len(w) not in _FORMATS:
+        raise ValueError(f"{name} must be (codes, scales) in MXFP4 or (codes, scales, outer) in NVFP4")
+    codes, scales = w[0], w[1]
+    _dev(codes, f"{name} codes", torch.uint8)
+    cols = 2 * codes.shape[-1] if codes.dim() >= 2 else 0
+    if codes.dim() < 2 or codes.device != dev or cols == 0:
+        raise ValueError(f"{name} codes must have rows of codes on {dev} "
+                         f"(got {tuple(codes.shape)} on {codes.device})")
+    rows, block = codes.numel() // (cols // 2), 32 if len(w) == 2 else 16
+    _dev(scales, f"{name} scales", torch.uint8)
+    if cols % 32 or scales.device != dev or scales.shape[-1] != cols // block or \
+            scales.numel() != rows * (cols // block):
+        raise ValueError(f"{name} scales must hold a byte for {block} codes of each of {rows} rows on {dev} "
+                         f"(got {tuple(scales.shape)} on {scales.device})")
+    outer = None
+    if len(w) == 3:
+        _dev(w[2], f"{name} outer", torch.float32, 1)
+        if w[2].device != dev:
+            raise ValueError(f"{name} outer must be on {dev} (got {w[2].device})")
+        outer = w[2].data_ptr()
+    return codes.data_ptr(), scales.data_ptr(), outer, rows, cols
+
+
+def moe_ffn_tokens(x, logits, k, w1, w2, act="silu", gated=False, score="softmax", renorm=True,
+                   scale=1.0, bias=None, token_mask=None, e0=0, out_dtype=None, workspace=None,
+                   out=None):
+    """The whole expert layer for up to 64 tokens: x bf16 [T, K] and logits
+    [T, E] (bf16|f32) -> a dict with out [T, K] (bf16, or ``out_dtype``
+    float32), topk_ids int32 [T, k] and gate f32 [T, k] (moe_route's; its
+    options too).
+
+    w1 [n_local*F, K] (gated: [n_local*2F, K], an expert's first F rows go
+    through ``act``, its last F multiply them) and w2 [n_local*K, F], each
+    (codes, scales) in MXFP4 or (codes, scales, outer) in NVFP4, of the experts
+    [e0, e0+n_local). act 'none', 'relu2' or 'silu'. ``out`` may hold any of the
+    results' buffers; ``workspace`` ffn_tokens_workspace_size(T, k, F) bytes,
+    of one call at a time."""
+    torch = _torch()
+    _dev(x, "x", torch.bfloat16, 2)
+    T, K = x.shape
+    dev = x.device
+    _dev(logits, "logits", ndim=2)
+    if logits.shape[0] != T or logits.device != dev:
+        raise ValueError(f"logits must have {T} rows on {dev} (got {tuple(logits.shape)} on {logits.device})")
+    E = logits.shape[1]
+    k, e0 = _number(k, "k", int), _c_size_of(e0, "e0", 32)
+    if act not in _ACTS:
+        raise ValueError(f"act must be 'none', 'relu2' or 'silu' (got {act!r})")
+    c1, s1, o1, rows1, cols1 = _weight(w1, "w1", dev)
+    c2, s2, o2, rows2, F = _weight(w2, "w2", dev)
+    if len(w1) != len(w2):
+        raise ValueError("w1 and w2 must have the same format")
+    n_local = rows2 // K if K else 0
+    if cols1 != K or n_local * K != rows2 or rows1 != n_local * F * (2 if gated else 1):
+        raise ValueError(f"w1 must be [n*{'2F' if gated else 'F'}, {K}] and w2 [n*{K}, F] "
+                         f"(got [{rows1}, {cols1}] and [{rows2}, {F}])")
+    if o1 is not None and (w1[2].shape[0] != n_local or w2[2].shape[0] != n_local):
+        raise ValueError(f"outer scales must have shape ({n_local},)")
+    if E < 1 or k < 1 or n_local < 1:
+        _check("moe_ffn_tokens", _EINVAL)
+    if T > 64 or k > 16 or T * k > 512 or k > E or E > 1024 or n_local > 1024:
+        _check("moe_ffn_tokens", _EUNSUPPORTED)
+    o = {} if out is None else {n: out[n] for n in ("out", "topk_ids", "gate") if n in out}
+    dtype = o["out"].dtype if o.get("out") is not None else (out_dtype or torch.bfloat16)
+    code = _out_dtype(dtype)
+    y = _buf(o, "out", dtype, (T, K), dev)
+    ids = _buf(o, "topk_ids", torch.int32, (T, k), dev)
+    gate = _buf(o, "gate", torch.float32, (T, k), dev)
+    if bias is not None:
+        bias = _on(bias, "bias", torch.float32, (E,), dev)
+    if token_mask is not None:
+        if isinstance(token_mask, torch.Tensor) and token_mask.dtype == torch.bool:
+            token_mask = token_mask.view(torch.uint8)
+        token_mask = _on(token_mask, "token_mask", torch.uint8, (T,), dev)
+    ws, ws_bytes = _workspace(workspace, ffn_tokens_workspace_size(T, k, F), dev)
+    _launch(dev, "moe_ffn_tokens", x.data_ptr(), logits.data_ptr(), _in_dtype(logits), T, E, k,
+            _score(score), 1 if renorm else 0, _number(scale, "scale"), bias, token_mask,
+            _FORMATS[len(w1)], c1, s1, o1, c2, s2, o2, e0, n_local, K, F, _ACTS[act],
+            1 if gated else 0, ids, gate, y, code, None if ws is None else ws.data_ptr(), ws_bytes)
+    return o

@@ -58,6 +58,25 @@ int grad_list_status(const void* const* grads, void* const* outs, const int* dty
   return NVFP4MOE_OK;
 }
 
+// A launch holds less than 2^32 threads: the quantizers take 16 elements a
+// thread at least, the tiled kernels 256 threads a tile.
+constexpr int64_t kMaxElems = (int64_t)1 << 35;
+constexpr int64_t kMaxTiles = (int64_t)1 << 23;
+// Widths of the few-token layer.
+constexpr int64_t kMaxTokensWidth = (int64_t)1 << 20;
+
+int mx_dequantize(bool mx8, const uint8_t* q, const uint8_t* e8, int64_t rows, int64_t cols,
+                  void* out, int out_dtype, void* stream) {
+  REQUIRE(rows >= 0 && cols >= 0, NVFP4MOE_EINVAL);
+  REQUIRE(out_dtype == NVFP4MOE_F32 || out_dtype == NVFP4MOE_BF16, NVFP4MOE_EINVAL);
+  if (rows == 0) return NVFP4MOE_OK;
+  REQUIRE(q && e8 && out, NVFP4MOE_EINVAL);
+  REQUIRE(cols > 0 && cols % 32 == 0 && rows < kMaxElems / cols, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(aligned16(q) && aligned16(e8) && aligned16(out), NVFP4MOE_EUNSUPPORTED);
+  return hip_status(launch_mx_dequantize(mx8, q, e8, rows, cols, out, out_dtype == NVFP4MOE_BF16,
+                                         as_stream(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -534,6 +553,155 @@ int moe_grad_clip(const void* const* grads, void* const* outs, const int* dtypes
   REQUIRE(aligned(sumsq, 8) && aligned(norm, 4), NVFP4MOE_EUNSUPPORTED);
   return hip_status(launch_grad_clip(grads, outs, dtypes, numels, n, sumsq, max_norm, norm,
                                      as_stream(stream)));
+}
+
+int mxfp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, const int64_t* n_live,
+                   uint8_t* codes, uint8_t* scales, void* stream) {
+  REQUIRE(rows >= 0 && cols >= 0, NVFP4MOE_EINVAL);
+  REQUIRE(x_dtype == NVFP4MOE_F32 || x_dtype == NVFP4MOE_BF16, NVFP4MOE_EINVAL);
+  if (rows == 0) return NVFP4MOE_OK;
+  REQUIRE(x && codes && scales, NVFP4MOE_EINVAL);
+  REQUIRE(cols > 0 && cols % 32 == 0 && rows < kMaxElems / cols, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(aligned16(x) && aligned16(codes) && aligned16(scales) && aligned(n_live, 8),
+          NVFP4MOE_EUNSUPPORTED);
+  return hip_status(launch_mxfp4_quantize(x, x_dtype == NVFP4MOE_BF16, rows, cols, n_live, codes,
+                                          scales, as_stream(stream)));
+}
+
+int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                     void* out, int out_dtype, void* stream) {
+  return mx_dequantize(false, codes, scales, rows, cols, out, out_dtype, stream);
+}
+
+int mxfp8_dequantize(const uint8_t* e4m3, const uint8_t* e8m0, int64_t rows, int64_t cols,
+                     void* out, int out_dtype, void* stream) {
+  return mx_dequantize(true, e4m3, e8m0, rows, cols, out, out_dtype, stream);
+}
+
+int moe_group(const int32_t* topk_ids, int64_t T, int k, int e0, int n_local, int64_t* offsets,
+              int64_t* padded_offsets, int32_t* row_token, int32_t* row_slot, int32_t* pair_row,
+              void* workspace, size_t workspace_bytes, void* stream) {
+  REQUIRE(T >= 0 && k > 0 && n_local > 0, NVFP4MOE_EINVAL);
+  REQUIRE(offsets && padded_offsets && workspace, NVFP4MOE_EINVAL);
+  if (T > 0) REQUIRE(topk_ids && row_token && row_slot, NVFP4MOE_EINVAL);
+  REQUIRE(n_local <= 1024 && k <= 64, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(T < ((int64_t)1 << 31) / k, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(workspace_bytes >= permute_workspace_bytes(T, k, n_local), NVFP4MOE_EWORKSPACE);
+  REQUIRE(aligned16(workspace), NVFP4MOE_EUNSUPPORTED);
+  return hip_status(launch_permute(topk_ids, T, k, e0, n_local, nullptr, nullptr, nullptr, 0,
+                                   offsets, padded_offsets, row_token, row_slot, pair_row, nullptr,
+                                   nullptr, nullptr, workspace, as_stream(stream)));
+}
+
+int moe_fwd_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a_rows,
+                               const int32_t* row_token, const uint8_t* b_codes,
+                               const uint8_t* b_scales, const int64_t* offsets, int G,
+                               int64_t m_cap, int64_t N, int64_t K, void* y, int y_dtype,
+                               void* stream) {
+  REQUIRE(G >= 0 && m_cap >= 0 && N >= 0 && K >= 0 && a_rows >= 0, NVFP4MOE_EINVAL);
+  REQUIRE(y_dtype == NVFP4MOE_F32 || y_dtype == NVFP4MOE_BF16, NVFP4MOE_EINVAL);
+  if (G == 0 || m_cap == 0 || N == 0 || a_rows == 0) return NVFP4MOE_OK;
+  REQUIRE(a_codes && a_scales && b_codes && b_scales && offsets && y, NVFP4MOE_EINVAL);
+  REQUIRE(row_token || a_rows >= m_cap, NVFP4MOE_EINVAL);
+  REQUIRE(N % 128 == 0 && K % 128 == 0 && K > 0 && K < (int64_t)1 << 23, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(G <= 4095 && m_cap < (int64_t)1 << 31 && a_rows < (int64_t)1 << 31, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(N / 128 < kMaxTiles / (m_cap / 32 + G + 1), NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(aligned16(a_codes) && aligned16(b_codes) && aligned16(y) && aligned(a_scales, 4) &&
+              aligned(b_scales, 4) && aligned(row_token, 4) && aligned(offsets, 8),
+          NVFP4MOE_EUNSUPPORTED);
+  return hip_status(launch_fwd_mxfp4(a_codes, a_scales, a_rows, row_token, b_codes, b_scales,
+                                     offsets, G, m_cap, N, K, y, y_dtype == NVFP4MOE_BF16,
+                                     as_stream(stream)));
+}
+
+int mxfp8_requant_sr_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                           const int32_t* row_token, int64_t rows_per_group,
+                           const int64_t* offsets, const int64_t* padded_offsets, int G, int64_t P,
+                           uint64_t seed, uint32_t tag, uint8_t* out_e4m3, uint8_t* out_e8m0,
+                           void* stream) {
+  REQUIRE(rows >= 0 && cols >= 0 && G >= 0 && P >= 0 && rows_per_group >= 0, NVFP4MOE_EINVAL);
+  REQUIRE(rows_per_group == 0 || !row_token, NVFP4MOE_EINVAL);
+  if (G == 0 || P == 0 || cols == 0) return NVFP4MOE_OK;
+  REQUIRE(offsets && padded_offsets && out_e4m3 && out_e8m0, NVFP4MOE_EINVAL);
+  if (rows > 0) REQUIRE(codes && scales, NVFP4MOE_EINVAL);
+  REQUIRE(cols % 128 == 0 && P % 32 == 0, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(P / 128 + 1 < kMaxTiles / (cols / 128), NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(aligned16(codes) && aligned16(out_e4m3) && aligned(scales, 4) && aligned(row_token, 4),
+          NVFP4MOE_EUNSUPPORTED);
+  return hip_status(launch_requant_sr_mxfp4(codes, scales, rows, cols, row_token, offsets,
+                                            padded_offsets, G, P, rows_per_group > 0, seed, tag,
+                                            out_e4m3, out_e8m0, as_stream(stream)));
+}
+
+size_t nvfp4moe_ffn_tokens_workspace_size(int64_t T, int k, int64_t F) {
+  if (T < 0 || k <= 0 || F < 0 || T > kTokensMaxT || k > kTokensMaxK || T * k > kTokensMaxPairs ||
+      F > kMaxTokensWidth)
+    return 0;
+  return tokens_workspace_bytes(T, k, F);
+}
+
+int moe_ffn_tokens(const void* x, const void* logits, int logits_dtype, int64_t T, int E, int k,
+                   int score, int renorm, float scale, const float* bias,
+                   const uint8_t* token_mask, int format, const uint8_t* w1_codes,
+                   const uint8_t* w1_scales, const float* w1_outer, const uint8_t* w2_codes,
+                   const uint8_t* w2_scales, const float* w2_outer, int e0, int n_local, int64_t K,
+                   int64_t F, int act, int gated, int32_t* topk_ids, float* gate, void* out,
+                   int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  REQUIRE(T >= 0 && E > 0 && k > 0 && n_local > 0 && K > 0 && F > 0, NVFP4MOE_EINVAL);
+  REQUIRE(logits_dtype == NVFP4MOE_F32 || logits_dtype == NVFP4MOE_BF16, NVFP4MOE_EINVAL);
+  REQUIRE(out_dtype == NVFP4MOE_F32 || out_dtype == NVFP4MOE_BF16, NVFP4MOE_EINVAL);
+  REQUIRE(score == NVFP4MOE_SCORE_SOFTMAX || score == NVFP4MOE_SCORE_SIGMOID, NVFP4MOE_EINVAL);
+  REQUIRE(format == NVFP4MOE_NVFP4 || format == NVFP4MOE_MXFP4, NVFP4MOE_EINVAL);
+  REQUIRE(act >= NVFP4MOE_ACT_NONE && act <= NVFP4MOE_ACT_SILU, NVFP4MOE_EINVAL);
+  REQUIRE(T <= kTokensMaxT && k <= kTokensMaxK && T * k <= kTokensMaxPairs && k <= E && E <= 1024 &&
+              n_local <= 1024,
+          NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(K % 128 == 0 && F % 128 == 0 && K <= kMaxTokensWidth && F <= kMaxTokensWidth,
+          NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(!bias || score == NVFP4MOE_SCORE_SIGMOID, NVFP4MOE_EUNSUPPORTED);
+  if (T == 0) return NVFP4MOE_OK;
+  const bool nv = format == NVFP4MOE_NVFP4;
+  REQUIRE(x && logits && w1_codes && w1_scales && w2_codes && w2_scales && topk_ids && gate && out &&
+              workspace,
+          NVFP4MOE_EINVAL);
+  REQUIRE(nv == (w1_outer != nullptr) && nv == (w2_outer != nullptr), NVFP4MOE_EINVAL);
+  REQUIRE(aligned16(x) && aligned16(w1_codes) && aligned16(w1_scales) && aligned16(w2_codes) &&
+              aligned16(w2_scales) && aligned16(out) && aligned16(workspace) &&
+              aligned(logits, logits_dtype == NVFP4MOE_F32 ? 4 : 2) && aligned(bias, 4) &&
+              aligned(w1_outer, 4) && aligned(w2_outer, 4) && aligned(topk_ids, 4) &&
+              aligned(gate, 4),
+          NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(workspace_bytes >= tokens_workspace_bytes(T, k, F), NVFP4MOE_EWORKSPACE);
+  TokensArgs a;
+  a.x = x;
+  a.logits = logits;
+  a.logits_bf16 = logits_dtype == NVFP4MOE_BF16;
+  a.T = (int)T;
+  a.E = E;
+  a.k = k;
+  a.sigmoid = score == NVFP4MOE_SCORE_SIGMOID;
+  a.renorm = renorm != 0;
+  a.scale = scale;
+  a.bias = bias;
+  a.token_mask = token_mask;
+  a.w1_codes = w1_codes;
+  a.w1_scales = w1_scales;
+  a.w1_outer = w1_outer;
+  a.w2_codes = w2_codes;
+  a.w2_scales = w2_scales;
+  a.w2_outer = w2_outer;
+  a.e0 = e0;
+  a.n_local = n_local;
+  a.K = K;
+  a.F = F;
+  a.act = act;
+  a.gated = gated != 0;
+  a.topk_ids = topk_ids;
+  a.gate = gate;
+  a.out = out;
+  a.out_bf16 = out_dtype == NVFP4MOE_BF16;
+  a.ws = static_cast<uint8_t*>(workspace);
+  return hip_status(launch_ffn_tokens(a, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -24,6 +24,13 @@ hipError_t launch_nvfp4_quantize_live(const void* x, bool bf16, int64_t rows, in
                                       const int64_t* n_live, uint8_t* codes, uint8_t* scales,
                                       float* outer, hipStream_t stream);
 
+// mxfp4.hip
+hipError_t launch_mxfp4_quantize(const void* x, bool bf16, int64_t rows, int64_t cols,
+                                 const int64_t* n_live, uint8_t* codes, uint8_t* scales,
+                                 hipStream_t stream);
+hipError_t launch_mx_dequantize(bool mx8, const uint8_t* q, const uint8_t* e8, int64_t rows,
+                                int64_t cols, void* out, bool out_bf16, hipStream_t stream);
+
 // combine.hip
 hipError_t launch_combine(const void* y, bool y_bf16, int64_t m_cap, int64_t T, int k,
                           int64_t N, const int32_t* pair_row, const float* gate, void* out,
@@ -71,6 +78,13 @@ hipError_t launch_mxfp8_quantize_dual(const void* x, bool bf16, int64_t rows, in
                                       const int64_t* offsets, const int64_t* padded, int G,
                                       int64_t P, uint8_t* row_out, uint8_t* row_e8, uint8_t* out,
                                       uint8_t* out_e8, hipStream_t stream);
+
+// saved MXFP4 rows (through row_token where it is given) or per-expert weights (blocked)
+hipError_t launch_requant_sr_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                   int64_t cols, const int32_t* row_token, const int64_t* offsets,
+                                   const int64_t* padded, int G, int64_t P, bool blocked,
+                                   uint64_t seed, uint32_t tag, uint8_t* out, uint8_t* out_e8,
+                                   hipStream_t stream);
 
 hipError_t launch_nvfp4_requant_sr(const uint8_t* codes, const uint8_t* scales,
                                    const float* outer, int64_t rpg, int64_t rows, int64_t cols,
@@ -121,6 +135,40 @@ hipError_t launch_fwd_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scal
                                    const uint8_t* b_scales, const float* b_outer,
                                    const int64_t* offsets, int G, int64_t m_cap, int64_t N,
                                    int64_t K, void* y, bool y_bf16, hipStream_t stream);
+
+// gemm_mxfp4.hip
+hipError_t launch_fwd_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a_rows,
+                            const int32_t* row_token, const uint8_t* b_codes,
+                            const uint8_t* b_scales, const int64_t* offsets, int G, int64_t m_cap,
+                            int64_t N, int64_t K, void* y, bool y_bf16, hipStream_t stream);
+
+// tokens.hip
+constexpr int kTokensMaxT = 64;            // tokens, pairs and slots of a few-token call
+constexpr int kTokensMaxPairs = 512;
+constexpr int kTokensMaxK = 16;
+struct TokensArgs {
+  const void* x;                           // bf16 [T, K]
+  const void* logits;
+  bool logits_bf16;
+  int T, E, k;
+  bool sigmoid, renorm;
+  float scale;
+  const float* bias;
+  const uint8_t* token_mask;
+  const uint8_t *w1_codes, *w1_scales, *w2_codes, *w2_scales;
+  const float *w1_outer, *w2_outer;        // NVFP4's, null for MXFP4
+  int e0, n_local;
+  int64_t K, F;
+  int act;
+  bool gated;
+  int32_t* topk_ids;
+  float* gate;
+  void* out;
+  bool out_bf16;
+  uint8_t* ws;
+};
+size_t tokens_workspace_bytes(int64_t T, int k, int64_t F);
+hipError_t launch_ffn_tokens(const TokensArgs& a, hipStream_t stream);
 
 // gemm_bwd.hip
 hipError_t launch_dgrad(const uint8_t* dy_e4m3, const uint8_t* dy_e8m0, const uint8_t* w_e4m3,

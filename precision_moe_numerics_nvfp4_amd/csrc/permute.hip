@@ -109,7 +109,8 @@ __device__ __forceinline__ void copy_rows(int nv, const int32_t* ldst, const int
       for (int u = 0; u < 8; ++u) ps[d[u]] = v[u];
     }
   }
-  for (int i = tid; i < nv; i += 256) po[ldst[i]] = qo[lsrc[i]];
+  if (po)                                   // null with K = 0: grouping without rows
+    for (int i = tid; i < nv; i += 256) po[ldst[i]] = qo[lsrc[i]];
 }
 
 // Exclusive scan of v over the 256 threads of the workgroup; returns the

@@ -5,6 +5,9 @@
 //    to float32, transposed, and re-quantized to MXFP8 with stochastic
 //    rounding ("Inkling 2 Small uses four-bit training ...", section
 //    "Stochastic rounding across transposes");
+//  * mxfp8_requant_sr_mxfp4: the same from saved MXFP4, whose activation rows
+//    may still be in token order: the tile then reads row row_token[r], so no
+//    gathered copy is made (a row is read once per expert it goes to);
 //  * mxfp8_quantize (COLWISE_GROUPED): dY is transposed and quantized with
 //    round-to-nearest-even, giving the wgrad operand;
 //  * the NVFP4 backward (nvfp4_requant_sr, nvfp4_quantize_sr colwise): the
@@ -54,7 +57,7 @@ namespace {
 constexpr int TP = 128;  // tokens per tile
 constexpr int TK = 128;  // columns per tile
 
-enum class Src { NVFP4, BF16, F32 };
+enum class Src { NVFP4, BF16, F32, MXFP4 };
 
 __device__ __forceinline__ int slot_of(int r) { return 16 * (r & 7) + (r >> 3); }
 
@@ -67,6 +70,12 @@ struct Tile<Src::NVFP4> {
   uint32_t codes[TP * CW];
   uint32_t scales[TP][TK / 64];              // 8 E4M3 bytes per slot
   float outer[TP];
+};
+template <>
+struct Tile<Src::MXFP4> {
+  static constexpr int CW = 18;              // code words per slot (16 used)
+  uint32_t codes[TP * CW];
+  uint32_t scales[TP];                       // 4 E8M0 bytes per slot
 };
 template <>
 struct Tile<Src::BF16> {
@@ -199,7 +208,8 @@ __global__ __launch_bounds__(256) void k_transpose_mx(
     const int64_t* __restrict__ offsets, const int64_t* __restrict__ padded, int G, int64_t P,
     uint64_t seed, uint32_t tag, uint8_t* __restrict__ out, uint8_t* __restrict__ out_e8,
     uint8_t* __restrict__ row_out = nullptr, uint8_t* __restrict__ row_e8 = nullptr,
-    const uint32_t* __restrict__ gbits = nullptr) {
+    const uint32_t* __restrict__ gbits = nullptr, const int32_t* __restrict__ row_token = nullptr,
+    int64_t src_rows = 0) {
   __shared__ Tile<S> tile;
   __shared__ int64_t row_of[TP];  // source row of each tile token, -1 = padding
   __shared__ int grp_of[TP];      // group of each tile token
@@ -224,6 +234,12 @@ __global__ __launch_bounds__(256) void k_transpose_mx(
       }
       const int64_t i = p - padded[lo];
       if (i < offsets[lo + 1] - offsets[lo]) r = offsets[lo] + i;
+      if constexpr (S == Src::MXFP4) {
+        if (r >= 0 && row_token) {
+          r = row_token[r];
+          if (r >= src_rows) r = -1;         // not a row of the source: taken as zero
+        }
+      }
       grp_of[tid] = lo;
     } else {
       grp_of[tid] = 0;
@@ -233,7 +249,7 @@ __global__ __launch_bounds__(256) void k_transpose_mx(
   __syncthreads();
 
   // ---- stage the input rows of this tile
-  if constexpr (S == Src::NVFP4) {
+  if constexpr (S == Src::NVFP4 || S == Src::MXFP4) {
     const uint8_t* codes = static_cast<const uint8_t*>(src);
     {  // 64 code bytes per row: 2 threads x 32 bytes
       const int t = tid >> 1, h = tid & 1;
@@ -248,7 +264,13 @@ __global__ __launch_bounds__(256) void k_transpose_mx(
       d[0] = make_uint2(a.x, a.y); d[1] = make_uint2(a.z, a.w);
       d[2] = make_uint2(b.x, b.y); d[3] = make_uint2(b.z, b.w);
     }
-    if (tid < TP) {
+    if constexpr (S == Src::MXFP4) {
+      if (tid < TP) {
+        const int64_t r = row_of[tid];
+        tile.scales[slot_of(tid)] =
+            r >= 0 ? *reinterpret_cast<const uint32_t*>(src_scales + r * (cols / 32) + k0 / 32) : 0u;
+      }
+    } else if (tid < TP) {
       const int64_t r = row_of[tid];
       uint2 sc = make_uint2(0, 0);
       float o = 0.0f;
@@ -286,7 +308,7 @@ __global__ __launch_bounds__(256) void k_transpose_mx(
   }
   __syncthreads();
 
-  if constexpr (ROWS && S != Src::NVFP4) {
+  if constexpr (ROWS && S != Src::NVFP4 && S != Src::MXFP4) {
     // row-wise pass over the staged tile: lane l takes 8 columns (chunk l % 16)
     // of token (l / 16) + 16 it; the four lanes of a quad hold one 32-column
     // block. Same exponent rule and rounding as the row-wise kernel.
@@ -344,6 +366,18 @@ __global__ __launch_bounds__(256) void k_transpose_mx(
         v[2 * j][i] = __fmul_rn(__fmul_rn(e0, Sb), o);       // e2m1 * S is exact
         v[2 * j + 1][i] = __fmul_rn(__fmul_rn(e1, Sb), o);
       }
+    } else if constexpr (S == Src::MXFP4) {
+      // the conversion takes the power of two of its scale operand, which is
+      // all that an E8M0 scale has: e2m1 * 2^(c - 127) in one instruction
+      typedef float f32x2 __attribute__((ext_vector_type(2)));
+      const uint32_t w = tile.codes[sl * Tile<S>::CW + kc];
+      const float sc = u2f(((tile.scales[sl] >> (8 * (kc >> 2))) & 0xFFu) << 23);
+      const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, sc, 0);
+      const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, sc, 1);
+      const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, sc, 2);
+      const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, sc, 3);
+      v[0][i] = a.x; v[1][i] = a.y; v[2][i] = b.x; v[3][i] = b.y;
+      v[4][i] = c.x; v[5][i] = c.y; v[6][i] = d.x; v[7][i] = d.y;
     } else if constexpr (S == Src::BF16) {
       const uint4 a = *reinterpret_cast<const uint4*>(&tile.v[sl][8 * kc]);
       const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -464,13 +498,12 @@ hipError_t run(const void* src, const uint8_t* sc, const float* so, int64_t rpg,
                int64_t cols, const int64_t* offsets, const int64_t* padded, int G, int64_t P,
                uint64_t seed, uint32_t tag, uint8_t* out, uint8_t* out_e8, hipStream_t stream,
                uint8_t* row_out = nullptr, uint8_t* row_e8 = nullptr,
-               const uint32_t* gbits = nullptr) {
-  (void)rows;
+               const uint32_t* gbits = nullptr, const int32_t* row_token = nullptr) {
   if (P == 0 || cols == 0 || G == 0) return hipSuccess;
   const int64_t grid = (P + TP - 1) / TP * (cols / TK);
   k_transpose_mx<S, SR, ROWS, NV, BLK><<<(unsigned)grid, 256, 0, stream>>>(
       src, sc, so, rpg, cols, offsets, padded, G, P, seed, tag, out, out_e8, row_out, row_e8,
-      gbits);
+      gbits, row_token, rows);
   return hipGetLastError();
 }
 
@@ -514,6 +547,16 @@ hipError_t launch_requant_sr(const uint8_t* codes, const uint8_t* scales, const 
                                                      out_e8, stream);
   return run<Src::NVFP4, true>(codes, scales, outer, rpg, rows, cols, offsets, padded, G, P, seed,
                                tag, out, out_e8, stream);
+}
+
+hipError_t launch_requant_sr_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                   int64_t cols, const int32_t* row_token, const int64_t* offsets,
+                                   const int64_t* padded, int G, int64_t P, bool blocked,
+                                   uint64_t seed, uint32_t tag, uint8_t* out, uint8_t* out_e8,
+                                   hipStream_t stream) {
+  auto f = blocked ? run<Src::MXFP4, true, false, false, true> : run<Src::MXFP4, true>;
+  return f(codes, scales, nullptr, 0, rows, cols, offsets, padded, G, P, seed, tag, out, out_e8,
+           stream, nullptr, nullptr, nullptr, row_token);
 }
 
 hipError_t launch_nvfp4_requant_sr(const uint8_t* codes, const uint8_t* scales,

@@ -8,7 +8,7 @@ re-quantize the saved NVFP4 activations and weights to MXFP8 with stochastic
 rounding through a float32 transpose, quantize dY to MXFP8 in both
 orientations, run the dgrad and wgrad grouped GEMMs.
 
-Also here: the expert FFN around the layer (ExpertFFNStep: down-projection,
+Also here: the same step with an MXFP4 forward (MXFP4LayerStep), the expert FFN around the layer (ExpertFFNStep: down-projection,
 per-token re-quantization of the intermediate, weighted combine, backward
 through both projections), the FFN with the router in front of it and the
 clipping of its gradients behind (RoutedFFNStep), and the NVFP4 backward
@@ -106,6 +106,46 @@ class ExpertLayerStep:
         self.quantize_dy(dy)
         self.dgrad()
         self.wgrad()
+
+
+class MXFP4LayerStep(ExpertLayerStep):
+    """ExpertLayerStep with an MXFP4 forward: the format the matrix units
+    multiply as it is stored. Activations stay in token order (the products
+    read them through ``perm["row_token"]``), and there are no outer scales;
+    gradients are MXFP8 as there."""
+
+    def __init__(self, T, K, N, E, k, e0=0, x_dtype=torch.bfloat16, out_dtype=torch.float32,
+                 seed=0x5EED0004, device="cuda"):
+        super().__init__(T, K, N, E, k, e0, x_dtype, out_dtype, seed, device)
+        e = lambda *s: torch.empty(s, dtype=torch.uint8, device=self.y.device)
+        self.xq = (e(T, K // 2), e(T, K // 32))
+        self.wq = (e(E * N, K // 2), e(E * N, K // 32))
+        self.perm = {n: self.perm[n] for n in ("offsets", "padded_offsets", "row_token", "row_slot")}
+
+    def quantize_x(self, x):
+        return B.mxfp4_quantize(x, None, *self.xq)
+
+    def quantize_w(self, w):
+        return B.mxfp4_quantize(w, None, *self.wq)
+
+    def permute(self, topk_ids):
+        return B.moe_group(topk_ids, self.e0, self.E, workspace=self.ws, out=self.perm)
+
+    def forward_gemm(self):
+        p = self.perm
+        return B.moe_fwd_grouped_gemm_mxfp4(*self.xq, *self.wq, p["offsets"],
+                                            row_token=p["row_token"], y=self.y)
+
+    def requant_x(self):
+        p = self.perm
+        return B.mxfp8_requant_sr_mxfp4(*self.xq, p["offsets"], p["padded_offsets"], self.P,
+                                        self.seed, 0, row_token=p["row_token"], out=self.xT[0],
+                                        out_e8=self.xT[1])
+
+    def requant_w(self):
+        return B.mxfp8_requant_sr_mxfp4(*self.wq, self.w_off, self.w_off, self.E * self.N,
+                                        self.seed, 1, rows_per_group=self.N, out=self.wT[0],
+                                        out_e8=self.wT[1])
 
 
 class ExpertFFNStep:
