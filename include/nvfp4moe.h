@@ -678,7 +678,7 @@ NVFP4MOE_API int moe_group(const int32_t* topk_ids, int64_t T, int k, int e0, in
  * y[r, n] = sum_k a[row, k] * b[g, n, k] for rows r of group g; y [m_cap, N]
  *   float32 or bfloat16 (round to nearest even). Products and the sums of a
  *   block of 32 are exact, the blocks are added in float32. Rows >= offsets[G]
- *   untouched. Requires N % 128 == 0, K % 128 == 0, K < 2^23, G <= 4095,
+ *   untouched. Requires N % 128 == 0, K % 128 == 0, K < 2^23, G <= 4000,
  *   m_cap < 2^31, a_rows < 2^31, scales 4-byte aligned.
  */
 NVFP4MOE_API int moe_fwd_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a_rows,

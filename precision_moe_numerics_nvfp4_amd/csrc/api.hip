@@ -604,7 +604,7 @@ int moe_fwd_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, 
   REQUIRE(a_codes && a_scales && b_codes && b_scales && offsets && y, NVFP4MOE_EINVAL);
   REQUIRE(row_token || a_rows >= m_cap, NVFP4MOE_EINVAL);
   REQUIRE(N % 128 == 0 && K % 128 == 0 && K > 0 && K < (int64_t)1 << 23, NVFP4MOE_EUNSUPPORTED);
-  REQUIRE(G <= 4095 && m_cap < (int64_t)1 << 31 && a_rows < (int64_t)1 << 31, NVFP4MOE_EUNSUPPORTED);
+  REQUIRE(G <= 4000 && m_cap < (int64_t)1 << 31 && a_rows < (int64_t)1 << 31, NVFP4MOE_EUNSUPPORTED);
   REQUIRE(N / 128 < kMaxTiles / (m_cap / 32 + G + 1), NVFP4MOE_EUNSUPPORTED);
   REQUIRE(aligned16(a_codes) && aligned16(b_codes) && aligned16(y) && aligned(a_scales, 4) &&
               aligned(b_scales, 4) && aligned(row_token, 4) && aligned(offsets, 8),

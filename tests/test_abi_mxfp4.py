@@ -58,7 +58,7 @@ def test_gemm_refusals(L):
     assert f(dt=7) == f(G=-1) == f(cap=-1) == f(N=-128) == f(K=-128) == f(rows=-1) == EINVAL
     assert f(rows=63) == EINVAL                                   # rows are read in place
     assert f(N=64) == f(K=64) == f(K=0) == f(K=1 << 23) == EUNSUP
-    assert f(G=4096) == f(cap=1 << 31, rows=1 << 31) == f(N=1 << 40) == EUNSUP
+    assert f(G=4001) == f(cap=1 << 31, rows=1 << 31) == f(N=1 << 40) == EUNSUP
     assert f(ac=FOUR) == f(bc=FOUR) == f(y=FOUR) == f(as_=ODD) == f(bs=ODD) == f(tok=ODD) == f(off=FOUR) == EUNSUP
     assert f(G=0) == f(cap=0) == f(N=0) == f(rows=0) == 0
 
