@@ -83,26 +83,37 @@ __global__ __launch_bounds__(256) void k_mxfp4_small(
 // ---------------------------------------------------------------------------
 // Large groups: tiles of up to 256 rows x 256 columns through an LDS ring.
 //
-// A stage is 128 contraction elements: 64 code bytes of each row of both
-// operands, by buffer loads with the LDS-destination bit (16 rows an
-// instruction; 16-byte piece p of row r at position p ^ chunk_key(r)), four
-// stages in the ring. The E8M0 bytes come 16 to a row, for four stages, into
-// a ring of two blocks; a wavefront holds its rows' 16 bytes in registers and
-// shifts a stage's four to the byte that its half of the lanes needs (the
-// instruction's operand select takes byte 0 for the first 64 elements and
-// byte 2 for the second).
+// A stage is 256 contraction elements: 128 code bytes (a cache line) of each
+// row of both operands, by buffer loads with the LDS-destination bit (8 rows an
+// instruction; 16-byte piece c of row r at position c ^ piece_key(r)), two
+// stages in the ring. The E8M0 bytes come 16 to a row, for two stages, into a
+// ring of two such blocks; a wavefront holds its rows' 16 bytes in registers and
+// shifts a dword of them to the byte that its half of the lanes needs (the
+// instruction's operand select takes byte 0 for the first 64 elements and byte 2
+// for the second).
 //
-// A stage is two steps of 64 elements. The fragments of a step are read from
+// A stage is four steps of 64 elements. The fragments of a step are read from
 // LDS under the products of the step before it: A in place, right after a
 // fragment's last product, B into the other of two sets. One barrier a stage,
-// between its steps: by then every wavefront holds the stage's last fragments,
-// so its buffer takes the stage four further on.
+// before its last step: by then every wavefront holds the stage's last
+// fragments, so its buffer takes the stage after the next.
+constexpr int kWN = 4, kWaves = 2 * kWN;    // 2 x 4 wavefronts of 128 x 64
+constexpr int kTN = 2;
 constexpr int kBN = 256;                    // columns of a tile
-constexpr int kRing = 4;                    // stages in flight
+constexpr int kRB = 128;                    // code bytes of a row and stage
+constexpr int kStage = 512 * kRB;
+constexpr int kScales = 2 * kStage;         // LDS offset of the scale ring
+constexpr int kScaleBlock = 512 * 16;
+constexpr int kLds = kScales + 2 * kScaleBlock;
 constexpr int kBufferWord3 = 0x00020000;    // raw buffer, 32-bit data format
+constexpr uint32_t kAway = 0x80000000u;     // past every range: the load gives zeros
 
 typedef __attribute__((address_space(3))) void lds_void;
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Rows of 128 bytes: for one piece, 8 consecutive rows land in the 8 distinct
+// 16-byte groups of 128 bytes and 16 in the 16 of 256.
+__device__ __forceinline__ int piece_key(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
 __device__ __forceinline__ void* uniform_ptr(const void* p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
@@ -111,10 +122,9 @@ __device__ __forceinline__ void* uniform_ptr(const void* p) {
   return reinterpret_cast<void*>(((uint64_t)hi << 32) | lo);
 }
 
-template <int N, bool LGKM>
+template <int N>
 __device__ __forceinline__ void wait_barrier() {
-  if constexpr (LGKM) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-  else asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 struct Gemm {
@@ -126,142 +136,140 @@ struct Gemm {
   int G;
 };
 
-// 2 x WN wavefronts; a wavefront's row block i is 2 i + wm (so that the rows of
-// a partial tile spread over all of them), its columns BN / WN from wn BN / WN.
-template <int WN>
-struct Ring {
-  static constexpr int NW = 2 * WN;
-  static constexpr int STAGE = (256 + kBN) * 64;
-  static constexpr int SC = kRing * STAGE;
-  static constexpr int SBLK = (256 + kBN) * 16;
-  static constexpr int LDS = SC + 2 * SBLK;
-  static constexpr int TN = kBN / (32 * WN);
+// A tile's place: rows row0 .. row0 + rows - 1 of group g, columns from n0.
+struct Tile {
+  int g, rows;
+  int64_t row0, n0;
 };
 
-template <int TM, int WN, class Store>
-__device__ __forceinline__ void tile(uint8_t* lsm, const Gemm& p, int g, int64_t row0, int rows,
-                                     int64_t n0, Store store) {
-  using R = Ring<WN>;
-  constexpr int NW = R::NW, TN = R::TN;
-  constexpr int CA = (4 * TM + NW - 1) / NW, CB = 16 / NW;   // code loads of a wavefront and stage
-  constexpr int NL = CA + CB, NS = 8 / NW;                   // scale loads of a block
-  int tid_ = threadIdx.x;
-  asm volatile("" : "+v"(tid_));            // per tile: nothing of it is held across tiles
-  const int lane = tid_ & 63, wave = __builtin_amdgcn_readfirstlane(tid_ >> 6);
-  const int wm = wave / WN, wn = wave % WN, half = lane >> 5, r32 = lane & 31;
-  const uint32_t ldq = (uint32_t)(p.K / 2), lds_ = (uint32_t)(p.K / 32);
-  const int ns = (int)(p.K / 128);
-  constexpr uint32_t kAway = 0x80000000u;   // past every range: the load gives zeros
+// What a tile's loads need, in registers from before its first load to its
+// last. A wavefront's load i fills rows 8 (kWaves i + wave) + lane / 8 of an
+// operand, and a lane's piece is the same in all of them.
+struct Loads {
+  __amdgpu_buffer_rsrc_t ra, rb, rs;        // codes of A and B, scales of the rows it loads
+  uint32_t oa[4], ob, os;                   // byte offsets
+  int end;                                  // stage offsets below it are inside the row
 
-  const int64_t a_base = p.row_token ? 0 : row0;
-  const int64_t b_base = (int64_t)g * p.N + n0;
-  auto rsrc = [](const uint8_t* q, int64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(q), (short)0,
-                                             (int)__builtin_amdgcn_readfirstlane((uint32_t)bytes),
-                                             kBufferWord3);
-  };
-  const int64_t a_n = p.row_token ? p.a_rows : rows;
-  const __amdgpu_buffer_rsrc_t ra = rsrc(p.ac + a_base * ldq, a_n * ldq);
-  const __amdgpu_buffer_rsrc_t sa = rsrc(p.as + a_base * lds_, a_n * lds_);
-  const __amdgpu_buffer_rsrc_t rb = rsrc(p.bc + b_base * ldq, (int64_t)kBN * ldq);
-  const __amdgpu_buffer_rsrc_t sb = rsrc(p.bs + b_base * lds_, (int64_t)kBN * lds_);
-  // the row of A that tile row r reads, or -1
-  auto row_of = [&](int r) -> int64_t {
-    if (r >= rows) return -1;
-    if (!p.row_token) return r;
-    const int64_t t = p.row_token[row0 + r];
-    return t < 0 ? 0 : (t < p.a_rows ? t : p.a_rows - 1);
-  };
-  uint32_t oa[CA], ob[CB], os[NS];
+  __device__ __forceinline__ void init(const Gemm& p, const Tile& t, int lane, int wave) {
+    const uint32_t ldq = (uint32_t)(p.K / 2), lds_ = (uint32_t)(p.K / 32);
+    const int64_t a_base = p.row_token ? 0 : t.row0, a_n = p.row_token ? p.a_rows : t.rows;
+    const int64_t b_base = (int64_t)t.g * p.N + t.n0;
+    auto rsrc = [](const uint8_t* q, int64_t bytes) {
+      return __builtin_amdgcn_make_buffer_rsrc(
+          uniform_ptr(q), (short)0, (int)__builtin_amdgcn_readfirstlane((uint32_t)bytes),
+          kBufferWord3);
+    };
+    ra = rsrc(p.ac + a_base * ldq, a_n * ldq);
+    rb = rsrc(p.bc + b_base * ldq, (int64_t)kBN * ldq);
+    const bool of_a = wave < kWaves / 2;    // 64 rows' scales a wavefront: A's, or B's
+    rs = of_a ? rsrc(p.as + a_base * lds_, a_n * lds_)
+              : rsrc(p.bs + b_base * lds_, (int64_t)kBN * lds_);
+    // the row of A that tile row r reads, or -1
+    auto row_of = [&](int r) -> int64_t {
+      if (r >= t.rows) return -1;
+      if (!p.row_token) return r;
+      const int64_t q = p.row_token[t.row0 + r];
+      return q < 0 ? 0 : (q < p.a_rows ? q : p.a_rows - 1);
+    };
+    const int piece = (lane & 7) ^ piece_key(8 * wave + (lane >> 3));
 #pragma unroll
-  for (int i = 0; i < CA; ++i) {
-    const int r = 16 * (NW * i + wave) + (lane >> 2);
-    const int64_t t = row_of(r);
-    oa[i] = t < 0 ? kAway : (uint32_t)(t * ldq) + (((lane & 3) ^ chunk_key(r)) << 4);
-  }
-#pragma unroll
-  for (int i = 0; i < CB; ++i) {
-    const int r = 16 * (NW * i + wave) + (lane >> 2);
-    ob[i] = (uint32_t)r * ldq + (((lane & 3) ^ chunk_key(r)) << 4);
-  }
-#pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const int q = 64 * (NW * i + wave) + lane;               // rows of A, then of B
-    const int64_t t = q < 256 ? row_of(q) : 0;
-    os[i] = q < 256 ? (t < 0 ? kAway : (uint32_t)(t * lds_)) : (uint32_t)(q - 256) * lds_;
-  }
-  auto issue = [&](int s) {
-    uint8_t* st = lsm + (s & (kRing - 1)) * R::STAGE;
-    const bool real = s < ns;
-    const uint32_t k = real ? (uint32_t)s * 64u : 0u;
-#pragma unroll
-    for (int i = 0; i < CA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + (NW * i + wave) * 1024), 16,
-                                               real ? oa[i] + k : kAway, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < CB; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rb, (lds_void*)(st + 256 * 64 + (NW * i + wave) * 1024), 16, real ? ob[i] + k : kAway, 0,
-          0, 0);
-  };
-  auto issue_scales = [&](int b) {
-    uint8_t* st = lsm + R::SC + (b & 1) * R::SBLK;
-    const bool real = b * 4 < ns;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const int w = NW * i + wave;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(w < 4 ? sa : sb, (lds_void*)(st + w * 1024), 16,
-                                               real ? os[i] + (uint32_t)b * 16u : kAway, 0, 0, 0);
+    for (int i = 0; i < 4; ++i) {
+      const int64_t q = row_of(8 * (kWaves * i + wave) + (lane >> 3));
+      oa[i] = q < 0 ? kAway : (uint32_t)(q * ldq) + 16u * piece;
     }
-  };
+    ob = (uint32_t)(8 * wave + (lane >> 3)) * ldq + 16u * piece;
+    end = (int)ldq - 16 * piece;
+    const int r = 64 * (wave % kWN) + lane;
+    const int64_t q = of_a ? row_of(r) : r;
+    os = q < 0 ? kAway : (uint32_t)(q * lds_);
+  }
+  // The codes of stage s. The range check covers the vector offset alone, and
+  // the scalar one (the place in the row, B's rows) stays inside the operand
+  // where that passes; elements past a row's end are zeros.
+  template <int TM>
+  __device__ __forceinline__ void codes(uint8_t* lsm, const Gemm& p, int s, int wave) const {
+    uint8_t* st = lsm + (s & 1) * kStage + wave * 1024;
+    const uint32_t k = (uint32_t)s * (uint32_t)kRB;
+    const bool real = (int)k < end;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + kWaves * i * 1024), 16,
+                                               real ? oa[i] : kAway, k, 0, 0);
+    const uint32_t o = real ? ob : kAway;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rb, (lds_void*)(st + 256 * kRB + kWaves * i * 1024), 16, o,
+          k + (uint32_t)(8 * kWaves * i) * (uint32_t)(p.K / 2), 0, 0);
+  }
+  // The scales of stages 2 b and 2 b + 1 (those behind the row's end belong to
+  // codes of zero).
+  __device__ __forceinline__ void scales(uint8_t* lsm, const Gemm& p, int b, int wave) const {
+    const bool real = b * 512 < p.K;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rs, (lds_void*)(lsm + kScales + (b & 1) * kScaleBlock + wave * 1024), 16,
+        real ? os + 16u * (uint32_t)b : kAway, 0, 0, 0);
+  }
+};
 
+// The products of a tile of 64 TM rows whose first loads (scales of block 0,
+// codes of stages 0 and 1) are on their way, the second stage's last. A
+// wavefront's row block i is block 2 i + wm of the tile (so that the rows of a
+// partial tile spread over all of them), its columns the 64 from 64 wn.
+template <int TM>
+__device__ __forceinline__ void products(uint8_t* lsm, const Gemm& p, const Loads& ld, int lane,
+                                         int wave, f32x16 (&acc)[4][kTN]) {
+  constexpr int TN = kTN;
+  const int wm = wave / kWN, wn = wave % kWN, half = lane >> 5, r32 = lane & 31;
+  const int ns = (int)((p.K + 255) / 256);
   // fragment 0's places; fragment i of A sits 64 rows further, of B 32
   const int fa = wm * 32 + r32, fb = wn * (32 * TN) + r32;
-  int pa[2], pb[2];
+  int pa[4], pb[4];
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    pa[s] = fa * 64 + (((2 * s + half) ^ chunk_key(fa)) << 4);
-    pb[s] = 256 * 64 + fb * 64 + (((2 * s + half) ^ chunk_key(fb)) << 4);
+  for (int s = 0; s < 4; ++s) {
+    pa[s] = fa * kRB + (((2 * s + half) ^ piece_key(fa)) << 4);
+    pb[s] = 256 * kRB + fb * kRB + (((2 * s + half) ^ piece_key(fb)) << 4);
   }
-  const int qa = R::SC + fa * 16, qb = R::SC + (256 + fb) * 16;
+  const int qa = kScales + fa * 16, qb = kScales + (256 + fb) * 16;
   u32x4 A[TM], B[2][TN], sA[TM], sB[TN];
   uint32_t ca[TM], cb[TN];
   auto read_a = [&](int i, int s, int step) {
-    A[i] = *reinterpret_cast<const u32x4*>(lsm + (s & (kRing - 1)) * R::STAGE + pa[step] + i * 64 * 64);
+    A[i] = *reinterpret_cast<const u32x4*>(lsm + (s & 1) * kStage + pa[step] + i * 64 * kRB);
   };
   auto read_b = [&](int set, int j, int s, int step) {
-    B[set][j] = *reinterpret_cast<const u32x4*>(lsm + (s & (kRing - 1)) * R::STAGE + pb[step] + j * 32 * 64);
+    B[set][j] = *reinterpret_cast<const u32x4*>(lsm + (s & 1) * kStage + pb[step] + j * 32 * kRB);
+  };
+  auto read_sa = [&](int i, int b) {
+    sA[i] = *reinterpret_cast<const u32x4*>(lsm + qa + (b & 1) * kScaleBlock + i * 64 * 16);
+  };
+  auto read_sb = [&](int j, int b) {
+    sB[j] = *reinterpret_cast<const u32x4*>(lsm + qb + (b & 1) * kScaleBlock + j * 32 * 16);
   };
   auto wide = [](const u32x4& v) {
     return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
   };
-
-  f32x16 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-
-  issue_scales(0);
-#pragma unroll
-  for (int s = 0; s < kRing; ++s) issue(s);
-  wait_barrier<3 * NL, false>();
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     read_a(i, 0, 0);
-    sA[i] = *reinterpret_cast<const u32x4*>(lsm + qa + i * 64 * 16);
+    read_sa(i, 0);
   }
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
     read_b(0, j, 0, 0);
-    sB[j] = *reinterpret_cast<const u32x4*>(lsm + qb + j * 32 * 16);
+    read_sb(j, 0);
   }
 
-  // the products of one step, and the reads of the next one's fragments
+  // The products of step T of a stage, and the reads of the next step's
+  // fragments (of the next stage after the last step, and of the next scale
+  // block after that block's last stage).
   auto step = [&](auto at, int s_next, int scale_block) {
-    constexpr int S = decltype(at)::value;                   // step of the stage
+    constexpr int T = decltype(at)::value, S = T & 1, NX = (T + 1) % 4;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -270,106 +278,106 @@ __device__ __forceinline__ void tile(uint8_t* lsm, const Gemm& p, int g, int64_t
         // columns first: a lane then holds four consecutive columns of a row
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
             wide(B[S][j]), wide(A[i]), acc[i][j], 4, 4, 2 * S, (int)cb[j], 2 * S, (int)ca[i]);
-      read_a(i, s_next, 1 - S);
-      if (i < TN) {
-        read_b(1 - S, i, s_next, 1 - S);
-        if constexpr (S == 1)
-          if (scale_block >= 0)
-            sB[i] = *reinterpret_cast<const u32x4*>(lsm + qb + (scale_block & 1) * R::SBLK + i * 32 * 16);
-      }
-      if constexpr (S == 1)
-        if (scale_block >= 0)
-          sA[i] = *reinterpret_cast<const u32x4*>(lsm + qa + (scale_block & 1) * R::SBLK + i * 64 * 16);
+      read_a(i, s_next, NX);
+      if (i < TN) read_b(1 - S, i, s_next, NX);
+      if constexpr (T == 3)
+        if (scale_block >= 0) {
+          read_sa(i, scale_block);
+          if (i < TN) read_sb(i, scale_block);
+        }
     }
-    if constexpr (TN > TM) {
 #pragma unroll
-      for (int j = TM; j < TN; ++j) {
-        read_b(1 - S, j, s_next, 1 - S);
-        if constexpr (S == 1)
-          if (scale_block >= 0)
-            sB[j] = *reinterpret_cast<const u32x4*>(lsm + qb + (scale_block & 1) * R::SBLK + j * 32 * 16);
-      }
+    for (int j = TM; j < TN; ++j) {
+      read_b(1 - S, j, s_next, NX);
+      if constexpr (T == 3)
+        if (scale_block >= 0) read_sb(j, scale_block);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  using S0 = std::integral_constant<int, 0>;
-  using S1 = std::integral_constant<int, 1>;
-  // Stage s = 4 b + Q. Between its steps everything but the loads of stages
-  // s + 2 and s + 3 (and a scale block issued among them) has landed.
+  // Stage 2 b + Q.
   auto stage = [&](int b, auto at) {
     constexpr int Q = decltype(at)::value;
-    const int s = 4 * b + Q;
+    const int s = 2 * b + Q;
+    auto shift = [&](int d) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) ca[i] = sA[i][Q] >> (8 * half);
+      for (int i = 0; i < TM; ++i) ca[i] = sA[i][d] >> (8 * half);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) cb[j] = sB[j][Q] >> (8 * half);
-    step(S0{}, s, -1);
-    wait_barrier<2 * NL + (Q == 1 || Q == 2 ? NS : 0), true>();
-    if constexpr (Q == 0) issue_scales(b + 1);
-    issue(s + kRing);
-    step(S1{}, s + 1, Q == 3 ? b + 1 : -1);
+      for (int j = 0; j < TN; ++j) cb[j] = sB[j][d] >> (8 * half);
+    };
+    shift(2 * Q);
+    step(std::integral_constant<int, 0>{}, s, -1);
+    step(std::integral_constant<int, 1>{}, s, -1);
+    shift(2 * Q + 1);
+    step(std::integral_constant<int, 2>{}, s, -1);
+    wait_barrier<0>();
+    if constexpr (Q == 0) ld.scales(lsm, p, b + 1, wave);
+    ld.codes<TM>(lsm, p, s + 2, wave);
+    step(std::integral_constant<int, 3>{}, s + 1, Q == 1 ? b + 1 : -1);
   };
-  const int nb = ns / 4;
+  const int nb = ns / 2;
   for (int b = 0; b < nb; ++b) {
     stage(b, std::integral_constant<int, 0>{});
     stage(b, std::integral_constant<int, 1>{});
-    stage(b, std::integral_constant<int, 2>{});
-    stage(b, std::integral_constant<int, 3>{});
   }
-  const int left = ns - 4 * nb;
-  if (left > 0) stage(nb, std::integral_constant<int, 0>{});
-  if (left > 1) stage(nb, std::integral_constant<int, 1>{});
-  if (left > 2) stage(nb, std::integral_constant<int, 2>{});
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the ring is free
-
-  store(acc, wave, lane);
+  if (ns & 1) stage(nb, std::integral_constant<int, 0>{});
+  wait_barrier<0>();                        // the ring is free
 }
 
-// A tile's rows through LDS, a wavefront's 32-row blocks one at a time, written
-// 16 bytes a lane along the rows.
-template <typename OutT, int TM, int TN>
-__device__ __forceinline__ void store_rows(uint8_t* lsm, const f32x16 (&acc)[TM][TN], int wave,
-                                           int lane, int wm, int rows, OutT* y, int64_t ld) {
-  constexpr int ES = sizeof(OutT), WC = 32 * TN, RS = WC * ES + 16, PPR = WC * ES / 16;
-  const int half = lane >> 5, r32 = lane & 31;
-  uint8_t* ep = lsm + wave * (32 * RS);
+// A tile's rows through LDS (the second stage's buffer), a wavefront's 32-row
+// blocks one at a time, written 16 bytes a lane along the rows. Float32 rows
+// take two halves of a block's columns one after the other.
+template <typename OutT, int TM>
+__device__ __forceinline__ void store_rows(uint8_t* lsm, const f32x16 (&acc)[4][kTN], int lane,
+                                           int wave, int rows, OutT* y, int64_t ld) {
+  constexpr int ES = sizeof(OutT), NC = ES == 2 ? kTN : 1;   // 32-column blocks at a time
+  constexpr int WC = 32 * NC, RS = WC * ES + 16, PPR = WC * ES / 16;
+  static_assert(kWaves * 32 * RS <= kStage, "the staging fits a stage's buffer");
+  const int wm = wave / kWN, half = lane >> 5, r32 = lane & 31;
+  uint8_t* ep = lsm + kStage + wave * (32 * RS);
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
+  for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
+    for (int c0 = 0; c0 < kTN; c0 += NC) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint8_t* d = ep + r32 * RS + (j * 32 + 8 * q + 4 * half) * ES;
-        const f32x16& v = acc[i][j];
-        if constexpr (ES == 2)
-          *reinterpret_cast<uint2*>(d) = make_uint2(pk_bf16(v[4 * q], v[4 * q + 1]),
-                                                    pk_bf16(v[4 * q + 2], v[4 * q + 3]));
-        else
-          *reinterpret_cast<float4*>(d) =
-              make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+      for (int j = 0; j < NC; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint8_t* d = ep + r32 * RS + (j * 32 + 8 * q + 4 * half) * ES;
+          const f32x16& v = acc[i][c0 + j];
+          if constexpr (ES == 2)
+            *reinterpret_cast<uint2*>(d) = make_uint2(pk_bf16(v[4 * q], v[4 * q + 1]),
+                                                      pk_bf16(v[4 * q + 2], v[4 * q + 3]));
+          else
+            *reinterpret_cast<float4*>(d) =
+                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
+#pragma unroll
+      for (int it = 0; it < 32 * PPR / 64; ++it) {
+        const int pc = it * 64 + lane, r = pc / PPR, c = pc % PPR;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(ep + r * RS + c * 16);
+        const int lr = (2 * i + wm) * 32 + r;
+        if (lr < rows)
+          __builtin_nontemporal_store(
+              v, reinterpret_cast<u32x4*>(y + (int64_t)lr * ld + c0 * 32 + c * (16 / ES)));
       }
-#pragma unroll
-    for (int it = 0; it < 32 * PPR / 64; ++it) {
-      const int pc = it * 64 + lane, r = pc / PPR, c = pc % PPR;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(ep + r * RS + c * 16);
-      const int lr = (2 * i + wm) * 32 + r;
-      if (lr < rows)
-        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y + (int64_t)lr * ld + c * (16 / ES)));
     }
-  }
 }
 
-// One workgroup per compute unit, each taking tiles v, v + gridDim.x, ...
-template <bool OUT_BF16, int WN>
-__global__ __launch_bounds__(128 * WN, 1) void k_mxfp4_tiles(Gemm p) {
+template <typename OutT>
+constexpr int kStores = 8 * sizeof(OutT);   // of a wavefront and whole tile: 128 x 64 in 16 bytes a lane
+
+// One workgroup per compute unit, each taking tiles v, v + gridDim.x, ... The
+// loads of a tile's first stage go out before the rows of the tile before it
+// are written.
+template <bool OUT_BF16>
+__global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lsm[];
-  using R = Ring<WN>;
   using OutT = std::conditional_t<OUT_BF16, uint16_t, float>;
-  int* pre = reinterpret_cast<int*>(lsm + R::LDS);
+  int* pre = reinterpret_cast<int*>(lsm + kLds);
   const int ntn = (int)(p.N / kBN);
   tile_prefix(p.G, [&](int e) { return (int)((p.offsets[e + 1] - p.offsets[e] + 255) / 256) * ntn; }, pre);
   const int total = pre[p.G];
-  for (int v = (int)blockIdx.x; v < total; v += (int)gridDim.x) {
+  auto locate = [&](int v) {
     const int x = v & 7, q8 = total >> 3, r8 = total & 7;
     const int t = x * q8 + (x < r8 ? x : r8) + (v >> 3);     // contiguous tiles to an XCD
     const int g = tile_group(pre, p.G, t);
@@ -377,39 +385,67 @@ __global__ __launch_bounds__(128 * WN, 1) void k_mxfp4_tiles(Gemm p) {
     int mi, ni;
     block_order(t - pre[g], (int)((a1 - a0 + 255) / 256), ntn, mi, ni);
     const int64_t row0 = a0 + (int64_t)mi * 256;
-    const int rows = (int)(a1 - row0 < 256 ? a1 - row0 : 256);
-    const int64_t n0 = (int64_t)ni * kBN;
-    auto store = [&](const auto& acc, int wave, int lane) {
-      store_rows<OutT>(lsm, acc, wave, lane, wave / WN, rows,
-                       static_cast<OutT*>(p.y) + row0 * p.N + n0 + (wave % WN) * (32 * R::TN), p.N);
-    };
-    const int tm = (rows + 63) / 64;
-    if (tm == 4) tile<4, WN>(lsm, p, g, row0, rows, n0, store);
-    else if (tm == 3) tile<3, WN>(lsm, p, g, row0, rows, n0, store);
-    else if (tm == 2) tile<2, WN>(lsm, p, g, row0, rows, n0, store);
-    else tile<1, WN>(lsm, p, g, row0, rows, n0, store);
-    __syncthreads();                        // the staging is the next tile's ring
+    return Tile{g, (int)(a1 - row0 < 256 ? a1 - row0 : 256), row0, (int64_t)ni * kBN};
+  };
+  int v = (int)blockIdx.x;
+  if (v >= total) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Tile t = locate(v);
+  Loads ld;
+  ld.init(p, t, threadIdx.x & 63, wave);
+  ld.scales(lsm, p, 0, wave);
+  ld.codes<4>(lsm, p, 0, wave);
+  bool stored = false;                      // a whole tile's rows since the first stage's loads
+  for (;;) {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));          // per tile: nothing derived from it is held across tiles
+    ld.codes<4>(lsm, p, 1, wave);
+    // the first stage: all but the second one's loads, and the stores between
+    // them (of a whole tile; of a partial one some may not have been issued)
+    if (stored) wait_barrier<8 + kStores<OutT>>();
+    else wait_barrier<8>();
+    f32x16 acc[4][kTN];
+    const int tm = (t.rows + 63) / 64;
+    if (tm == 4) products<4>(lsm, p, ld, lane, wave, acc);
+    else if (tm == 3) products<3>(lsm, p, ld, lane, wave, acc);
+    else if (tm == 2) products<2>(lsm, p, ld, lane, wave, acc);
+    else products<1>(lsm, p, ld, lane, wave, acc);
+    const Tile done = t;
+    stored = done.rows == 256;
+    v += (int)gridDim.x;
+    if (v < total) {
+      t = locate(v);
+      ld.init(p, t, lane, wave);
+      ld.scales(lsm, p, 0, wave);
+      ld.codes<4>(lsm, p, 0, wave);
+    }
+    OutT* y = static_cast<OutT*>(p.y) + done.row0 * p.N + done.n0 + (wave % kWN) * (32 * kTN);
+    if (tm == 4) store_rows<OutT, 4>(lsm, acc, lane, wave, done.rows, y, p.N);
+    else if (tm == 3) store_rows<OutT, 3>(lsm, acc, lane, wave, done.rows, y, p.N);
+    else if (tm == 2) store_rows<OutT, 2>(lsm, acc, lane, wave, done.rows, y, p.N);
+    else store_rows<OutT, 1>(lsm, acc, lane, wave, done.rows, y, p.N);
+    if (v >= total) return;
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the staging is read
   }
 }
 
 constexpr size_t kMaxPre = 16128;          // the tile-count scan: G <= 4000
 
-template <bool OUT_BF16, int WN>
+template <bool OUT_BF16>
 hipError_t tiles(const Gemm& p, int64_t most, hipStream_t stream) {
   static bool done = false;
-  auto k = k_mxfp4_tiles<OUT_BF16, WN>;
-  constexpr size_t lds = Ring<WN>::LDS;
-  static_assert(lds + kMaxPre + 256 <= 160 * 1024, "LDS");
+  auto k = k_mxfp4_tiles<OUT_BF16>;
+  static_assert(kLds + kMaxPre + 256 <= 160 * 1024, "LDS");
   if (!done) {
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k),
                                        hipFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(lds + kMaxPre));
+                                       (int)(kLds + kMaxPre));
     if (e != hipSuccess) return e;
     done = true;
   }
   const int64_t grid = most < device_cu_count() ? most : device_cu_count();
   const size_t pre = ((size_t)(p.G + 1) * 4 + 15) & ~(size_t)15;
-  k<<<(unsigned)grid, 128 * WN, lds + pre, stream>>>(p);
+  k<<<(unsigned)grid, 64 * kWaves, kLds + pre, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -423,7 +459,7 @@ hipError_t launch_fwd_mxfp4(const uint8_t* ac, const uint8_t* as, int64_t a_rows
   if (N % kBN == 0 && m_cap > 128 * (int64_t)G && a_bytes < (int64_t)1 << 31) {
     const Gemm p{ac, as, bc, bs, row_token, offsets, a_rows, N, K, y, G};
     const int64_t most = ((m_cap + 255) / 256 + G) * (N / kBN);
-    return y_bf16 ? tiles<true, 4>(p, most, stream) : tiles<false, 4>(p, most, stream);
+    return y_bf16 ? tiles<true>(p, most, stream) : tiles<false>(p, most, stream);
   }
   const int64_t tiles = ((m_cap + 31) / 32 + G) * (N / 128);
   auto k = y_bf16 ? k_mxfp4_small<true> : k_mxfp4_small<false>;
