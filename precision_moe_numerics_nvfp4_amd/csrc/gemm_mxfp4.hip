@@ -183,24 +183,29 @@ struct Loads {
     const int64_t q = of_a ? row_of(r) : r;
     os = q < 0 ? kAway : (uint32_t)(q * lds_);
   }
-  // The codes of stage s. The range check covers the vector offset alone, and
-  // the scalar one (the place in the row, B's rows) stays inside the operand
-  // where that passes; elements past a row's end are zeros.
-  template <int TM>
-  __device__ __forceinline__ void codes(uint8_t* lsm, const Gemm& p, int s, int wave) const {
-    uint8_t* st = lsm + (s & 1) * kStage + wave * 1024;
+  // Load i of A's codes of stage s, and of B's. The range check covers the
+  // vector offset alone, and the scalar one (the place in the row, B's rows)
+  // stays inside the operand where that passes; elements past a row's end are
+  // zeros.
+  __device__ __forceinline__ void a(uint8_t* lsm, int s, int wave, int i) const {
     const uint32_t k = (uint32_t)s * (uint32_t)kRB;
-    const bool real = (int)k < end;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        ra, (lds_void*)(lsm + (s & 1) * kStage + (kWaves * i + wave) * 1024), 16,
+        (int)k < end ? oa[i] : kAway, k, 0, 0);
+  }
+  __device__ __forceinline__ void b(uint8_t* lsm, const Gemm& p, int s, int wave, int i) const {
+    const uint32_t k = (uint32_t)s * (uint32_t)kRB;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rb, (lds_void*)(lsm + (s & 1) * kStage + 256 * kRB + (kWaves * i + wave) * 1024), 16,
+        (int)k < end ? ob : kAway, k + (uint32_t)(8 * kWaves * i) * (uint32_t)(p.K / 2), 0, 0);
+  }
+  // The first loads of a tile: the scales of block 0, the codes of stage 0.
+  __device__ __forceinline__ void first(uint8_t* lsm, const Gemm& p, int wave) const {
+    scales(lsm, p, 0, wave);
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + kWaves * i * 1024), 16,
-                                               real ? oa[i] : kAway, k, 0, 0);
-    const uint32_t o = real ? ob : kAway;
+    for (int i = 0; i < 4; ++i) a(lsm, 0, wave, i);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rb, (lds_void*)(st + 256 * kRB + kWaves * i * 1024), 16, o,
-          k + (uint32_t)(8 * kWaves * i) * (uint32_t)(p.K / 2), 0, 0);
+    for (int i = 0; i < 4; ++i) b(lsm, p, 0, wave, i);
   }
   // The scales of stages 2 b and 2 b + 1 (those behind the row's end belong to
   // codes of zero).
@@ -212,8 +217,8 @@ struct Loads {
   }
 };
 
-// The products of a tile of 64 TM rows whose first loads (scales of block 0,
-// codes of stages 0 and 1) are on their way, the second stage's last. A
+// The products of a tile of 64 TM rows whose first stage is in LDS and whose
+// second stage's loads of A are on their way. A
 // wavefront's row block i is block 2 i + wm of the tile (so that the rows of a
 // partial tile spread over all of them), its columns the 64 from 64 wn.
 template <int TM>
@@ -267,8 +272,9 @@ __device__ __forceinline__ void products(uint8_t* lsm, const Gemm& p, const Load
 
   // The products of step T of a stage, and the reads of the next step's
   // fragments (of the next stage after the last step, and of the next scale
-  // block after that block's last stage).
-  auto step = [&](auto at, int s_next, int scale_block) {
+  // block after that block's last stage). load(i) follows the products of row
+  // block i.
+  auto step = [&](auto at, int s_next, int scale_block, auto load) {
     constexpr int T = decltype(at)::value, S = T & 1, NX = (T + 1) % 4;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -278,6 +284,7 @@ __device__ __forceinline__ void products(uint8_t* lsm, const Gemm& p, const Load
         // columns first: a lane then holds four consecutive columns of a row
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
             wide(B[S][j]), wide(A[i]), acc[i][j], 4, 4, 2 * S, (int)cb[j], 2 * S, (int)ca[i]);
+      load(i);
       read_a(i, s_next, NX);
       if (i < TN) read_b(1 - S, i, s_next, NX);
       if constexpr (T == 3)
@@ -294,7 +301,9 @@ __device__ __forceinline__ void products(uint8_t* lsm, const Gemm& p, const Load
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  // Stage 2 b + Q.
+  // Stage 2 b + Q. The loads into the buffer of the stage before it, free since
+  // that stage's barrier, follow its products one by one: A's in that stage's
+  // last step, B's in this one's first (eight at once hold up all wavefronts).
   auto stage = [&](int b, auto at) {
     constexpr int Q = decltype(at)::value;
     const int s = 2 * b + Q;
@@ -305,14 +314,17 @@ __device__ __forceinline__ void products(uint8_t* lsm, const Gemm& p, const Load
       for (int j = 0; j < TN; ++j) cb[j] = sB[j][d] >> (8 * half);
     };
     shift(2 * Q);
-    step(std::integral_constant<int, 0>{}, s, -1);
-    step(std::integral_constant<int, 1>{}, s, -1);
+    step(std::integral_constant<int, 0>{}, s, -1, [&](int i) {
+#pragma unroll
+      for (int d = i * 4 / TM; d < (i + 1) * 4 / TM; ++d) ld.b(lsm, p, s + 1, wave, d);
+    });
+    step(std::integral_constant<int, 1>{}, s, -1, [](int) {});
     shift(2 * Q + 1);
-    step(std::integral_constant<int, 2>{}, s, -1);
+    step(std::integral_constant<int, 2>{}, s, -1, [](int) {});
     wait_barrier<0>();
     if constexpr (Q == 0) ld.scales(lsm, p, b + 1, wave);
-    ld.codes<TM>(lsm, p, s + 2, wave);
-    step(std::integral_constant<int, 3>{}, s + 1, Q == 1 ? b + 1 : -1);
+    step(std::integral_constant<int, 3>{}, s + 1, Q == 1 ? b + 1 : -1,
+         [&](int i) { ld.a(lsm, s + 2, wave, i); });
   };
   const int nb = ns / 2;
   for (int b = 0; b < nb; ++b) {
@@ -393,17 +405,17 @@ __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
   Tile t = locate(v);
   Loads ld;
   ld.init(p, t, threadIdx.x & 63, wave);
-  ld.scales(lsm, p, 0, wave);
-  ld.codes<4>(lsm, p, 0, wave);
+  ld.first(lsm, p, wave);
   bool stored = false;                      // a whole tile's rows since the first stage's loads
   for (;;) {
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));          // per tile: nothing derived from it is held across tiles
-    ld.codes<4>(lsm, p, 1, wave);
-    // the first stage: all but the second one's loads, and the stores between
-    // them (of a whole tile; of a partial one some may not have been issued)
-    if (stored) wait_barrier<8 + kStores<OutT>>();
-    else wait_barrier<8>();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ld.a(lsm, 1, wave, i);
+    // the first stage: all but these loads, and the stores between them (of a
+    // whole tile; of a partial one some may not have been issued)
+    if (stored) wait_barrier<4 + kStores<OutT>>();
+    else wait_barrier<4>();
     f32x16 acc[4][kTN];
     const int tm = (t.rows + 63) / 64;
     if (tm == 4) products<4>(lsm, p, ld, lane, wave, acc);
@@ -416,8 +428,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
     if (v < total) {
       t = locate(v);
       ld.init(p, t, lane, wave);
-      ld.scales(lsm, p, 0, wave);
-      ld.codes<4>(lsm, p, 0, wave);
+      ld.first(lsm, p, wave);
     }
     OutT* y = static_cast<OutT*>(p.y) + done.row0 * p.N + done.n0 + (wave % kWN) * (32 * kTN);
     if (tm == 4) store_rows<OutT, 4>(lsm, acc, lane, wave, done.rows, y, p.N);
