@@ -276,9 +276,9 @@ __device__ __forceinline__ void products(uint8_t* lsm, const Gemm& p, const Load
   // block i.
   auto step = [&](auto at, int s_next, int scale_block, auto load) {
     constexpr int T = decltype(at)::value, S = T & 1, NX = (T + 1) % 4;
-    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
+      __builtin_amdgcn_sched_barrier(0);    // reads and loads stay where they are written
 #pragma unroll
       for (int j = 0; j < TN; ++j)
         // columns first: a lane then holds four consecutive columns of a row
@@ -378,9 +378,17 @@ __device__ __forceinline__ void store_rows(uint8_t* lsm, const f32x16 (&acc)[4][
 template <typename OutT>
 constexpr int kStores = 8 * sizeof(OutT);   // of a wavefront and whole tile: 128 x 64 in 16 bytes a lane
 
-// One workgroup per compute unit, each taking tiles v, v + gridDim.x, ... The
-// loads of a tile's first stage go out before the rows of the tile before it
-// are written.
+// One workgroup per compute unit. The tiles are split into eight contiguous
+// ranges, one per XCD (workgroup w runs on XCD w % 8), whose workgroups take
+// theirs a round at a time: those an XCD runs together share rows of both
+// operands in its L2. (Lower tiles last, for an even load, measured slower: the
+// weights are then read twice.) What is left for a last round after at most four
+// whole ones goes by halves or quarters of its rows, where that gives no
+// workgroup a second piece: 8 x 1024 rows, 1024 -> 2048, one round and an eighth
+// 29.5 -> 26.2 us, 31000 rows over 48 groups, 4096 -> 1536, three and a half
+// 136.9 -> 134.9 us; after nine rounds, whose ends lie further apart than a
+// tile takes, it lost (1536 -> 4096 164 -> 169 us). The loads of a tile's first
+// stage go out before the rows of the tile before it are written.
 template <bool OUT_BF16>
 __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lsm[];
@@ -389,20 +397,34 @@ __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
   const int ntn = (int)(p.N / kBN);
   tile_prefix(p.G, [&](int e) { return (int)((p.offsets[e + 1] - p.offsets[e] + 255) / 256) * ntn; }, pre);
   const int total = pre[p.G];
-  auto locate = [&](int v) {
-    const int x = v & 7, q8 = total >> 3, r8 = total & 7;
-    const int t = x * q8 + (x < r8 ? x : r8) + (v >> 3);     // contiguous tiles to an XCD
-    const int g = tile_group(pre, p.G, t);
-    const int64_t a0 = p.offsets[g], a1 = p.offsets[g + 1];
+  const int x = blockIdx.x & 7, place = blockIdx.x >> 3;
+  const int wide = (int)gridDim.x >> 3;     // workgroups on this XCD
+  const int first = (int)((int64_t)total * x / 8), n = (int)((int64_t)total * (x + 1) / 8) - first;
+  const int whole = n / wide * wide, left = n - whole;
+  const int cut = whole > 4 * wide ? 1 : 4 * left <= wide ? 4 : 2 * left <= wide ? 2 : 1;
+  auto locate = [&](int round, Tile& t) {
+    int at = round * wide + place, skip = 0;
+    if (at >= whole) {
+      const int piece = at - whole;
+      if (piece >= left * cut) return false;
+      at = whole + piece / cut;
+      skip = piece % cut * (256 / cut);
+    }
+    at += first;
+    t.g = tile_group(pre, p.G, at);
+    const int64_t a0 = p.offsets[t.g], a1 = p.offsets[t.g + 1];
     int mi, ni;
-    block_order(t - pre[g], (int)((a1 - a0 + 255) / 256), ntn, mi, ni);
-    const int64_t row0 = a0 + (int64_t)mi * 256;
-    return Tile{g, (int)(a1 - row0 < 256 ? a1 - row0 : 256), row0, (int64_t)ni * kBN};
+    block_order(at - pre[t.g], (int)((a1 - a0 + 255) / 256), ntn, mi, ni);
+    const int most = at - first >= whole ? 256 / cut : 256;
+    t.row0 = a0 + (int64_t)mi * 256 + skip;
+    t.rows = (int)(a1 - t.row0 < most ? a1 - t.row0 : most);
+    t.n0 = (int64_t)ni * kBN;
+    return t.rows > 0;
   };
-  int v = (int)blockIdx.x;
-  if (v >= total) return;
+  int round = 0;
+  Tile t;
+  if (!locate(round, t)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  Tile t = locate(v);
   Loads ld;
   ld.init(p, t, threadIdx.x & 63, wave);
   ld.first(lsm, p, wave);
@@ -424,9 +446,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
     else products<1>(lsm, p, ld, lane, wave, acc);
     const Tile done = t;
     stored = done.rows == 256;
-    v += (int)gridDim.x;
-    if (v < total) {
-      t = locate(v);
+    const bool more = locate(++round, t);
+    if (more) {
       ld.init(p, t, lane, wave);
       ld.first(lsm, p, wave);
     }
@@ -435,7 +456,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
     else if (tm == 3) store_rows<OutT, 3>(lsm, acc, lane, wave, done.rows, y, p.N);
     else if (tm == 2) store_rows<OutT, 2>(lsm, acc, lane, wave, done.rows, y, p.N);
     else store_rows<OutT, 1>(lsm, acc, lane, wave, done.rows, y, p.N);
-    if (v >= total) return;
+    if (!more) return;
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the staging is read
   }
 }
@@ -454,7 +475,9 @@ hipError_t tiles(const Gemm& p, int64_t most, hipStream_t stream) {
     if (e != hipSuccess) return e;
     done = true;
   }
-  const int64_t grid = most < device_cu_count() ? most : device_cu_count();
+  // a multiple of eight workgroups: every XCD's range has some
+  const int64_t cus = device_cu_count() / 8 * 8, upto = (most + 7) / 8 * 8;
+  const int64_t grid = upto < cus ? upto : cus;
   const size_t pre = ((size_t)(p.G + 1) * 4 + 15) & ~(size_t)15;
   k<<<(unsigned)grid, 64 * kWaves, kLds + pre, stream>>>(p);
   return hipGetLastError();
