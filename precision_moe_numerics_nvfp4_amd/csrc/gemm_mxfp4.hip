@@ -26,10 +26,13 @@ __device__ __forceinline__ i32x8 frag(const uint4 v) {
   return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
 }
 
-// 32 rows x 128 columns per workgroup, a wavefront to 32 columns, fragments
-// straight from global memory.
+// Gathered activations of 2 GiB and more, past the 32-bit offsets of the tiles
+// below: 32 rows x 128 columns per workgroup, a wavefront to 32 columns,
+// fragments straight from global memory. (For all else the tiles are faster, a
+// few rows to a group included: 506 rows over 48 groups, 4096 -> 1536, 49.7 us
+// against 78.)
 template <bool OUT_BF16>
-__global__ __launch_bounds__(256) void k_mxfp4_small(
+__global__ __launch_bounds__(256) void k_mxfp4_wide(
     const uint8_t* __restrict__ ac, const uint8_t* __restrict__ as, int64_t a_rows,
     const int32_t* __restrict__ row_token, const uint8_t* __restrict__ bc,
     const uint8_t* __restrict__ bs, const int64_t* __restrict__ offsets, int G, int64_t N,
@@ -136,9 +139,10 @@ struct Gemm {
   int G;
 };
 
-// A tile's place: rows row0 .. row0 + rows - 1 of group g, columns from n0.
+// A tile's place: rows row0 .. row0 + rows - 1 of group g, cols (256, or 128 at
+// the end of an odd N / 128) columns from n0.
 struct Tile {
-  int g, rows;
+  int g, rows, cols;
   int64_t row0, n0;
 };
 
@@ -147,7 +151,7 @@ struct Tile {
 // operand, and a lane's piece is the same in all of them.
 struct Loads {
   __amdgpu_buffer_rsrc_t ra, rb, rs;        // codes of A and B, scales of the rows it loads
-  uint32_t oa[4], ob, os;                   // byte offsets
+  uint32_t oa[4], ob, ob2, os;              // byte offsets (B: its first and second 128 rows)
   int end;                                  // stage offsets below it are inside the row
 
   __device__ __forceinline__ void init(const Gemm& p, const Tile& t, int lane, int wave) {
@@ -160,10 +164,10 @@ struct Loads {
           kBufferWord3);
     };
     ra = rsrc(p.ac + a_base * ldq, a_n * ldq);
-    rb = rsrc(p.bc + b_base * ldq, (int64_t)kBN * ldq);
+    rb = rsrc(p.bc + b_base * ldq, (int64_t)t.cols * ldq);
     const bool of_a = wave < kWaves / 2;    // 64 rows' scales a wavefront: A's, or B's
     rs = of_a ? rsrc(p.as + a_base * lds_, a_n * lds_)
-              : rsrc(p.bs + b_base * lds_, (int64_t)kBN * lds_);
+              : rsrc(p.bs + b_base * lds_, (int64_t)t.cols * lds_);
     // the row of A that tile row r reads, or -1
     auto row_of = [&](int r) -> int64_t {
       if (r >= t.rows) return -1;
@@ -178,9 +182,10 @@ struct Loads {
       oa[i] = q < 0 ? kAway : (uint32_t)(q * ldq) + 16u * piece;
     }
     ob = (uint32_t)(8 * wave + (lane >> 3)) * ldq + 16u * piece;
+    ob2 = t.cols > 128 ? ob : kAway;
     end = (int)ldq - 16 * piece;
     const int r = 64 * (wave % kWN) + lane;
-    const int64_t q = of_a ? row_of(r) : r;
+    const int64_t q = of_a ? row_of(r) : r < t.cols ? r : -1;
     os = q < 0 ? kAway : (uint32_t)(q * lds_);
   }
   // Load i of A's codes of stage s, and of B's. The range check covers the
@@ -197,7 +202,8 @@ struct Loads {
     const uint32_t k = (uint32_t)s * (uint32_t)kRB;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         rb, (lds_void*)(lsm + (s & 1) * kStage + 256 * kRB + (kWaves * i + wave) * 1024), 16,
-        (int)k < end ? ob : kAway, k + (uint32_t)(8 * kWaves * i) * (uint32_t)(p.K / 2), 0, 0);
+        (int)k < end ? (i < 2 ? ob : ob2) : kAway,
+        k + (uint32_t)(8 * kWaves * i) * (uint32_t)(p.K / 2), 0, 0);
   }
   // The first loads of a tile: the scales of block 0, the codes of stage 0.
   __device__ __forceinline__ void first(uint8_t* lsm, const Gemm& p, int wave) const {
@@ -394,7 +400,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lsm[];
   using OutT = std::conditional_t<OUT_BF16, uint16_t, float>;
   int* pre = reinterpret_cast<int*>(lsm + kLds);
-  const int ntn = (int)(p.N / kBN);
+  const int ntn = (int)((p.N + kBN - 1) / kBN);
   tile_prefix(p.G, [&](int e) { return (int)((p.offsets[e + 1] - p.offsets[e] + 255) / 256) * ntn; }, pre);
   const int total = pre[p.G];
   const int x = blockIdx.x & 7, place = blockIdx.x >> 3;
@@ -419,6 +425,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
     t.row0 = a0 + (int64_t)mi * 256 + skip;
     t.rows = (int)(a1 - t.row0 < most ? a1 - t.row0 : most);
     t.n0 = (int64_t)ni * kBN;
+    t.cols = p.N - t.n0 < kBN ? 128 : kBN;
     return t.rows > 0;
   };
   int round = 0;
@@ -445,14 +452,15 @@ __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
     else if (tm == 2) products<2>(lsm, p, ld, lane, wave, acc);
     else products<1>(lsm, p, ld, lane, wave, acc);
     const Tile done = t;
-    stored = done.rows == 256;
+    stored = done.rows == 256 && done.cols == kBN;
     const bool more = locate(++round, t);
     if (more) {
       ld.init(p, t, lane, wave);
       ld.first(lsm, p, wave);
     }
     OutT* y = static_cast<OutT*>(p.y) + done.row0 * p.N + done.n0 + (wave % kWN) * (32 * kTN);
-    if (tm == 4) store_rows<OutT, 4>(lsm, acc, lane, wave, done.rows, y, p.N);
+    if ((wave % kWN) * (32 * kTN) >= done.cols) {
+    } else if (tm == 4) store_rows<OutT, 4>(lsm, acc, lane, wave, done.rows, y, p.N);
     else if (tm == 3) store_rows<OutT, 3>(lsm, acc, lane, wave, done.rows, y, p.N);
     else if (tm == 2) store_rows<OutT, 2>(lsm, acc, lane, wave, done.rows, y, p.N);
     else store_rows<OutT, 1>(lsm, acc, lane, wave, done.rows, y, p.N);
@@ -490,13 +498,13 @@ hipError_t launch_fwd_mxfp4(const uint8_t* ac, const uint8_t* as, int64_t a_rows
                             const int64_t* offsets, int G, int64_t m_cap, int64_t N, int64_t K,
                             void* y, bool y_bf16, hipStream_t stream) {
   const int64_t a_bytes = (row_token ? a_rows : 256) * (K / 2);
-  if (N % kBN == 0 && m_cap > 128 * (int64_t)G && a_bytes < (int64_t)1 << 31) {
+  if (a_bytes < (int64_t)1 << 31) {
     const Gemm p{ac, as, bc, bs, row_token, offsets, a_rows, N, K, y, G};
-    const int64_t most = ((m_cap + 255) / 256 + G) * (N / kBN);
+    const int64_t most = ((m_cap + 255) / 256 + G) * ((N + kBN - 1) / kBN);
     return y_bf16 ? tiles<true>(p, most, stream) : tiles<false>(p, most, stream);
   }
   const int64_t tiles = ((m_cap + 31) / 32 + G) * (N / 128);
-  auto k = y_bf16 ? k_mxfp4_small<true> : k_mxfp4_small<false>;
+  auto k = y_bf16 ? k_mxfp4_wide<true> : k_mxfp4_wide<false>;
   k<<<(unsigned)tiles, 256, 0, stream>>>(ac, as, a_rows, row_token, bc, bs, offsets, G, N, K, y);
   return hipGetLastError();
 }

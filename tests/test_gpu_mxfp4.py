@@ -393,3 +393,28 @@ def test_refusals(nv):
         nv.moe_group(z(4, 2, dt=torch.int32), 0, 1025)
     with pytest.raises(ValueError):
         nv.moe_group(z(4, 2, dt=torch.int32), 1 << 33, 8)
+
+
+def test_product_gathers_past_32_bits(nv):
+    """Activations of more than 2 GiB: rows at both ends of them."""
+    import torch
+    T, K, N, G = 1050000, 4096, 128, 2
+    codes = torch.zeros(T, K // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.full((T, K // 32), 127, dtype=torch.uint8, device="cuda")
+    assert codes.numel() > 1 << 31
+    rng = np.random.default_rng(17)
+    tok = np.array([0, T - 1, 1048577, 5, T - 2, 1048575], np.int32)
+    a = M4.quantize(rng.normal(size=(6, K)).astype(np.float32))
+    codes[to_dev(tok.astype(np.int64))], scales[to_dev(tok.astype(np.int64))] = to_dev(a[0]), to_dev(a[1])
+    b = M4.quantize((rng.normal(size=(G * N, K)) * 0.02).astype(np.float32))
+    off = np.array([0, 2, 6])
+    y = nv.moe_fwd_grouped_gemm_mxfp4(codes, scales, to_dev(b[0]), to_dev(b[1]), to_dev(off), row_token=to_dev(tok))
+    ref, mag = M4.fwd_grouped(a, b, off, N)
+    assert (np.abs(from_dev(y) - ref) <= (K / 32 + 1) * 2.0 ** -23 * mag).all()
+    # in place, the tile's own rows are addressed: the last ones lie past 2 GiB too
+    off = np.array([0, 1048570, T])
+    y = nv.moe_fwd_grouped_gemm_mxfp4(codes, scales, to_dev(b[0]), to_dev(b[1]), to_dev(off), out_dtype=torch.bfloat16)
+    for r, i in ((T - 1, 1), (1048577, 2), (5, 3)):
+        ref, mag = M4.fwd_grouped((a[0][i:i + 1], a[1][i:i + 1]), tuple(v[(r >= 1048570) * N:][:N] for v in b), [0, 1], N)
+        d = np.abs(y[r].double().cpu().numpy() - ref[0])
+        assert (d <= (K / 32 + 1) * 2.0 ** -23 * mag[0] + 2.0 ** -8 * np.abs(ref[0])).all()
