@@ -389,7 +389,8 @@ constexpr int kStores = 8 * sizeof(OutT);   // of a wavefront and whole tile: 12
 // theirs a round at a time: those an XCD runs together share rows of both
 // operands in its L2. (Lower tiles last, for an even load, measured slower: the
 // weights are then read twice.) What is left for a last round after at most four
-// whole ones goes by halves or quarters of its rows, where that gives no
+// whole ones goes by halves or quarters of its rows (by halves of the columns
+// where there are few rows), where that gives no
 // workgroup a second piece: 8 x 1024 rows, 1024 -> 2048, one round and an eighth
 // 29.5 -> 26.2 us, 31000 rows over 48 groups, 4096 -> 1536, three and a half
 // 136.9 -> 134.9 us; after nine rounds, whose ends lie further apart than a
@@ -409,24 +410,32 @@ __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
   const int whole = n / wide * wide, left = n - whole;
   const int cut = whole > 4 * wide ? 1 : 4 * left <= wide ? 4 : 2 * left <= wide ? 2 : 1;
   auto locate = [&](int round, Tile& t) {
-    int at = round * wide + place, skip = 0;
+    int at = round * wide + place, piece = 0, pieces = 1;
     if (at >= whole) {
-      const int piece = at - whole;
+      piece = at - whole;
       if (piece >= left * cut) return false;
       at = whole + piece / cut;
-      skip = piece % cut * (256 / cut);
+      piece %= cut;
+      pieces = cut;
     }
     at += first;
     t.g = tile_group(pre, p.G, at);
     const int64_t a0 = p.offsets[t.g], a1 = p.offsets[t.g + 1];
     int mi, ni;
     block_order(at - pre[t.g], (int)((a1 - a0 + 255) / 256), ntn, mi, ni);
-    const int most = at - first >= whole ? 256 / cut : 256;
-    t.row0 = a0 + (int64_t)mi * 256 + skip;
-    t.rows = (int)(a1 - t.row0 < most ? a1 - t.row0 : most);
+    t.row0 = a0 + (int64_t)mi * 256;
     t.n0 = (int64_t)ni * kBN;
+    t.rows = (int)(a1 - t.row0 < 256 ? a1 - t.row0 : 256);
     t.cols = p.N - t.n0 < kBN ? 128 : kBN;
-    return t.rows > 0;
+    if (pieces > 1 && t.rows <= 64) {       // two halves of the columns
+      t.n0 += 128 * piece;
+      t.cols = piece * 128 < t.cols ? 128 : 0;
+    } else if (pieces > 1) {                // of the rows
+      const int most = 256 / pieces, from = piece * most;
+      t.row0 += from;
+      t.rows = t.rows - from < most ? t.rows - from : most;
+    }
+    return t.rows > 0 && t.cols > 0;
   };
   int round = 0;
   Tile t;
