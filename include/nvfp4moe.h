@@ -703,7 +703,7 @@ NVFP4MOE_API int mxfp8_requant_sr_mxfp4(const uint8_t* codes, const uint8_t* sca
                            void* stream);
 
 /* Bytes of device workspace moe_ffn_tokens needs (0 for sizes it refuses). */
-NVFP4MOE_API size_t nvfp4moe_ffn_tokens_workspace_size(int64_t T, int k, int64_t F);
+NVFP4MOE_API size_t nvfp4moe_ffn_tokens_workspace_size(int64_t T, int k, int64_t K, int64_t F);
 
 /*
  * The whole expert layer for a few tokens (decoding): routing, both

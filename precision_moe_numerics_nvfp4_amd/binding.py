@@ -83,7 +83,7 @@ SIGNATURES = {
                                     _p, _c_int, _p], _c_int),
     "mxfp8_requant_sr_mxfp4": ([_p, _p, _c_i64, _c_i64, _p, _c_i64, _p, _p, _c_int, _c_i64, _c_u64,
                                 _c_u32, _p, _p, _p], _c_int),
-    "nvfp4moe_ffn_tokens_workspace_size": ([_c_i64, _c_int, _c_i64], _c_size),
+    "nvfp4moe_ffn_tokens_workspace_size": ([_c_i64, _c_int, _c_i64, _c_i64], _c_size),
     "moe_ffn_tokens": ([_p, _p, _c_int, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_f32, _p, _p,
                         _c_int, _p, _p, _p, _p, _p, _p, _c_int, _c_int, _c_i64, _c_i64, _c_int,
                         _c_int, _p, _p, _p, _c_int, _p, _c_size, _p], _c_int),
@@ -1149,8 +1149,8 @@ def mxfp8_requant_sr_mxfp4(codes, scales, offsets, padded_offsets, P, seed, tag,
 
 
 @functools.lru_cache(maxsize=256)
-def ffn_tokens_workspace_size(T, k, F):
-    return int(lib().nvfp4moe_ffn_tokens_workspace_size(int(T), int(k), int(F)))
+def ffn_tokens_workspace_size(T, k, K, F):
+    return int(lib().nvfp4moe_ffn_tokens_workspace_size(int(T), int(k), int(K), int(F)))
 
 
 def _weight(w, name, dev):
@@ -1192,7 +1192,7 @@ def moe_ffn_tokens(x, logits, k, w1, w2, act="silu", gated=False, score="softmax
     through ``act``, its last F multiply them) and w2 [n_local*K, F], each
     (codes, scales) in MXFP4 or (codes, scales, outer) in NVFP4, of the experts
     [e0, e0+n_local). act 'none', 'relu2' or 'silu'. ``out`` may hold any of the
-    results' buffers; ``workspace`` ffn_tokens_workspace_size(T, k, F) bytes,
+    results' buffers; ``workspace`` ffn_tokens_workspace_size(T, k, K, F) bytes,
     of one call at a time."""
     torch = _torch()
     _dev(x, "x", torch.bfloat16, 2)
@@ -1231,7 +1231,7 @@ def moe_ffn_tokens(x, logits, k, w1, w2, act="silu", gated=False, score="softmax
         if isinstance(token_mask, torch.Tensor) and token_mask.dtype == torch.bool:
             token_mask = token_mask.view(torch.uint8)
         token_mask = _on(token_mask, "token_mask", torch.uint8, (T,), dev)
-    ws, ws_bytes = _workspace(workspace, ffn_tokens_workspace_size(T, k, F), dev)
+    ws, ws_bytes = _workspace(workspace, ffn_tokens_workspace_size(T, k, K, F), dev)
     _launch(dev, "moe_ffn_tokens", x.data_ptr(), logits.data_ptr(), _in_dtype(logits), T, E, k,
             _score(score), 1 if renorm else 0, _number(scale, "scale"), bias, token_mask,
             _FORMATS[len(w1)], c1, s1, o1, c2, s2, o2, e0, n_local, K, F, _ACTS[act],

@@ -633,11 +633,11 @@ int mxfp8_requant_sr_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t 
                                             out_e4m3, out_e8m0, as_stream(stream)));
 }
 
-size_t nvfp4moe_ffn_tokens_workspace_size(int64_t T, int k, int64_t F) {
-  if (T < 0 || k <= 0 || F < 0 || T > kTokensMaxT || k > kTokensMaxK || T * k > kTokensMaxPairs ||
-      F > kMaxTokensWidth)
+size_t nvfp4moe_ffn_tokens_workspace_size(int64_t T, int k, int64_t K, int64_t F) {
+  if (T < 0 || k <= 0 || K < 0 || F < 0 || T > kTokensMaxT || k > kTokensMaxK || T * k > kTokensMaxPairs ||
+      K > kMaxTokensWidth || F > kMaxTokensWidth)
     return 0;
-  return tokens_workspace_bytes(T, k, F);
+  return tokens_workspace_bytes(T, k, K, F);
 }
 
 int moe_ffn_tokens(const void* x, const void* logits, int logits_dtype, int64_t T, int E, int k,
@@ -671,7 +671,7 @@ int moe_ffn_tokens(const void* x, const void* logits, int logits_dtype, int64_t 
               aligned(w1_outer, 4) && aligned(w2_outer, 4) && aligned(topk_ids, 4) &&
               aligned(gate, 4),
           NVFP4MOE_EUNSUPPORTED);
-  REQUIRE(workspace_bytes >= tokens_workspace_bytes(T, k, F), NVFP4MOE_EWORKSPACE);
+  REQUIRE(workspace_bytes >= tokens_workspace_bytes(T, k, K, F), NVFP4MOE_EWORKSPACE);
   TokensArgs a;
   a.x = x;
   a.logits = logits;

@@ -167,7 +167,7 @@ struct TokensArgs {
   bool out_bf16;
   uint8_t* ws;
 };
-size_t tokens_workspace_bytes(int64_t T, int k, int64_t F);
+size_t tokens_workspace_bytes(int64_t T, int k, int64_t K, int64_t F);
 hipError_t launch_ffn_tokens(const TokensArgs& a, hipStream_t stream);
 
 // gemm_bwd.hip

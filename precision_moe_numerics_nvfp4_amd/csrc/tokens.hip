@@ -16,15 +16,18 @@
 // expert's weights are read once.
 //
 // k_tokens_up: every workgroup repeats the selection (a wavefront per token;
-// reading a result of another launch would cost more), lists the pairs of each
-// local expert, then takes (expert, 16 rows of W1) units; its wavefronts split
-// the contraction and join through LDS.
-// k_tokens_down: a workgroup takes 16 rows of W2 for every selected expert; its
-// wavefronts split (expert, contraction) and join once at the end. A column of
-// B is a token, so pairs of one token in several experts add up in the
-// accumulators; gates and W2's outer scales were multiplied into h before.
+// reading a result of another launch would cost more) and lists the pairs of
+// each local expert. A wavefront's piece of work is 16 RS rows of W1 by 256
+// elements, loaded while the piece before it is multiplied; the wavefronts that
+// share rows split the contraction and join through LDS.
+// k_tokens_down: a workgroup takes 16 rows of W2 for every selected expert, its
+// wavefronts split (expert, contraction). A column of a product is a pair; each
+// wavefront adds its columns to its own copy of the output rows in LDS, and the
+// copies are added at the end. Gates and W2's outer scales were multiplied into
+// h before.
 #include "codecs.hpp"
 #include "internal.hpp"
+#include "lanes.hpp"
 
 namespace nvfp4moe {
 
@@ -39,32 +42,42 @@ typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 1024;
 constexpr int kWavesT = kThreads / 64;
 constexpr int kMaxExperts = 1024;
+// Up to so many tokens every workgroup selects by itself; beyond, a launch before does.
+constexpr int kSelectHere = 16;
 constexpr float kNegInfT = -__builtin_huge_valf();
 
-// Workspace: what k_tokens_up leaves for k_tokens_down.
-struct TokensTable {
-  int n_active;                              // selected local experts
-  int expert[kTokensMaxPairs];               // each one's local index, ascending
-  int16_t pair[kTokensMaxPairs][kTokensMaxT];  // its pair of token t, or -1
+// The pairs of each selected local expert: in LDS of k_tokens_up, and in the
+// workspace for k_tokens_down.
+struct Lists {
+  int n_active;
+  int16_t expert[kTokensMaxPairs];           // local index, ascending
+  int16_t first[kTokensMaxPairs], n[kTokensMaxPairs];
+  int16_t pair[kTokensMaxPairs];             // t k + slot, expert by expert
+  int16_t token[kTokensMaxPairs];            // t
 };
-constexpr size_t kTableBytes = (sizeof(TokensTable) + 255) / 256 * 256;
+constexpr size_t kListBytes = (sizeof(Lists) + 255) / 256 * 256;
 
 // ------------------------------------------------------------- wavefront reductions
 
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d, 64));
-  return v;
+template <class T, class Op>
+__device__ __forceinline__ T wave_join(T v, Op op) {
+  v = op(v, across<0>(v));
+  v = op(v, across<1>(v));
+  v = op(v, across<2>(v));
+  v = op(v, across<3>(v));
+  return join_rows(v, op);
 }
-__device__ __forceinline__ uint32_t wave_min_u32(uint32_t v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = min(v, (uint32_t)__shfl_xor((int)v, d, 64));
-  return v;
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  return wave_join(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
-__device__ __forceinline__ float wave_sum_f32(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-  return v;
+__device__ __forceinline__ uint32_t wave_min(uint32_t v) {
+  return wave_join(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+__device__ __forceinline__ float wave_max(float v) {
+  return wave_join(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  return wave_join(v, [](float a, float b) { return a + b; });
 }
 
 // Order-preserving bits of a number that can be selected; 0 for NaN and -inf.
@@ -110,11 +123,10 @@ __device__ __forceinline__ void select(const TokensArgs& a, int t, int& id, floa
   }
   float denom = 0.0f;
   if (!a.sigmoid) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+    top = wave_max(top);
 #pragma unroll
     for (int i = 0; i < NE; ++i) denom += x[i] > kNegInfT ? expf(x[i] - top) : 0.0f;
-    denom = wave_sum_f32(denom);
+    denom = wave_sum(denom);
   }
   id = -1;
   for (int j = 0; j < a.k; ++j) {
@@ -128,14 +140,14 @@ __device__ __forceinline__ void select(const TokensArgs& a, int t, int& id, floa
       if constexpr (BIAS) bl = more ? lo[i] : bl;
       bi = more ? lane + 64 * i : bi;
     }
-    const uint32_t mh = wave_max_u32(bh);
+    const uint32_t mh = wave_max(bh);
     if (mh == 0) break;                      // no expert left
     bool best = bh == mh;
     if constexpr (BIAS) {
-      const uint32_t ml = wave_max_u32(best ? bl : 0u);
+      const uint32_t ml = wave_max(best ? bl : 0u);
       best = best && bl == ml;
     }
-    const int e = (int)wave_min_u32(best ? (uint32_t)bi : 0xFFFFu);
+    const int e = (int)wave_min(best ? (uint32_t)bi : 0xFFFFu);
     if (lane == j) id = e;
 #pragma unroll
     for (int i = 0; i < NE; ++i)
@@ -153,42 +165,40 @@ __device__ __forceinline__ void select(const TokensArgs& a, int t, int& id, floa
     s = s < 0x1p-126f ? 0.0f : s;
   }
   if (a.renorm) {
-    const float total = wave_sum_f32(s);
+    const float total = wave_sum(s);
     s = total > 0.0f ? s / total : 0.0f;
   }
   gate = a.scale * s;
 }
 
-// 32 codes (16 bytes, one row's elements 32 g .. 32 g + 31 of a 128-element
-// chunk) to four bfloat16 fragments. MXFP4: one scale byte, folded into the
-// conversion. NVFP4: two E4M3 scales of 16, the products exact.
+// Fragment m of a row's elements 32 g .. 32 g + 31 of a 128-element chunk: their
+// 8 m .. 8 m + 7. MXFP4: one scale byte, folded into the conversion. NVFP4: two
+// E4M3 scales of 16, the products exact.
 template <bool NV>
-__device__ __forceinline__ void dequant(const u32x4v w, uint32_t s, bf16x8 (&f)[4]) {
+__device__ __forceinline__ bf16x8 dequant(const u32x4v w, uint32_t s, int m) {
+  uint32_t p[4];
+  if constexpr (NV) {
+    const float sc = m < 2 ? __builtin_amdgcn_cvt_f32_fp8((int)s, 0)
+                           : __builtin_amdgcn_cvt_f32_fp8((int)s, 1);
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    uint32_t p[4];
-    if constexpr (NV) {
-      const float sc = __builtin_amdgcn_cvt_f32_fp8((int)(m < 2 ? s & 0xFFu : s >> 8), 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float u, v;
-        e2m1x2_to_f32(w[m], i, u, v);
-        p[i] = pk_bf16(__fmul_rn(u, sc), __fmul_rn(v, sc));
-      }
-    } else {
-      const float sc = u2f(s << 23);
-      p[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[m], sc, 0));
-      p[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[m], sc, 1));
-      p[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[m], sc, 2));
-      p[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[m], sc, 3));
+    for (int i = 0; i < 4; ++i) {
+      float u, v;
+      e2m1x2_to_f32(w[m], i, u, v);
+      p[i] = pk_bf16(__fmul_rn(u, sc), __fmul_rn(v, sc));
     }
-    f[m] = __builtin_bit_cast(bf16x8, u32x4v{p[0], p[1], p[2], p[3]});
+  } else {
+    const float sc = u2f(s << 23);
+    p[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[m], sc, 0));
+    p[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[m], sc, 1));
+    p[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[m], sc, 2));
+    p[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[m], sc, 3));
   }
+  return __builtin_bit_cast(bf16x8, u32x4v{p[0], p[1], p[2], p[3]});
 }
 
-// The scales of lane group g's 32 elements in chunk c of a row.
+// The scales of lane group g's 32 elements of chunk c of a row: a byte, or two.
 template <bool NV>
-__device__ __forceinline__ uint32_t load_scale(const uint8_t* row, int64_t c, int g) {
+__device__ __forceinline__ uint32_t load_scale(const uint8_t* row, int c, int g) {
   if constexpr (NV) return *reinterpret_cast<const uint16_t*>(row + c * 8 + 2 * g);
   else return row[c * 4 + g];
 }
@@ -202,20 +212,11 @@ __device__ __forceinline__ float activate(float v, int act) {
   return v;
 }
 
-template <int NE, bool BIAS, bool NV, bool GATED>
-__global__ __launch_bounds__(kThreads) void k_tokens_up(TokensArgs a) {
-  __shared__ int ids[kTokensMaxPairs];
-  __shared__ float gates[kTokensMaxPairs];
-  __shared__ int cnt[kMaxExperts];
-  __shared__ int act_e[kTokensMaxPairs], act_n[kTokensMaxPairs], act_0[kTokensMaxPairs];
-  __shared__ int where[kMaxExperts];
-  __shared__ int16_t list[kTokensMaxPairs];
-  __shared__ int wave_a[kWavesT], wave_n[kWavesT];
-  __shared__ float red[kWavesT][GATED ? 2 : 1][256];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int pairs = a.T * a.k;
-
-  for (int t = wave; t < a.T; t += kWavesT) {
+// select() for each token, a wavefront at a time.
+template <int NE, bool BIAS>
+__device__ __forceinline__ void select_all(const TokensArgs& a, int* ids, float* gates) {
+  const int lane = threadIdx.x & 63;
+  for (int t = threadIdx.x >> 6; t < a.T; t += kWavesT) {
     int id;
     float gate;
     select<NE, BIAS>(a, t, id, gate);
@@ -228,115 +229,252 @@ __global__ __launch_bounds__(kThreads) void k_tokens_up(TokensArgs a) {
       }
     }
   }
-  if (tid < a.n_local) cnt[tid] = 0;
+}
+
+// The experts and gates of all tokens (selected here, or read where a launch
+// before has them) and the lists of pairs, by a whole workgroup.
+__device__ __forceinline__ void route(const TokensArgs& a, Lists& l, float* gates) {
+  __shared__ int ids[kTokensMaxPairs];
+  __shared__ int cnt[kMaxExperts];
+  __shared__ int16_t where[kMaxExperts];
+  __shared__ int waves[kWavesT];
+  static_assert(kThreads >= kMaxExperts && kThreads >= kTokensMaxPairs, "one pass of the threads");
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  cnt[tid] = 0;
+  if (a.T > kSelectHere) {
+    if (tid < a.T * a.k) {
+      ids[tid] = a.topk_ids[tid];
+      gates[tid] = a.gate[tid];
+    }
+  } else if (a.bias) {
+    if (a.E <= 64) select_all<1, true>(a, ids, gates);
+    else if (a.E <= 384) select_all<6, true>(a, ids, gates);
+    else select_all<16, true>(a, ids, gates);
+  } else {
+    if (a.E <= 64) select_all<1, false>(a, ids, gates);
+    else if (a.E <= 384) select_all<6, false>(a, ids, gates);
+    else select_all<16, false>(a, ids, gates);
+  }
   __syncthreads();
-  // the pairs of each local expert; the order inside an expert is arbitrary
-  // (a pair is a column of its own: no result depends on it)
+  // the order of pairs inside an expert is arbitrary (a pair is a column of its
+  // own: no result depends on it)
   int le = -1, pos = 0;
-  if (tid < pairs) {
+  if (tid < a.T * a.k) {
     le = ids[tid] - a.e0;
     if (ids[tid] < 0 || le < 0 || le >= a.n_local) le = -1;
     if (le >= 0) pos = atomicAdd(&cnt[le], 1);
   }
   __syncthreads();
-  const int c = tid < a.n_local ? cnt[tid] : 0;
-  const uint64_t some = __ballot(c > 0);
-  int incl = c;
+  // thread t: expert t; selected ones and pairs before it in one scan
+  const int c = cnt[tid], own = (c > 0) << 16 | c;
+  int incl = own;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int u = __shfl_up(incl, d, 64);
     if (lane >= d) incl += u;
   }
-  if (lane == 63) {
-    wave_a[wave] = __popcll(some);
-    wave_n[wave] = incl;
-  }
+  if (lane == 63) waves[wave] = incl;
   __syncthreads();
-  int na = 0, a0 = 0, n0 = 0;
+  int before = incl - own, all = 0;
 #pragma unroll
   for (int i = 0; i < kWavesT; ++i) {
-    a0 += i < wave ? wave_a[i] : 0;
-    n0 += i < wave ? wave_n[i] : 0;
-    na += wave_a[i];
+    before += i < wave ? waves[i] : 0;
+    all += waves[i];
   }
   if (c > 0) {
-    const int at = a0 + __popcll(some & ~(~0ull << lane));
-    act_e[at] = tid;
-    act_n[at] = c;
-    act_0[at] = n0 + incl - c;
-    where[tid] = at;
+    const int at = before >> 16;
+    l.expert[at] = (int16_t)tid;
+    l.n[at] = (int16_t)c;
+    l.first[at] = (int16_t)(before & 0xFFFF);
+    where[tid] = (int16_t)at;
+  }
+  if (tid == 0) l.n_active = all >> 16;
+  __syncthreads();
+  if (le >= 0) {
+    const int at = l.first[where[le]] + pos;
+    l.pair[at] = (int16_t)tid;
+    l.token[at] = (int16_t)(tid / a.k);
   }
   __syncthreads();
-  if (le >= 0) list[act_0[where[le]] + pos] = (int16_t)tid;
-  __syncthreads();
+}
 
-  // the table of the second kernel, a part from each workgroup
-  TokensTable* tab = reinterpret_cast<TokensTable*>(a.ws);
-  if (blockIdx.x == 0 && tid == 0) tab->n_active = na;
-  for (int i = (int)blockIdx.x + (int)gridDim.x * wave; i < na; i += (int)gridDim.x * kWavesT) {
-    int p = -1;
-    for (int j = 0; j < act_n[i]; ++j) {
-      const int q = list[act_0[i] + j];
-      if (q / a.k == lane) p = q;
-    }
-    tab->pair[i][lane] = (int16_t)p;
-    if (lane == 0) tab->expert[i] = act_e[i];
+enum Kind { kUp, kUpGated, kDown };
+constexpr int RS = 2;                        // slices of 16 rows (gated: one of each matrix)
+
+// A grid-wide list of jobs, (selected expert, 16 RF rows of its product): W1 x
+// with the activation to h, or W2 h to y. NT tiles of 16 pairs at most.
+template <bool NV, Kind KIND, int NT>
+__global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
+  constexpr bool DOWN = KIND == kDown, GATED = KIND == kUpGated;
+  constexpr int RF = GATED ? RS / 2 : RS;    // slices of the product
+  constexpr int CH = NT == 1 && !DOWN ? 2 : 1;      // 128-element chunks of a piece
+  constexpr int PL = DOWN ? 2 : 1;           // parts of the other operand
+  constexpr int SB = NV ? 16 : 32;           // elements of a scale
+  __shared__ Lists l;
+  __shared__ float gates[DOWN ? 1 : kTokensMaxPairs];
+  __shared__ f32x4 red[kWavesT][RS][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr int words = (int)(sizeof(Lists) / 4);
+  if constexpr (DOWN) {
+    for (int i = tid; i < words; i += kThreads)
+      reinterpret_cast<int*>(&l)[i] = reinterpret_cast<const int*>(a.ws)[i];
+    __syncthreads();
+  } else {
+    route(a, l, gates);
+    if (blockIdx.x == 0)
+      for (int i = tid; i < words; i += kThreads)
+        reinterpret_cast<int*>(a.ws)[i] = reinterpret_cast<int*>(&l)[i];
   }
 
-  const int slices = (int)(a.F / 16);
-  const int64_t units = (int64_t)na * slices;
   const int r = lane & 15, g = lane >> 4;
-  const int64_t K = a.K, F = a.F;
-  const int chunks = (int)(K / 128);
-  constexpr int M = GATED ? 2 : 1;
-  const int64_t srow = K / (NV ? 16 : 32);
-  uint16_t* hhi = reinterpret_cast<uint16_t*>(a.ws + kTableBytes);
-  uint16_t* hlo = hhi + (int64_t)pairs * F;
-  const int64_t u1 = units * ((int64_t)blockIdx.x + 1) / gridDim.x;
-  for (int64_t u = units * (int64_t)blockIdx.x / gridDim.x; u < u1; ++u) {
-    const int ai = (int)(u / slices), sl = (int)(u % slices);
-    const int e = act_e[ai], n = act_n[ai], first = act_0[ai];
-    for (int t0 = 0; t0 < n; t0 += 16) {
-      const int p = list[first + (t0 + r < n ? t0 + r : n - 1)];
-      const uint16_t* xr = static_cast<const uint16_t*>(a.x) + (int64_t)(p / a.k) * K;
-      f32x4 acc[M];
+  const int64_t L = DOWN ? a.F : a.K, R = DOWN ? a.K : a.F;   // contraction, rows of the product
+  const int64_t rows_e = GATED ? 2 * R : R;
+  const uint8_t* codes = DOWN ? a.w2_codes : a.w1_codes;
+  const uint8_t* scales = DOWN ? a.w2_scales : a.w1_scales;
+  uint16_t* hhi = reinterpret_cast<uint16_t*>(a.ws + kListBytes);
+  uint16_t* hlo = hhi + (int64_t)a.T * a.k * a.F;
+  float* y = reinterpret_cast<float*>(hlo + (int64_t)a.T * a.k * a.F);
+
+  const int chunks = (int)(L / 128), groups = (int)(R / (16 * RF)), jobs = l.n_active * groups;
+  if (jobs == 0) return;
+  // S = 2^lg wavefronts share a job's contraction, per chunks each in steps of
+  // CH; the workgroup has kWavesT / S jobs at once. The split of the fewest
+  // steps over all rounds, a round's join counted as half of one.
+  int lg = 0, least = 0x7FFFFFFF;
+  for (int i = 0; 1 << i <= kWavesT && (i == 0 || 1 << (i - 1) < chunks); ++i) {
+    const int slots = (kWavesT >> i) * (int)gridDim.x;
+    const int st = ((chunks + (1 << i) - 1) / (1 << i) + CH - 1) / CH;
+    const int cost = (jobs + slots - 1) / slots * (2 * st + 1);
+    if (cost <= least) {
+      least = cost;
+      lg = i;
+    }
+  }
+  const int jobs_at_once = kWavesT >> lg, mine = wave >> lg;
+  const int per = (chunks + (1 << lg) - 1) >> lg, steps = (per + CH - 1) / CH;
+  const int c_first = (wave & ((1 << lg) - 1)) * per, c_end = min(c_first + per, chunks);
+  const int rounds = (jobs + jobs_at_once - 1) / jobs_at_once;
+
+  u32x4v w[RS][CH];
+  uint32_t sc[RS][CH];
+  // the piece of round q and step st; past the end: some piece, not used
+  auto load = [&](int q, int st) {
+    const int j = min(q * jobs_at_once + mine, jobs - 1);
+    const int64_t row0 = l.expert[j / groups] * rows_e + j % groups * (16 * RF) + r;
 #pragma unroll
-      for (int m = 0; m < M; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      for (int ch = wave; ch < chunks; ch += kWavesT) {
-        bf16x8 b[4];
+    for (int i = 0; i < RS; ++i) {
+      const int64_t row = row0 + (GATED ? i * R : 16 * i);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          b[q] = *reinterpret_cast<const bf16x8*>(xr + ch * 128 + 32 * g + 8 * q);
+      for (int x = 0; x < CH; ++x) {
+        const int c = min(c_first + st * CH + x, chunks - 1);
+        w[i][x] = *reinterpret_cast<const u32x4v*>(codes + row * (L / 2) + c * 64 + 16 * g);
+        sc[i][x] = load_scale<NV>(scales + row * (L / SB), c, g);
+      }
+    }
+  };
+  if ((int)blockIdx.x < rounds) load((int)blockIdx.x, 0);
+  for (int q = (int)blockIdx.x; q < rounds; q += (int)gridDim.x) {
+    const int j = q * jobs_at_once + mine;
+    const bool real = j < jobs;
+    const int ai = (real ? j : jobs - 1) / groups;
+    const int n = l.n[ai], first = l.first[ai];
+    int most = 1;                            // tiles of the round's longest list
+    for (int i = 0; NT > 1 && i < jobs_at_once; ++i)
+      most = max(most, (l.n[min(q * jobs_at_once + i, jobs - 1) / groups] + 15) / 16);
+    f32x4 acc[NT][RS];
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-          const int64_t row = (int64_t)e * (M * F) + m * F + sl * 16 + r;
-          const u32x4v w = *reinterpret_cast<const u32x4v*>(a.w1_codes + row * (K / 2) + ch * 64 + 16 * g);
-          bf16x8 f[4];
-          dequant<NV>(w, load_scale<NV>(a.w1_scales + row * srow, ch, g), f);
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[q], b[q], acc[m], 0, 0, 0);
+      for (int i = 0; i < RS; ++i) acc[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int st = 0; st < steps; ++st) {
+      u32x4v wc[RS][CH];
+      uint32_t scc[RS][CH];
+#pragma unroll
+      for (int i = 0; i < RS; ++i) {
+#pragma unroll
+        for (int x = 0; x < CH; ++x) {
+          wc[i][x] = w[i][x];
+          scc[i][x] = sc[i][x];
         }
       }
+      const int c0 = c_first + st * CH;
+      // A tile's columns: lanes past the list read nothing (their columns go
+      // nowhere). The first tile's are asked for before the next weights, which
+      // then stay in flight: loads return in order.
+      bf16x8 b[CH][PL][4];
+      auto columns = [&](int t) {
+        if (16 * t + r >= n) return;
+        const int at = first + 16 * t + r;
+        const int64_t from = (DOWN ? l.pair[at] : l.token[at]) * L + 32 * g;
 #pragma unroll
-      for (int m = 0; m < M; ++m) *reinterpret_cast<f32x4*>(&red[wave][m][lane * 4]) = acc[m];
-      __syncthreads();
-      if (wave == 0) {
-        f32x4 v[M];
+        for (int x = 0; x < CH; ++x) {
+          const int c = min(c0 + x, chunks - 1);
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-          v[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int i = 0; i < kWavesT; ++i) v[m] += *reinterpret_cast<const f32x4*>(&red[i][m][lane * 4]);
+          for (int m = 0; m < 4; ++m) {
+            if constexpr (DOWN) {
+              b[x][0][m] = *reinterpret_cast<const bf16x8*>(hlo + from + c * 128 + 8 * m);
+              b[x][1][m] = *reinterpret_cast<const bf16x8*>(hhi + from + c * 128 + 8 * m);
+            } else {
+              b[x][0][m] = *reinterpret_cast<const bf16x8*>(static_cast<const uint16_t*>(a.x) + from + c * 128 + 8 * m);
+            }
+          }
         }
-        if (t0 + r < n) {
+      };
+      columns(0);
+      asm volatile("" ::: "memory");
+      if (st + 1 < steps) load(q, st + 1);
+      else if (q + (int)gridDim.x < rounds) load(q + (int)gridDim.x, 0);
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (16 * t >= n) break;
+        if (t > 0) columns(t);
+#pragma unroll
+        for (int x = 0; x < CH; ++x) {
+          if (c0 + x >= c_end || !real) continue;            // loaded to no use
+#pragma unroll
+          for (int i = 0; i < RS; ++i)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const bf16x8 f = dequant<NV>(wc[i][x], scc[i][x], m);
+#pragma unroll
+              for (int u = 0; u < PL; ++u)
+                acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, b[x][u][m], acc[t][i], 0, 0, 0);
+            }
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (t >= most) break;
+#pragma unroll
+      for (int i = 0; i < RS; ++i) red[wave][i][lane] = acc[t][i];
+      __syncthreads();
+      // item: four rows of a slice, one column
+      for (int it = tid; it < jobs_at_once * RF * 64; it += kThreads) {
+        const int li = it & 63, s = it / 64 % RF, jm = it / 64 / RF;
+        const int jj = q * jobs_at_once + jm;
+        if (jj >= jobs) continue;
+        const int aj = jj / groups, col = 16 * t + (li & 15);
+        if (col >= l.n[aj]) continue;
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f}, u = v;
+        for (int i = 0; i < 1 << lg; ++i) {
+          v += red[(jm << lg) + i][s][li];
+          if constexpr (GATED) u += red[(jm << lg) + i][RF + s][li];
+        }
+        const int e = l.expert[aj], p = l.pair[l.first[aj] + col];
+        const int64_t at = p * R + jj % groups * (16 * RF) + 16 * s + 4 * (li >> 4);
+        if constexpr (DOWN) {
+          *reinterpret_cast<f32x4*>(y + at) = v;
+        } else {
           const float o1 = NV ? a.w1_outer[e] : 1.0f;
           const float go = gates[p] * (NV ? a.w2_outer[e] : 1.0f);
           float h[4], lo[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            h[i] = activate(v[0][i] * o1, a.act);
-            if constexpr (GATED) h[i] *= v[M - 1][i] * o1;
+            h[i] = activate(v[i] * o1, a.act);
+            if constexpr (GATED) h[i] *= u[i] * o1;
             h[i] *= go;
           }
           const uint32_t h01 = pk_bf16(h[0], h[1]), h23 = pk_bf16(h[2], h[3]);
@@ -344,7 +482,6 @@ __global__ __launch_bounds__(kThreads) void k_tokens_up(TokensArgs a) {
           lo[1] = h[1] - u2f(h01 & 0xFFFF0000u);
           lo[2] = h[2] - u2f(h23 << 16);
           lo[3] = h[3] - u2f(h23 & 0xFFFF0000u);
-          const int64_t at = (int64_t)p * F + sl * 16 + 4 * g;
           *reinterpret_cast<uint2*>(hhi + at) = make_uint2(h01, h23);
           *reinterpret_cast<uint2*>(hlo + at) = make_uint2(pk_bf16(lo[0], lo[1]), pk_bf16(lo[2], lo[3]));
         }
@@ -354,104 +491,67 @@ __global__ __launch_bounds__(kThreads) void k_tokens_up(TokensArgs a) {
   }
 }
 
-template <bool NV>
-__global__ __launch_bounds__(kThreads) void k_tokens_down(TokensArgs a) {
-  __shared__ int16_t pair[kTokensMaxPairs][kTokensMaxT];
-  __shared__ int expert[kTokensMaxPairs];
-  __shared__ float red[kWavesT][256];
-  const TokensTable* tab = reinterpret_cast<const TokensTable*>(a.ws);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int r = lane & 15, g = lane >> 4;
-  const int na = tab->n_active;
-  for (int i = tid; i < na; i += kThreads) expert[i] = tab->expert[i];
-  for (int i = tid; i < na * kTokensMaxT / 8; i += kThreads)
-    reinterpret_cast<uint4*>(pair)[i] = reinterpret_cast<const uint4*>(tab->pair)[i];
-  __syncthreads();
-  const int64_t K = a.K, F = a.F;
-  const int chunks = (int)(F / 128);
-  const int64_t srow = F / (NV ? 16 : 32);
-  const uint16_t* hhi = reinterpret_cast<const uint16_t*>(a.ws + kTableBytes);
-  const uint16_t* hlo = hhi + (int64_t)a.T * a.k * F;
-  const int64_t c0 = (int64_t)blockIdx.x * 16;
-  const int nt = (a.T + 15) / 16;
-  f32x4 acc[4];
+// out[t] = the sum of y over the token's pairs, slot by slot. A thread has four
+// columns of a token; a pair that is not local has no row of y (what is read
+// there is dropped).
+__global__ __launch_bounds__(256) void k_tokens_sum(TokensArgs a) {
+  const int t = blockIdx.y;
+  const int64_t col = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (col >= a.K) return;
+  const float* y = reinterpret_cast<const float*>(a.ws + kListBytes + (int64_t)a.T * a.k * a.F * 4) +
+                   (int64_t)t * a.k * a.K + col;
+  const int32_t* ids = a.topk_ids + (int64_t)t * a.k;
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j0 = 0; j0 < a.k; j0 += 4) {
+    f32x4 u[4];
+    int id[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j = wave; j < na * chunks; j += kWavesT) {
-    const int ai = j / chunks, ch = j % chunks;
-    const int64_t row = (int64_t)expert[ai] * K + c0 + r;
-    const u32x4v w = *reinterpret_cast<const u32x4v*>(a.w2_codes + row * (F / 2) + ch * 64 + 16 * g);
-    bf16x8 f[4];
-    dequant<NV>(w, load_scale<NV>(a.w2_scales + row * srow, ch, g), f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i >= nt) break;
-      const int p = pair[ai][16 * i + r];
-      if (__ballot(p >= 0) == 0) continue;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        u32x4v bh = {0, 0, 0, 0}, bl = {0, 0, 0, 0};
-        if (p >= 0) {
-          const int64_t at = (int64_t)p * F + ch * 128 + 32 * g + 8 * q;
-          bh = *reinterpret_cast<const u32x4v*>(hhi + at);
-          bl = *reinterpret_cast<const u32x4v*>(hlo + at);
-        }
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[q], __builtin_bit_cast(bf16x8, bl), acc[i], 0, 0, 0);
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[q], __builtin_bit_cast(bf16x8, bh), acc[i], 0, 0, 0);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int at = min(j0 + j, a.k - 1);
+      id[j] = j0 + j < a.k ? ids[at] : -1;
+      u[j] = *reinterpret_cast<const f32x4*>(y + at * a.K);
     }
-  }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i >= nt) break;
-    *reinterpret_cast<f32x4*>(&red[wave][lane * 4]) = acc[i];
-    __syncthreads();
-    if (wave == 0) {
-      f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int q = 0; q < kWavesT; ++q) v += *reinterpret_cast<const f32x4*>(&red[q][lane * 4]);
-      const int t = 16 * i + r;
-      if (t < a.T) {
-        const int64_t at = (int64_t)t * K + c0 + 4 * g;
-        if (a.out_bf16)
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-              make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
-        else
-          *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at) = v;
-      }
-    }
-    __syncthreads();
+    for (int j = 0; j < 4; ++j)
+      if (id[j] >= 0 && id[j] >= a.e0 && (int64_t)id[j] - a.e0 < a.n_local) v += u[j];
   }
+  const int64_t at = (int64_t)t * a.K + col;
+  if (a.out_bf16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+        make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+  else
+    *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at) = v;
 }
 
-template <int NE, bool BIAS>
-void up(const TokensArgs& a, unsigned grid, hipStream_t stream) {
-  const bool nv = a.w1_outer != nullptr;
-  auto k = nv ? (a.gated ? k_tokens_up<NE, BIAS, true, true> : k_tokens_up<NE, BIAS, true, false>)
-              : (a.gated ? k_tokens_up<NE, BIAS, false, true> : k_tokens_up<NE, BIAS, false, false>);
+template <bool NV, Kind KIND>
+hipError_t product(const TokensArgs& a, unsigned grid, hipStream_t stream) {
+  auto k = a.T <= 16 ? k_tokens_product<NV, KIND, 1> : k_tokens_product<NV, KIND, 4>;
   k<<<grid, kThreads, 0, stream>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t tokens_workspace_bytes(int64_t T, int k, int64_t F) {
-  return kTableBytes + (size_t)(T * k * F) * 4;
+// The lists, h in two bfloat16 parts, y in float32, by pair.
+size_t tokens_workspace_bytes(int64_t T, int k, int64_t K, int64_t F) {
+  return kListBytes + (size_t)(T * k * (K + F)) * 4;
 }
 
 hipError_t launch_ffn_tokens(const TokensArgs& a, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
-  const int64_t most = a.T * a.k < a.n_local ? a.T * a.k : a.n_local;   // experts selected at most
-  int64_t grid = most * (a.F / 16);
-  if (grid > device_cu_count()) grid = device_cu_count();
-  const bool bias = a.bias != nullptr;
-  if (a.E <= 64) bias ? up<1, true>(a, grid, stream) : up<1, false>(a, grid, stream);
-  else if (a.E <= 384) bias ? up<6, true>(a, grid, stream) : up<6, false>(a, grid, stream);
-  else bias ? up<16, true>(a, grid, stream) : up<16, false>(a, grid, stream);
-  hipError_t e = hipGetLastError();
+  hipError_t e = hipSuccess;
+  if (a.T > kSelectHere)
+    e = launch_route(a.logits, a.logits_bf16, a.T, a.E, a.k, a.sigmoid, a.renorm, a.scale, a.bias,
+                     a.token_mask, a.topk_ids, a.gate, nullptr, nullptr, nullptr, stream);
   if (e != hipSuccess) return e;
-  const unsigned cols = (unsigned)(a.K / 16);
-  if (a.w1_outer) k_tokens_down<true><<<cols, kThreads, 0, stream>>>(a);
-  else k_tokens_down<false><<<cols, kThreads, 0, stream>>>(a);
+  const bool nv = a.w1_outer != nullptr;
+  const unsigned cus = (unsigned)device_cu_count();
+  if (nv) e = a.gated ? product<true, kUpGated>(a, cus, stream) : product<true, kUp>(a, cus, stream);
+  else e = a.gated ? product<false, kUpGated>(a, cus, stream) : product<false, kUp>(a, cus, stream);
+  if (e != hipSuccess) return e;
+  e = nv ? product<true, kDown>(a, cus, stream) : product<false, kDown>(a, cus, stream);
+  if (e != hipSuccess) return e;
+  k_tokens_sum<<<dim3((unsigned)((a.K / 4 + 255) / 256), (unsigned)a.T), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -92,8 +92,9 @@ def test_ffn_tokens_refusals(L):
         assert f(**{name: FOUR}) == EUNSUP, name
     for name in ("lg", "ids", "gate"):
         assert f(**{name: ODD}) == EUNSUP, name
-    need = L.nvfp4moe_ffn_tokens_workspace_size(4, 2, 128)
+    need = L.nvfp4moe_ffn_tokens_workspace_size(4, 2, 128, 128)
     assert need > 0 and f(wsb=need - 1) == EWS
     assert f(T=0, x=None) == 0
     size = L.nvfp4moe_ffn_tokens_workspace_size
-    assert size(65, 1, 128) == size(64, 9, 128) == size(-1, 2, 128) == size(1 << 62, 2, 128) == size(4, 2, 1 << 40) == 0
+    assert size(65, 1, 128, 128) == size(64, 9, 128, 128) == size(-1, 2, 128, 128) == size(1 << 62, 2, 128, 128) == 0
+    assert size(4, 2, 1 << 40, 128) == size(4, 2, 128, 1 << 40) == 0

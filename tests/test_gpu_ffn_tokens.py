@@ -166,7 +166,7 @@ def test_same_bits_and_two_streams(nv):
     ref = run()
     torch.cuda.synchronize()
     s = [torch.cuda.Stream(), torch.cuda.Stream()]
-    ws = [torch.empty(nv.ffn_tokens_workspace_size(40, 4, 256), dtype=torch.uint8, device="cuda") for _ in s]
+    ws = [torch.empty(nv.ffn_tokens_workspace_size(40, 4, 512, 256), dtype=torch.uint8, device="cuda") for _ in s]
     outs = []
     for i in range(6):
         with torch.cuda.stream(s[i % 2]):
@@ -184,7 +184,7 @@ def test_graph(nv):
     out = dict(out=torch.empty(20, 256, dtype=torch.bfloat16, device="cuda"),
                topk_ids=torch.empty(20, 3, dtype=torch.int32, device="cuda"),
                gate=torch.empty(20, 3, device="cuda"))
-    ws = torch.empty(nv.ffn_tokens_workspace_size(20, 3, 256), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(nv.ffn_tokens_workspace_size(20, 3, 256, 256), dtype=torch.uint8, device="cuda")
     run = lambda c, **kw: nv.moe_ffn_tokens(c["x"], c["logits"], 3, c["w1"], c["w2"], e0=8,
                                             token_mask=c["token_mask"], **kw)
     refs = [[t.clone() for t in run(c).values()] for c in (a, b)]
