@@ -40,4 +40,11 @@ __device__ __forceinline__ T join_rows(T v, Op op) {
   return op(__builtin_bit_cast(T, q0), __builtin_bit_cast(T, q1));
 }
 
+// Orders the LDS accesses of one wavefront's lanes before and after it (the
+// hardware runs them in order; this keeps the compiler from moving them).
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 }  // namespace nvfp4moe

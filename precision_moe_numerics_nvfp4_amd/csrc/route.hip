@@ -104,13 +104,6 @@ __device__ __forceinline__ int group_min(int v) {
   return group_join<L>(v, [](int a, int b) { return a < b ? a : b; });
 }
 
-// Orders the LDS accesses of one wavefront's lanes before and after it (the
-// hardware runs them in order; this keeps the compiler from moving them).
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // exp(x) for x <= 0 by the hardware's 2^x: the rounded product x * log2(e)
 // costs a relative 2^-24 |x|, the instruction one unit in the last place.
 __device__ __forceinline__ float exp_neg(float x) {

@@ -38,21 +38,25 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2v __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
+typedef u32x4v u32x4v_4 __attribute__((aligned(4)));
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
 constexpr int kWavesT = kThreads / 64;
 constexpr int kMaxExperts = 1024;
 // Up to so many tokens every workgroup selects by itself; beyond, a launch before does.
 constexpr int kSelectHere = 16;
 constexpr float kNegInfT = -__builtin_huge_valf();
 
-// The pairs of each selected local expert: in LDS of k_tokens_up, and in the
-// workspace for k_tokens_down.
+constexpr int kCols = 16;                    // pairs of a list at most: a matrix instruction's columns
+
+// The pairs of the selected local experts in lists of up to kCols, an expert's
+// lists next to each other: in LDS, and in the workspace for the second product.
 struct Lists {
-  int n_active;
+  int count;
   int16_t expert[kTokensMaxPairs];           // local index, ascending
+  int16_t lead[kTokensMaxPairs], lists[kTokensMaxPairs];   // the expert's first list, and how many
   int16_t first[kTokensMaxPairs], n[kTokensMaxPairs];
-  int16_t pair[kTokensMaxPairs];             // t k + slot, expert by expert
+  int16_t pair[kTokensMaxPairs];             // t k + slot, list by list
   int16_t token[kTokensMaxPairs];            // t
 };
 constexpr size_t kListBytes = (sizeof(Lists) + 255) / 256 * 256;
@@ -196,13 +200,6 @@ __device__ __forceinline__ bf16x8 dequant(const u32x4v w, uint32_t s, int m) {
   return __builtin_bit_cast(bf16x8, u32x4v{p[0], p[1], p[2], p[3]});
 }
 
-// The scales of lane group g's 32 elements of chunk c of a row: a byte, or two.
-template <bool NV>
-__device__ __forceinline__ uint32_t load_scale(const uint8_t* row, int c, int g) {
-  if constexpr (NV) return *reinterpret_cast<const uint16_t*>(row + c * 8 + 2 * g);
-  else return row[c * 4 + g];
-}
-
 __device__ __forceinline__ float activate(float v, int act) {
   if (act == 2) return v / (1.0f + expf(-v));
   if (act == 1) {
@@ -238,9 +235,9 @@ __device__ __forceinline__ void route(const TokensArgs& a, Lists& l, float* gate
   __shared__ int cnt[kMaxExperts];
   __shared__ int16_t where[kMaxExperts];
   __shared__ int waves[kWavesT];
-  static_assert(kThreads >= kMaxExperts && kThreads >= kTokensMaxPairs, "one pass of the threads");
+  static_assert(2 * kThreads >= kMaxExperts && kThreads >= kTokensMaxPairs, "one pass of the threads");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  cnt[tid] = 0;
+  cnt[2 * tid] = cnt[2 * tid + 1] = 0;
   if (a.T > kSelectHere) {
     if (tid < a.T * a.k) {
       ids[tid] = a.topk_ids[tid];
@@ -265,8 +262,9 @@ __device__ __forceinline__ void route(const TokensArgs& a, Lists& l, float* gate
     if (le >= 0) pos = atomicAdd(&cnt[le], 1);
   }
   __syncthreads();
-  // thread t: expert t; selected ones and pairs before it in one scan
-  const int c = cnt[tid], own = (c > 0) << 16 | c;
+  // thread t: experts 2 t and 2 t + 1; lists and pairs before them in one scan
+  const int c0 = cnt[2 * tid], c1 = cnt[2 * tid + 1];
+  const int own = ((c0 + kCols - 1) / kCols + (c1 + kCols - 1) / kCols) << 16 | (c0 + c1);
   int incl = own;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -281,17 +279,24 @@ __device__ __forceinline__ void route(const TokensArgs& a, Lists& l, float* gate
     before += i < wave ? waves[i] : 0;
     all += waves[i];
   }
-  if (c > 0) {
-    const int at = before >> 16;
-    l.expert[at] = (int16_t)tid;
-    l.n[at] = (int16_t)c;
-    l.first[at] = (int16_t)(before & 0xFFFF);
-    where[tid] = (int16_t)at;
-  }
-  if (tid == 0) l.n_active = all >> 16;
+  auto list = [&](int e, int c) {
+    const int lead = before >> 16, lists = (c + kCols - 1) / kCols, first = before & 0xFFFF;
+    for (int i = 0; i < lists; ++i) {
+      l.expert[lead + i] = (int16_t)e;
+      l.lead[lead + i] = (int16_t)lead;
+      l.lists[lead + i] = (int16_t)lists;
+      l.n[lead + i] = (int16_t)min(c - i * kCols, kCols);
+      l.first[lead + i] = (int16_t)(first + i * kCols);
+    }
+    if (c > 0) where[e] = (int16_t)first;
+    before += lists << 16 | c;
+  };
+  list(2 * tid, c0);
+  list(2 * tid + 1, c1);
+  if (tid == 0) l.count = all >> 16;
   __syncthreads();
   if (le >= 0) {
-    const int at = l.first[where[le]] + pos;
+    const int at = where[le] + pos;
     l.pair[at] = (int16_t)tid;
     l.token[at] = (int16_t)(tid / a.k);
   }
@@ -299,19 +304,31 @@ __device__ __forceinline__ void route(const TokensArgs& a, Lists& l, float* gate
 }
 
 enum Kind { kUp, kUpGated, kDown };
-constexpr int RS = 2;                        // slices of 16 rows (gated: one of each matrix)
+constexpr int RS = 4;                        // slices of 16 rows in a job (gated: half of each matrix)
 
-// A grid-wide list of jobs, (selected expert, 16 RF rows of its product): W1 x
-// with the activation to h, or W2 h to y. NT tiles of 16 pairs at most.
-template <bool NV, Kind KIND, int NT>
+// A grid-wide list of jobs, (list of pairs, 16 RF rows of its product): W1 x
+// with the activation to h, or W2 h to y.
+template <bool NV, Kind KIND>
 __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
   constexpr bool DOWN = KIND == kDown, GATED = KIND == kUpGated;
-  constexpr int RF = GATED ? RS / 2 : RS;    // slices of the product
-  constexpr int CH = NT == 1 && !DOWN ? 2 : 1;      // 128-element chunks of a piece
-  constexpr int PL = DOWN ? 2 : 1;           // parts of the other operand
-  constexpr int SB = NV ? 16 : 32;           // elements of a scale
+  constexpr int RF = GATED ? RS / 2 : RS;                    // slices of the product
+  constexpr int CH = DOWN ? 1 : 2;                           // 128-element chunks of a piece
+  constexpr int PL = DOWN ? 2 : 1;                           // parts of the other operand
+  constexpr int SB = NV ? 16 : 32;                           // elements of a scale
+  // A wavefront's own LDS. Scales: of its rows, 32 bytes of each at a time (one
+  // by one they would take as many requests as the codes). Columns: a piece of
+  // all of them.
+  constexpr int SStride = 32 + 16, SChunks = 32 * SB / 128, SQ = RS / 2;
+  constexpr int SSteps = SChunks / CH;                       // steps that a block of scales lasts
+  constexpr int CBytes = CH * PL * 256, CStride = CBytes + 16, XQ = kCols * CBytes / 1024;
+  constexpr int CLanes = CBytes / 16;                        // lanes that hold a column
+  struct Own {
+    uint8_t scales[16 + 16 * RS * SStride];
+    uint8_t columns[kCols * CStride];
+  };
   __shared__ Lists l;
   __shared__ float gates[DOWN ? 1 : kTokensMaxPairs];
+  __shared__ __attribute__((aligned(16))) Own owns[kWavesT];
   __shared__ f32x4 red[kWavesT][RS][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -336,7 +353,7 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
   uint16_t* hlo = hhi + (int64_t)a.T * a.k * a.F;
   float* y = reinterpret_cast<float*>(hlo + (int64_t)a.T * a.k * a.F);
 
-  const int chunks = (int)(L / 128), groups = (int)(R / (16 * RF)), jobs = l.n_active * groups;
+  const int chunks = (int)(L / 128), groups = (int)(R / (16 * RF)), jobs = l.count * groups;
   if (jobs == 0) return;
   // S = 2^lg wavefronts share a job's contraction, per chunks each in steps of
   // CH; the workgroup has kWavesT / S jobs at once. The split of the fewest
@@ -356,20 +373,57 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
   const int c_first = (wave & ((1 << lg) - 1)) * per, c_end = min(c_first + per, chunks);
   const int rounds = (jobs + jobs_at_once - 1) / jobs_at_once;
 
-  u32x4v w[RS][CH];
-  uint32_t sc[RS][CH];
-  // the piece of round q and step st; past the end: some piece, not used
+  Own& own = owns[wave];
+  // a job's list and rows; the lists of an expert take turns at the same rows
+  auto decode = [&](int j, int& ai, int& group) {
+    ai = j / groups;
+    group = j % groups;
+    const int n = l.lists[ai];
+    if (n > 1) {
+      const int lead = l.lead[ai], u = j - lead * groups;
+      ai = lead + u % n;
+      group = u / n;
+    }
+  };
+  const int64_t scale_end = (int64_t)a.n_local * rows_e * (L / SB) - 16;
+  u32x4v w[RS][CH], xq[XQ], sq[SQ];
+  int shift[SQ] = {};                        // of this lane's scales in LDS
+  // The piece of round q and step st; past the end: some piece, not used. The
+  // columns and scales before the codes: loads return in order.
   auto load = [&](int q, int st) {
     const int j = min(q * jobs_at_once + mine, jobs - 1);
-    const int64_t row0 = l.expert[j / groups] * rows_e + j % groups * (16 * RF) + r;
+    int ai, group;
+    decode(j, ai, group);
+    const int n = l.n[ai], first = l.first[ai];
+    const int64_t row0 = l.expert[ai] * rows_e + group * (16 * RF);
+    const int c0 = c_first + st * CH;
+#pragma unroll
+    for (int i = 0; i < XQ; ++i) {
+      if (i * 64 / CLanes >= n) break;
+      const int u = i * 64 + lane, at = first + min(u / CLanes, n - 1);
+      const int c = min(c0 + u % (CH * 16) / 16, chunks - 1);
+      const uint16_t* from = DOWN ? (u / (CH * 16) % 2 ? hhi : hlo) : static_cast<const uint16_t*>(a.x);
+      xq[i] = *reinterpret_cast<const u32x4v*>(from + (DOWN ? l.pair[at] : l.token[at]) * L + c * 128 + u % 16 * 8);
+    }
+    if (st % SSteps == 0) {
+      // 16 bytes a lane; the last rows' may reach past the array and are moved back
+#pragma unroll
+      for (int u = 0; u < SQ; ++u) {
+        const int i = 32 * u + lane / 2;
+        const int64_t row = row0 + (GATED ? i / 32 * R + i % 32 : i);
+        const int64_t want = row * (L / SB) + min(c0, chunks - 1) * (128 / SB) + lane % 2 * 16;
+        const int64_t have = want < scale_end ? want : scale_end;
+        shift[u] = (int)(have - want);
+        sq[u] = *reinterpret_cast<const u32x4v_4*>(scales + have);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < RS; ++i) {
-      const int64_t row = row0 + (GATED ? i * R : 16 * i);
+      const int64_t row = row0 + r + (GATED ? i / RF * R + 16 * (i % RF) : 16 * i);
 #pragma unroll
       for (int x = 0; x < CH; ++x) {
-        const int c = min(c_first + st * CH + x, chunks - 1);
+        const int c = min(c0 + x, chunks - 1);
         w[i][x] = *reinterpret_cast<const u32x4v*>(codes + row * (L / 2) + c * 64 + 16 * g);
-        sc[i][x] = load_scale<NV>(scales + row * (L / SB), c, g);
       }
     }
   };
@@ -377,117 +431,107 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
   for (int q = (int)blockIdx.x; q < rounds; q += (int)gridDim.x) {
     const int j = q * jobs_at_once + mine;
     const bool real = j < jobs;
-    const int ai = (real ? j : jobs - 1) / groups;
-    const int n = l.n[ai], first = l.first[ai];
-    int most = 1;                            // tiles of the round's longest list
-    for (int i = 0; NT > 1 && i < jobs_at_once; ++i)
-      most = max(most, (l.n[min(q * jobs_at_once + i, jobs - 1) / groups] + 15) / 16);
-    f32x4 acc[NT][RS];
+    int ai, group;
+    decode(real ? j : jobs - 1, ai, group);
+    const int n = l.n[ai];
+    f32x4 acc[RS];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < RS; ++i) acc[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < RS; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     for (int st = 0; st < steps; ++st) {
       u32x4v wc[RS][CH];
-      uint32_t scc[RS][CH];
+#pragma unroll
+      for (int i = 0; i < RS; ++i) {
+#pragma unroll
+        for (int x = 0; x < CH; ++x) wc[i][x] = w[i][x];
+      }
+      const int c0 = c_first + st * CH;
+      if (st % SSteps == 0) {
+#pragma unroll
+        for (int u = 0; u < SQ; ++u)
+          *reinterpret_cast<u32x4v_4*>(own.scales + 16 + (32 * u + lane / 2) * SStride + lane % 2 * 16 + shift[u]) = sq[u];
+      }
+#pragma unroll
+      for (int i = 0; i < XQ; ++i) {
+        if (i * 64 / CLanes >= n) break;
+        const int u = i * 64 + lane;
+        *reinterpret_cast<u32x4v*>(own.columns + u / CLanes * CStride + u % CLanes * 16) = xq[i];
+      }
+      wave_lds_fence();
+      uint32_t sc[RS][CH];
 #pragma unroll
       for (int i = 0; i < RS; ++i) {
 #pragma unroll
         for (int x = 0; x < CH; ++x) {
-          wc[i][x] = w[i][x];
-          scc[i][x] = sc[i][x];
+          const uint8_t* from = own.scales + 16 + (16 * i + r) * SStride + (st % SSteps * CH + x) * (128 / SB);
+          if constexpr (NV) sc[i][x] = *reinterpret_cast<const uint16_t*>(from + 2 * g);
+          else sc[i][x] = from[g];
         }
       }
-      const int c0 = c_first + st * CH;
-      // A tile's columns: lanes past the list read nothing (their columns go
-      // nowhere). The first tile's are asked for before the next weights, which
-      // then stay in flight: loads return in order.
-      bf16x8 b[CH][PL][4];
-      auto columns = [&](int t) {
-        if (16 * t + r >= n) return;
-        const int at = first + 16 * t + r;
-        const int64_t from = (DOWN ? l.pair[at] : l.token[at]) * L + 32 * g;
-#pragma unroll
-        for (int x = 0; x < CH; ++x) {
-          const int c = min(c0 + x, chunks - 1);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            if constexpr (DOWN) {
-              b[x][0][m] = *reinterpret_cast<const bf16x8*>(hlo + from + c * 128 + 8 * m);
-              b[x][1][m] = *reinterpret_cast<const bf16x8*>(hhi + from + c * 128 + 8 * m);
-            } else {
-              b[x][0][m] = *reinterpret_cast<const bf16x8*>(static_cast<const uint16_t*>(a.x) + from + c * 128 + 8 * m);
-            }
-          }
-        }
-      };
-      columns(0);
-      asm volatile("" ::: "memory");
       if (st + 1 < steps) load(q, st + 1);
       else if (q + (int)gridDim.x < rounds) load(q + (int)gridDim.x, 0);
-      asm volatile("" ::: "memory");
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (16 * t >= n) break;
-        if (t > 0) columns(t);
+      for (int x = 0; x < CH; ++x) {
+        if (c0 + x >= c_end || !real) continue;              // loaded to no use
+        bf16x8 b[PL][4];                     // columns past the list: some other's, they go nowhere
 #pragma unroll
-        for (int x = 0; x < CH; ++x) {
-          if (c0 + x >= c_end || !real) continue;            // loaded to no use
+        for (int u = 0; u < PL; ++u)
 #pragma unroll
-          for (int i = 0; i < RS; ++i)
+          for (int m = 0; m < 4; ++m)
+            b[u][m] = *reinterpret_cast<const bf16x8*>(own.columns + min(r, n - 1) * CStride +
+                                                       (u * CH + x) * 256 + g * 64 + m * 16);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const bf16x8 f = dequant<NV>(wc[i][x], scc[i][x], m);
+        for (int i = 0; i < RS; ++i)
 #pragma unroll
-              for (int u = 0; u < PL; ++u)
-                acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, b[x][u][m], acc[t][i], 0, 0, 0);
-            }
-        }
-      }
-    }
+          for (int m = 0; m < 4; ++m) {
+            const bf16x8 f = dequant<NV>(wc[i][x], sc[i][x], m);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (t >= most) break;
-#pragma unroll
-      for (int i = 0; i < RS; ++i) red[wave][i][lane] = acc[t][i];
-      __syncthreads();
-      // item: four rows of a slice, one column
-      for (int it = tid; it < jobs_at_once * RF * 64; it += kThreads) {
-        const int li = it & 63, s = it / 64 % RF, jm = it / 64 / RF;
-        const int jj = q * jobs_at_once + jm;
-        if (jj >= jobs) continue;
-        const int aj = jj / groups, col = 16 * t + (li & 15);
-        if (col >= l.n[aj]) continue;
-        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f}, u = v;
-        for (int i = 0; i < 1 << lg; ++i) {
-          v += red[(jm << lg) + i][s][li];
-          if constexpr (GATED) u += red[(jm << lg) + i][RF + s][li];
-        }
-        const int e = l.expert[aj], p = l.pair[l.first[aj] + col];
-        const int64_t at = p * R + jj % groups * (16 * RF) + 16 * s + 4 * (li >> 4);
-        if constexpr (DOWN) {
-          *reinterpret_cast<f32x4*>(y + at) = v;
-        } else {
-          const float o1 = NV ? a.w1_outer[e] : 1.0f;
-          const float go = gates[p] * (NV ? a.w2_outer[e] : 1.0f);
-          float h[4], lo[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            h[i] = activate(v[i] * o1, a.act);
-            if constexpr (GATED) h[i] *= u[i] * o1;
-            h[i] *= go;
+            for (int u = 0; u < PL; ++u)
+              acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, b[u][m], acc[i], 0, 0, 0);
           }
-          const uint32_t h01 = pk_bf16(h[0], h[1]), h23 = pk_bf16(h[2], h[3]);
-          lo[0] = h[0] - u2f(h01 << 16);
-          lo[1] = h[1] - u2f(h01 & 0xFFFF0000u);
-          lo[2] = h[2] - u2f(h23 << 16);
-          lo[3] = h[3] - u2f(h23 & 0xFFFF0000u);
-          *reinterpret_cast<uint2*>(hhi + at) = make_uint2(h01, h23);
-          *reinterpret_cast<uint2*>(hlo + at) = make_uint2(pk_bf16(lo[0], lo[1]), pk_bf16(lo[2], lo[3]));
-        }
       }
-      __syncthreads();
+      wave_lds_fence();
     }
+#pragma unroll
+    for (int i = 0; i < RS; ++i) red[wave][i][lane] = acc[i];
+    __syncthreads();
+    // item: four rows of a slice, one column
+    for (int it = tid; it < jobs_at_once * RF * 64; it += kThreads) {
+      const int li = it & 63, s = it / 64 % RF, jm = it / 64 / RF;
+      const int jj = q * jobs_at_once + jm;
+      if (jj >= jobs) continue;
+      int aj, gj;
+      decode(jj, aj, gj);
+      const int col = li & 15;
+      if (col >= l.n[aj]) continue;
+      f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f}, u = v;
+      for (int i = 0; i < 1 << lg; ++i) {
+        v += red[(jm << lg) + i][s][li];
+        if constexpr (GATED) u += red[(jm << lg) + i][RF + s][li];
+      }
+      const int e = l.expert[aj], p = l.pair[l.first[aj] + col];
+      const int64_t at = p * R + gj * (16 * RF) + 16 * s + 4 * (li >> 4);
+      if constexpr (DOWN) {
+        *reinterpret_cast<f32x4*>(y + at) = v;
+      } else {
+        const float o1 = NV ? a.w1_outer[e] : 1.0f;
+        const float go = gates[p] * (NV ? a.w2_outer[e] : 1.0f);
+        float h[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          h[i] = activate(v[i] * o1, a.act);
+          if constexpr (GATED) h[i] *= u[i] * o1;
+          h[i] *= go;
+        }
+        const uint32_t h01 = pk_bf16(h[0], h[1]), h23 = pk_bf16(h[2], h[3]);
+        lo[0] = h[0] - u2f(h01 << 16);
+        lo[1] = h[1] - u2f(h01 & 0xFFFF0000u);
+        lo[2] = h[2] - u2f(h23 << 16);
+        lo[3] = h[3] - u2f(h23 & 0xFFFF0000u);
+        *reinterpret_cast<uint2*>(hhi + at) = make_uint2(h01, h23);
+        *reinterpret_cast<uint2*>(hlo + at) = make_uint2(pk_bf16(lo[0], lo[1]), pk_bf16(lo[2], lo[3]));
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -525,8 +569,7 @@ __global__ __launch_bounds__(256) void k_tokens_sum(TokensArgs a) {
 
 template <bool NV, Kind KIND>
 hipError_t product(const TokensArgs& a, unsigned grid, hipStream_t stream) {
-  auto k = a.T <= 16 ? k_tokens_product<NV, KIND, 1> : k_tokens_product<NV, KIND, 4>;
-  k<<<grid, kThreads, 0, stream>>>(a);
+  k_tokens_product<NV, KIND><<<grid, kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
