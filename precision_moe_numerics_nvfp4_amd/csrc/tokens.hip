@@ -47,9 +47,7 @@ constexpr int kMaxExperts = 1024;
 constexpr int kSelectHere = 16;
 constexpr float kNegInfT = -__builtin_huge_valf();
 
-constexpr int kCols = 16;                    // pairs of a list at most: a matrix instruction's columns
-
-// The pairs of the selected local experts in lists of up to kCols, an expert's
+// The pairs of the selected local experts in lists of up to COLS, an expert's
 // lists next to each other: in LDS, and in the workspace for the second product.
 struct Lists {
   int count;
@@ -230,14 +228,15 @@ __device__ __forceinline__ void select_all(const TokensArgs& a, int* ids, float*
 
 // The experts and gates of all tokens (selected here, or read where a launch
 // before has them) and the lists of pairs, by a whole workgroup.
+template <int COLS>
 __device__ __forceinline__ void route(const TokensArgs& a, Lists& l, float* gates) {
   __shared__ int ids[kTokensMaxPairs];
-  __shared__ int cnt[kMaxExperts];
+  __shared__ uint32_t members[2][kMaxExperts];               // an expert's tokens, a bit each
   __shared__ int16_t where[kMaxExperts];
   __shared__ int waves[kWavesT];
-  static_assert(2 * kThreads >= kMaxExperts && kThreads >= kTokensMaxPairs, "one pass of the threads");
+  static_assert(2 * kThreads >= kMaxExperts && kThreads >= kTokensMaxPairs && kTokensMaxT <= 64, "one pass of the threads");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  cnt[2 * tid] = cnt[2 * tid + 1] = 0;
+  for (int i = tid; i < kMaxExperts; i += kThreads) members[0][i] = members[1][i] = 0;
   if (a.T > kSelectHere) {
     if (tid < a.T * a.k) {
       ids[tid] = a.topk_ids[tid];
@@ -253,18 +252,20 @@ __device__ __forceinline__ void route(const TokensArgs& a, Lists& l, float* gate
     else select_all<16, false>(a, ids, gates);
   }
   __syncthreads();
-  // the order of pairs inside an expert is arbitrary (a pair is a column of its
-  // own: no result depends on it)
-  int le = -1, pos = 0;
+  // A token selects an expert at most once: a pair's place in its expert's lists
+  // is the number of earlier tokens there, the same in every workgroup.
+  const int t = tid / a.k;
+  int le = -1;
   if (tid < a.T * a.k) {
     le = ids[tid] - a.e0;
     if (ids[tid] < 0 || le < 0 || le >= a.n_local) le = -1;
-    if (le >= 0) pos = atomicAdd(&cnt[le], 1);
+    if (le >= 0) atomicOr(&members[t >> 5][le], 1u << (t & 31));
   }
   __syncthreads();
   // thread t: experts 2 t and 2 t + 1; lists and pairs before them in one scan
-  const int c0 = cnt[2 * tid], c1 = cnt[2 * tid + 1];
-  const int own = ((c0 + kCols - 1) / kCols + (c1 + kCols - 1) / kCols) << 16 | (c0 + c1);
+  auto size = [&](int e) { return __popc(members[0][e]) + __popc(members[1][e]); };
+  const int c0 = size(2 * tid), c1 = size(2 * tid + 1);
+  const int own = ((c0 + COLS - 1) / COLS + (c1 + COLS - 1) / COLS) << 16 | (c0 + c1);
   int incl = own;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -280,13 +281,13 @@ __device__ __forceinline__ void route(const TokensArgs& a, Lists& l, float* gate
     all += waves[i];
   }
   auto list = [&](int e, int c) {
-    const int lead = before >> 16, lists = (c + kCols - 1) / kCols, first = before & 0xFFFF;
+    const int lead = before >> 16, lists = (c + COLS - 1) / COLS, first = before & 0xFFFF;
     for (int i = 0; i < lists; ++i) {
       l.expert[lead + i] = (int16_t)e;
       l.lead[lead + i] = (int16_t)lead;
       l.lists[lead + i] = (int16_t)lists;
-      l.n[lead + i] = (int16_t)min(c - i * kCols, kCols);
-      l.first[lead + i] = (int16_t)(first + i * kCols);
+      l.n[lead + i] = (int16_t)min(c - i * COLS, COLS);
+      l.first[lead + i] = (int16_t)(first + i * COLS);
     }
     if (c > 0) where[e] = (int16_t)first;
     before += lists << 16 | c;
@@ -296,23 +297,26 @@ __device__ __forceinline__ void route(const TokensArgs& a, Lists& l, float* gate
   if (tid == 0) l.count = all >> 16;
   __syncthreads();
   if (le >= 0) {
-    const int at = where[le] + pos;
+    const uint32_t m0 = members[0][le], m1 = members[1][le], below = (1u << (t & 31)) - 1;
+    const int at = where[le] + (t < 32 ? __popc(m0 & below) : __popc(m0) + __popc(m1 & below));
     l.pair[at] = (int16_t)tid;
-    l.token[at] = (int16_t)(tid / a.k);
+    l.token[at] = (int16_t)t;
   }
   __syncthreads();
 }
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 enum Kind { kUp, kUpGated, kDown };
 constexpr int RS = 4;                        // slices of 16 rows in a job (gated: half of each matrix)
 
 // A grid-wide list of jobs, (list of pairs, 16 RF rows of its product): W1 x
 // with the activation to h, or W2 h to y.
-template <bool NV, Kind KIND>
+template <bool NV, Kind KIND, int COLS>
 __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
   constexpr bool DOWN = KIND == kDown, GATED = KIND == kUpGated;
   constexpr int RF = GATED ? RS / 2 : RS;                    // slices of the product
-  constexpr int CH = DOWN ? 1 : 2;                           // 128-element chunks of a piece
+  constexpr int CH = DOWN && COLS > 8 ? 1 : 2;                 // 128-element chunks of a piece
   constexpr int PL = DOWN ? 2 : 1;                           // parts of the other operand
   constexpr int SB = NV ? 16 : 32;                           // elements of a scale
   // A wavefront's own LDS. Scales: of its rows, 32 bytes of each at a time (one
@@ -320,11 +324,11 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
   // all of them.
   constexpr int SStride = 32 + 16, SChunks = 32 * SB / 128, SQ = RS / 2;
   constexpr int SSteps = SChunks / CH;                       // steps that a block of scales lasts
-  constexpr int CBytes = CH * PL * 256, CStride = CBytes + 16, XQ = kCols * CBytes / 1024;
+  constexpr int CBytes = CH * PL * 256, CStride = CBytes + 16, XQ = COLS * CBytes / 1024;
   constexpr int CLanes = CBytes / 16;                        // lanes that hold a column
   struct Own {
     uint8_t scales[16 + 16 * RS * SStride];
-    uint8_t columns[kCols * CStride];
+    uint8_t columns[COLS * CStride];
   };
   __shared__ Lists l;
   __shared__ float gates[DOWN ? 1 : kTokensMaxPairs];
@@ -338,7 +342,7 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
       reinterpret_cast<int*>(&l)[i] = reinterpret_cast<const int*>(a.ws)[i];
     __syncthreads();
   } else {
-    route(a, l, gates);
+    route<COLS>(a, l, gates);
     if (blockIdx.x == 0)
       for (int i = tid; i < words; i += kThreads)
         reinterpret_cast<int*>(a.ws)[i] = reinterpret_cast<int*>(&l)[i];
@@ -385,55 +389,66 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
       group = u / n;
     }
   };
-  const int64_t scale_end = (int64_t)a.n_local * rows_e * (L / SB) - 16;
   u32x4v w[RS][CH], xq[XQ], sq[SQ];
   int shift[SQ] = {};                        // of this lane's scales in LDS
-  // The piece of round q and step st; past the end: some piece, not used. The
-  // columns and scales before the codes: loads return in order.
-  auto load = [&](int q, int st) {
-    const int j = min(q * jobs_at_once + mine, jobs - 1);
+  // The job that loads are for: uniform bases, and 32 bits of offset a lane.
+  const uint32_t w_lane = r * (uint32_t)(L / 2) + 16 * g;
+  uint32_t x_lane[XQ];
+  int64_t row0 = 0;
+  int n_next = 0;
+  auto take = [&](int q) {
     int ai, group;
-    decode(j, ai, group);
-    const int n = l.n[ai], first = l.first[ai];
-    const int64_t row0 = l.expert[ai] * rows_e + group * (16 * RF);
-    const int c0 = c_first + st * CH;
+    decode(min(q * jobs_at_once + mine, jobs - 1), ai, group);
+    row0 = uniform(l.expert[ai]) * rows_e + uniform(group) * (16 * RF);
+    n_next = uniform(l.n[ai]);
+    const int first = uniform(l.first[ai]);
 #pragma unroll
     for (int i = 0; i < XQ; ++i) {
-      if (i * 64 / CLanes >= n) break;
-      const int u = i * 64 + lane, at = first + min(u / CLanes, n - 1);
-      const int c = min(c0 + u % (CH * 16) / 16, chunks - 1);
+      if (i * 64 / CLanes >= n_next) break;
+      const int u = i * 64 + lane, at = first + min(u / CLanes, n_next - 1);
+      x_lane[i] = (uint32_t)(DOWN ? l.pair[at] : l.token[at]) * (uint32_t)(2 * L) + u % 16 * 16;
+    }
+  };
+  // Its piece of step st. The columns and scales before the codes: loads return
+  // in order.
+  auto load = [&](int st) {
+    const int c0 = min(c_first + st * CH, chunks - 1);
+#pragma unroll
+    for (int i = 0; i < XQ; ++i) {
+      if (i * 64 / CLanes >= n_next) break;
+      const int u = i * 64 + lane;
+      const uint32_t chunk = CH > 1 ? min(u / 16 % CH, chunks - 1 - c0) * 256 : 0;
       const uint16_t* from = DOWN ? (u / (CH * 16) % 2 ? hhi : hlo) : static_cast<const uint16_t*>(a.x);
-      xq[i] = *reinterpret_cast<const u32x4v*>(from + (DOWN ? l.pair[at] : l.token[at]) * L + c * 128 + u % 16 * 8);
+      xq[i] = *reinterpret_cast<const u32x4v*>(reinterpret_cast<const char*>(from + c0 * 128) + (x_lane[i] + chunk));
     }
     if (st % SSteps == 0) {
       // 16 bytes a lane; the last rows' may reach past the array and are moved back
+      const int64_t at = row0 * (L / SB) + c0 * (128 / SB);
 #pragma unroll
       for (int u = 0; u < SQ; ++u) {
-        const int i = 32 * u + lane / 2;
-        const int64_t row = row0 + (GATED ? i / 32 * R + i % 32 : i);
-        const int64_t want = row * (L / SB) + min(c0, chunks - 1) * (128 / SB) + lane % 2 * 16;
-        const int64_t have = want < scale_end ? want : scale_end;
-        shift[u] = (int)(have - want);
-        sq[u] = *reinterpret_cast<const u32x4v_4*>(scales + have);
+        const int64_t base = at + (GATED ? u * R : 32 * u) * (L / SB);
+        const int left = (int)min((int64_t)a.n_local * rows_e * (L / SB) - 16 - base, (int64_t)0x7FFFFFFF);
+        const int want = (lane / 2) * (int)(L / SB) + lane % 2 * 16, have = min(want, left);
+        shift[u] = have - want;
+        sq[u] = *reinterpret_cast<const u32x4v_4*>(scales + base + (uint32_t)have);
       }
     }
 #pragma unroll
     for (int i = 0; i < RS; ++i) {
-      const int64_t row = row0 + r + (GATED ? i / RF * R + 16 * (i % RF) : 16 * i);
+      const uint8_t* row = codes + (row0 + (GATED ? i / RF * R + 16 * (i % RF) : 16 * i)) * (L / 2);
 #pragma unroll
-      for (int x = 0; x < CH; ++x) {
-        const int c = min(c0 + x, chunks - 1);
-        w[i][x] = *reinterpret_cast<const u32x4v*>(codes + row * (L / 2) + c * 64 + 16 * g);
-      }
+      for (int x = 0; x < CH; ++x)
+        w[i][x] = *reinterpret_cast<const u32x4v*>(row + min(c0 + x, chunks - 1) * 64 + w_lane);
     }
   };
-  if ((int)blockIdx.x < rounds) load((int)blockIdx.x, 0);
+  if ((int)blockIdx.x < rounds) {
+    take((int)blockIdx.x);
+    load(0);
+  }
   for (int q = (int)blockIdx.x; q < rounds; q += (int)gridDim.x) {
     const int j = q * jobs_at_once + mine;
     const bool real = j < jobs;
-    int ai, group;
-    decode(real ? j : jobs - 1, ai, group);
-    const int n = l.n[ai];
+    const int n = n_next;
     f32x4 acc[RS];
 #pragma unroll
     for (int i = 0; i < RS; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -467,8 +482,12 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
           else sc[i][x] = from[g];
         }
       }
-      if (st + 1 < steps) load(q, st + 1);
-      else if (q + (int)gridDim.x < rounds) load(q + (int)gridDim.x, 0);
+      if (st + 1 < steps) {
+        load(st + 1);
+      } else if (q + (int)gridDim.x < rounds) {
+        take(q + (int)gridDim.x);
+        load(0);
+      }
 #pragma unroll
       for (int x = 0; x < CH; ++x) {
         if (c0 + x >= c_end || !real) continue;              // loaded to no use
@@ -567,9 +586,12 @@ __global__ __launch_bounds__(256) void k_tokens_sum(TokensArgs a) {
     *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at) = v;
 }
 
+// Lists of 8 leave the second product room for two chunks of weights in flight,
+// lists of 16 read a busy expert's weights half as often.
 template <bool NV, Kind KIND>
 hipError_t product(const TokensArgs& a, unsigned grid, hipStream_t stream) {
-  k_tokens_product<NV, KIND><<<grid, kThreads, 0, stream>>>(a);
+  auto k = a.T * a.k > 7 * a.E ? k_tokens_product<NV, KIND, 16> : k_tokens_product<NV, KIND, 8>;
+  k<<<grid, kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

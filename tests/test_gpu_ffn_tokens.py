@@ -82,7 +82,7 @@ def _check(nv, c, k, n, out_dtype="bfloat16", **how):
     (1, 1, 1, 1, 0, 128, 128), (1, 2, 8, 8, 0, 256, 384), (3, 2, 8, 3, 2, 640, 128), (16, 2, 4, 4, 0, 128, 256),
     (17, 3, 12, 6, 3, 256, 128), (33, 8, 130, 30, 60, 128, 256), (64, 8, 64, 16, 16, 384, 128),
     (64, 1, 2, 2, 0, 256, 256), (5, 16, 500, 40, 100, 128, 128), (2, 4, 1024, 1024, 0, 128, 128),
-    (1, 8, 16, 16, 0, 2176, 640),
+    (1, 8, 16, 16, 0, 2176, 640), (64, 2, 2, 2, 0, 1024, 1024), (47, 2, 5, 5, 0, 1152, 640), (30, 3, 40, 3, 20, 512, 640),
 ])
 def test_sizes(nv, fmt, T, k, E, n, e0, K, F):
     c = _case(T + K, T, k, E, n, K, F, fmt)
