@@ -131,9 +131,11 @@ __device__ __forceinline__ void select(const TokensArgs& a, int t, int& id, floa
     denom = wave_sum(denom);
   }
   id = -1;
+  float v = 0.0f;
   for (int j = 0; j < a.k; ++j) {
     uint32_t bh = hi[0], bl = BIAS ? lo[0] : 0;
     int bi = lane;
+    float bx = x[0];
 #pragma unroll
     for (int i = 1; i < NE; ++i) {
       bool more = hi[i] > bh;
@@ -141,6 +143,7 @@ __device__ __forceinline__ void select(const TokensArgs& a, int t, int& id, floa
       bh = more ? hi[i] : bh;
       if constexpr (BIAS) bl = more ? lo[i] : bl;
       bi = more ? lane + 64 * i : bi;
+      bx = more ? x[i] : bx;
     }
     const uint32_t mh = wave_max(bh);
     if (mh == 0) break;                      // no expert left
@@ -149,8 +152,18 @@ __device__ __forceinline__ void select(const TokensArgs& a, int t, int& id, floa
       const uint32_t ml = wave_max(best ? bl : 0u);
       best = best && bl == ml;
     }
-    const int e = (int)wave_min(best ? (uint32_t)bi : 0xFFFFu);
-    if (lane == j) id = e;
+    uint64_t who = __ballot(best);
+    if (who & (who - 1)) {                   // equals: the lowest index
+      const int e = (int)wave_min(best ? (uint32_t)bi : 0xFFFFu);
+      who = __ballot(best && bi == e);
+    }
+    const int from = __builtin_ctzll(who);
+    const int e = __builtin_amdgcn_readlane(bi, from);
+    const float ex = u2f(__builtin_amdgcn_readlane(f2u(bx), from));
+    if (lane == j) {
+      id = e;
+      v = ex;
+    }
 #pragma unroll
     for (int i = 0; i < NE; ++i)
       if (lane + 64 * i == e) hi[i] = 0;
@@ -162,7 +175,6 @@ __device__ __forceinline__ void select(const TokensArgs& a, int t, int& id, floa
   }
   float s = 0.0f;
   if (id >= 0) {
-    const float v = logit(a, (int64_t)t * a.E + id);
     s = a.sigmoid ? 1.0f / (1.0f + expf(-v)) : expf(v - top) / denom;
     s = s < 0x1p-126f ? 0.0f : s;
   }
@@ -362,11 +374,12 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
   // S = 2^lg wavefronts share a job's contraction, per chunks each in steps of
   // CH; the workgroup has kWavesT / S jobs at once. The split of the fewest
   // steps over all rounds, a round's join counted as half of one.
-  int lg = 0, least = 0x7FFFFFFF;
+  int lg = 0;
+  float least = __builtin_huge_valf();
   for (int i = 0; 1 << i <= kWavesT && (i == 0 || 1 << (i - 1) < chunks); ++i) {
-    const int slots = (kWavesT >> i) * (int)gridDim.x;
-    const int st = ((chunks + (1 << i) - 1) / (1 << i) + CH - 1) / CH;
-    const int cost = (jobs + slots - 1) / slots * (2 * st + 1);
+    const int st = (((chunks + (1 << i) - 1) >> i) + CH - 1) / CH;
+    const float turns = ceilf((float)jobs * (1 << i) * __builtin_amdgcn_rcpf((float)(kWavesT * (int)gridDim.x)));
+    const float cost = turns * (float)(2 * st + 1);
     if (cost <= least) {
       least = cost;
       lg = i;
@@ -565,17 +578,17 @@ __global__ __launch_bounds__(256) void k_tokens_sum(TokensArgs a) {
                    (int64_t)t * a.k * a.K + col;
   const int32_t* ids = a.topk_ids + (int64_t)t * a.k;
   f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j0 = 0; j0 < a.k; j0 += 4) {
-    f32x4 u[4];
-    int id[4];
+  for (int j0 = 0; j0 < a.k; j0 += 8) {
+    f32x4 u[8];
+    int id[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const int at = min(j0 + j, a.k - 1);
       id[j] = j0 + j < a.k ? ids[at] : -1;
       u[j] = *reinterpret_cast<const f32x4*>(y + at * a.K);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 8; ++j)
       if (id[j] >= 0 && id[j] >= a.e0 && (int64_t)id[j] - a.e0 < a.n_local) v += u[j];
   }
   const int64_t at = (int64_t)t * a.K + col;
