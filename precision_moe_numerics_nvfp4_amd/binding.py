@@ -143,7 +143,10 @@ def _torch():
 
 
 def _dev(t, name, dtype=None, ndim=None):
-    torch = _torch()
+    torch = _TORCH or _torch()
+    if t.__class__ is torch.Tensor and t.is_cuda and t.is_contiguous() and \
+            (dtype is None or t.dtype is dtype) and (ndim is None or t.dim() == ndim):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -685,7 +688,7 @@ def moe_bwd_wgrad_nvfp4(dyT, xT, padded_offsets, N, K, dw=None):
 def _launch(dev, name, *args):
     """Call the library with ``dev`` as the current device, on its current
     stream (the last argument of every call), and check the status."""
-    torch = _torch()
+    torch = _TORCH or _torch()
     f = getattr(_LIB or lib(), name)
     stream = torch._C._cuda_getCurrentRawStream(dev.index)
     if torch._C._cuda_getDevice() == dev.index:
@@ -700,7 +703,7 @@ def _launch(dev, name, *args):
 def _on(t, name, dtype, shape, dev):
     """The address of a tensor that goes with another one: its type, shape
     and device."""
-    if t.__class__ is not _torch().Tensor or t.dtype != dtype or not t.is_contiguous():
+    if t.__class__ is not (_TORCH or _torch()).Tensor or t.dtype is not dtype or not t.is_contiguous():
         _dev(t, name, dtype)
     if t.shape != shape or t.device != dev:
         raise ValueError(f"{name} must have shape {tuple(shape)} on {dev} "
@@ -983,17 +986,18 @@ def _c_size_of(v, name, bits=64):
 
 def _mxfp4_pair(codes, scales, name, dev):
     """Addresses, rows and columns of an MXFP4 tensor (any leading dimensions)."""
-    torch = _torch()
-    _dev(codes, f"{name} codes", torch.uint8)
-    if codes.dim() < 2:
-        raise ValueError(f"{name} codes must have at least 2 dimensions (got {codes.dim()})")
-    half = codes.shape[-1]
+    u8 = (_TORCH or _torch()).uint8
+    _dev(codes, name, u8)
+    shape = codes.shape
+    if len(shape) < 2:
+        raise ValueError(f"{name} codes must have at least 2 dimensions (got {len(shape)})")
+    half = shape[-1]
     rows = codes.numel() // half if half else 0
     if half % 16:
         raise ValueError(f"{name} codes must hold whole blocks of 32 (got {2 * half} columns)")
     if codes.device != dev:
         raise ValueError(f"{name} codes must be on {dev} (got {codes.device})")
-    _dev(scales, f"{name} scales", torch.uint8)
+    _dev(scales, name, u8)
     if scales.device != dev or scales.numel() != rows * (half // 16) or scales.shape[-1] != half // 16:
         raise ValueError(f"{name} scales must hold {half // 16} bytes for each of {rows} rows on {dev} "
                          f"(got {tuple(scales.shape)} on {scales.device})")
@@ -1004,7 +1008,7 @@ def mxfp4_quantize(x, offsets=None, codes=None, scales=None):
     """x [rows, cols] float32|bfloat16 -> MXFP4 (codes [rows, cols/2] u8, scales
     [rows, cols/32] u8). With ``offsets`` (moe_group's) only the routed rows
     r < offsets[-1]; later rows of the outputs untouched."""
-    torch = _torch()
+    torch = _TORCH or _torch()
     _dev(x, "x", ndim=2)
     rows, cols = x.shape
     dev, live = x.device, None
@@ -1023,7 +1027,7 @@ def mxfp4_quantize(x, offsets=None, codes=None, scales=None):
 
 
 def _dequantize(fn, q, scales, rows, cols, dev, out_dtype, out):
-    torch = _torch()
+    torch = _TORCH or _torch()
     o = {"out": out}
     dtype = out.dtype if out is not None else (out_dtype or torch.float32)
     code = _out_dtype(dtype)
@@ -1040,7 +1044,7 @@ def mxfp4_dequantize(codes, scales, out_dtype=None, out=None):
 
 def mxfp8_dequantize(e4m3, e8m0, out_dtype=None, out=None):
     """Values [rows, cols] (float32|bfloat16) of MXFP8 elements [rows, cols]."""
-    torch = _torch()
+    torch = _TORCH or _torch()
     _dev(e4m3, "e4m3", torch.uint8, 2)
     rows, cols = e4m3.shape
     if cols % 32:
@@ -1054,7 +1058,7 @@ def moe_group(topk_ids, e0, n_local, workspace=None, out=None):
     padded_offsets (int64 [n_local+1]), row_token, row_slot (int32 [T*k]; rows
     >= offsets[-1] untouched) and pair_row (int32 [T, k]; an ``out`` dict
     without it asks for none)."""
-    torch = _torch()
+    torch = _TORCH or _torch()
     _dev(topk_ids, "topk_ids", torch.int32, 2)
     T, k = topk_ids.shape
     e0, n_local = _c_size_of(e0, "e0", 32), _c_size_of(n_local, "n_local", 32)
@@ -1089,7 +1093,7 @@ def moe_fwd_grouped_gemm_mxfp4(a_codes, a_scales, b_codes, b_scales, offsets, ro
     [G*N, K] or [G, N, K]; offsets int64 [G+1] on the device. With ``row_token``
     (int32 [m_cap], moe_group's) row r reads activation row row_token[r], else
     row r. Rows >= offsets[-1] of y are untouched."""
-    torch = _torch()
+    torch = _TORCH or _torch()
     _dev(a_codes, "a codes", ndim=2)
     dev = a_codes.device
     ac, as_, rows, K = _mxfp4_pair(a_codes, a_scales, "a", dev)
@@ -1116,7 +1120,7 @@ def mxfp8_requant_sr_mxfp4(codes, scales, offsets, padded_offsets, P, seed, tag,
     transpose, as mxfp8_requant_sr: activations [cols, P] (+ E8M0 [cols, P/32]),
     read through ``row_token`` where it is given; weights (rows_per_group)
     per-expert blocks [G * cols, rows_per_group], P = G * rows_per_group."""
-    torch = _torch()
+    torch = _TORCH or _torch()
     _dev(codes, "codes", ndim=2)
     dev = codes.device
     q, e, rows, cols = _mxfp4_pair(codes, scales, "mxfp4", dev)
@@ -1156,27 +1160,29 @@ def ffn_tokens_workspace_size(T, k, K, F):
 def _weight(w, name, dev):
     """Parts of a 4-bit weight: MXFP4 (codes, scales) or NVFP4 (codes, scales,
     outer [n_local]), its addresses, rows and columns."""
-    torch = _torch()
+    torch = _TORCH or _torch()
     if not isinstance(w, (tuple, list)) or len(w) not in _FORMATS:
         raise ValueError(f"{name} must be (codes, scales) in MXFP4 or (codes, scales, outer) in NVFP4")
     codes, scales = w[0], w[1]
-    _dev(codes, f"{name} codes", torch.uint8)
-    cols = 2 * codes.shape[-1] if codes.dim() >= 2 else 0
-    if codes.dim() < 2 or codes.device != dev or cols == 0:
+    _dev(codes, name, torch.uint8)
+    shape = codes.shape
+    cols = 2 * shape[-1] if len(shape) >= 2 else 0
+    if cols == 0 or codes.device != dev:
         raise ValueError(f"{name} codes must have rows of codes on {dev} "
-                         f"(got {tuple(codes.shape)} on {codes.device})")
+                         f"(got {tuple(shape)} on {codes.device})")
     rows, block = codes.numel() // (cols // 2), 32 if len(w) == 2 else 16
-    _dev(scales, f"{name} scales", torch.uint8)
-    if cols % 32 or scales.device != dev or scales.shape[-1] != cols // block or \
-            scales.numel() != rows * (cols // block):
+    _dev(scales, name, torch.uint8)
+    if cols % 32 or scales.numel() != rows * (cols // block) or scales.shape[-1] != cols // block or \
+            scales.device != dev:
         raise ValueError(f"{name} scales must hold a byte for {block} codes of each of {rows} rows on {dev} "
                          f"(got {tuple(scales.shape)} on {scales.device})")
     outer = None
     if len(w) == 3:
-        _dev(w[2], f"{name} outer", torch.float32, 1)
-        if w[2].device != dev:
-            raise ValueError(f"{name} outer must be on {dev} (got {w[2].device})")
-        outer = w[2].data_ptr()
+        outer = w[2]
+        _dev(outer, name, torch.float32, 1)
+        if outer.device != dev:
+            raise ValueError(f"{name} outer must be on {dev} (got {outer.device})")
+        outer = outer.data_ptr()
     return codes.data_ptr(), scales.data_ptr(), outer, rows, cols
 
 
@@ -1194,7 +1200,7 @@ def moe_ffn_tokens(x, logits, k, w1, w2, act="silu", gated=False, score="softmax
     [e0, e0+n_local). act 'none', 'relu2' or 'silu'. ``out`` may hold any of the
     results' buffers; ``workspace`` ffn_tokens_workspace_size(T, k, K, F) bytes,
     of one call at a time."""
-    torch = _torch()
+    torch = _TORCH or _torch()
     _dev(x, "x", torch.bfloat16, 2)
     T, K = x.shape
     dev = x.device
