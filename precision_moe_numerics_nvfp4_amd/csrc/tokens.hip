@@ -1,5 +1,5 @@
 // The whole expert layer for a few tokens: selection and gates, up-projection,
-// activation, down-projection and the weighted sum, in two kernels.
+// activation, down-projection and the weighted sum.
 //
 //   (ids, gate)[t]  as moe_route
 //   h[t, j]   = act(W1[e] x[t]), or act(W1a[e] x[t]) * (W1b[e] x[t]) with e = ids[t, j]
@@ -8,23 +8,35 @@
 // Weights are 4-bit (MXFP4 or NVFP4) and dequantized in registers; every
 // dequantized element (up to 6 significant bits) is exact in bfloat16, so the
 // products run on v_mfma_f32_16x16x32_bf16 with the weight rows as A and the
-// tokens as B. The activations are not quantized. h is carried between the
-// kernels as two bfloat16 parts (value and remainder, 16 bits together), each
-// with a product of its own: one part would cost half the output's last bit.
+// tokens as B. The activations are not quantized. h (with the gate and W2's outer
+// scale in it) is carried between the products as two bfloat16 parts, value and
+// remainder, 16 bits together, each with products of its own: one part would
+// cost half the output's last bit. y, a row of W2 h per pair, is float32.
 //
-// What bounds it is the weights' bytes: with up to 64 tokens each selected
-// expert's weights are read once.
+// Launches: past 16 tokens the router's own; up; down; the sum of a token's rows.
+// Up to 16 tokens every workgroup of the first product repeats the selection, a
+// wavefront to a token (16 tokens x 8 experts: 22.6 us the layer against 25.1
+// with the router's launch; 32 x 48: 102 against 98).
 //
-// k_tokens_up: every workgroup repeats the selection (a wavefront per token;
-// reading a result of another launch would cost more) and lists the pairs of
-// each local expert. A wavefront's piece of work is 16 RS rows of W1 by 256
-// elements, loaded while the piece before it is multiplied; the wavefronts that
-// share rows split the contraction and join through LDS.
-// k_tokens_down: a workgroup takes 16 rows of W2 for every selected expert, its
-// wavefronts split (expert, contraction). A column of a product is a pair; each
-// wavefront adds its columns to its own copy of the output rows in LDS, and the
-// copies are added at the end. Gates and W2's outer scales were multiplied into
-// h before.
+// What bounds it is the weights' bytes in flight: each selected expert's weights
+// are read once (a list of pairs at a time), the operations are few. So a
+// wavefront holds one piece, 64 rows of 128 or 256 elements, in registers while
+// the next is on its way, and what else has to be read comes in few requests:
+// the scales 32 bytes of a row at a time, the columns (tokens or h) a line at a
+// time, both through the wavefront's own LDS (a byte of scale and a fragment of
+// column a lane, straight to registers, took as many requests as the weights: 7
+// tokens gated 143 us instead of 96). Jobs go round a grid of one workgroup per
+// compute unit; a job's contraction is split over as many wavefronts as gives
+// the fewest steps, joined through LDS.
+//
+// Measured (MI355X): one token, 8 of 48 experts, 4096 -> 1536 -> 4096, NVFP4, 57
+// MB: 30 us, of it up 16.4 (1.7 launch, 3 selection and lists), down 13, sum 3.8;
+// 7 tokens, 6 of 48 experts, gated 4096 -> 2 x 2048 -> 4096, MXFP4, 390 MB: 88 us,
+// 4.4 TB/s; 64 tokens, 48 of 384 experts, NVFP4, 240 MB: 72 us, 3.3 TB/s (its
+// conversions, four vector instructions to two elements, are busy for half of
+// it, and 5 rounds of jobs are 4.2 rounds' work). Not kept: the last workgroup to
+// finish 64 columns adds their rows in the down launch (64 tokens 127 us, 7
+// tokens 96: every job waits for its rows to reach memory).
 #include "codecs.hpp"
 #include "internal.hpp"
 #include "lanes.hpp"
@@ -43,7 +55,8 @@ typedef u32x4v u32x4v_4 __attribute__((aligned(4)));
 constexpr int kThreads = 512;
 constexpr int kWavesT = kThreads / 64;
 constexpr int kMaxExperts = 1024;
-// Up to so many tokens every workgroup selects by itself; beyond, a launch before does.
+// Up to so many tokens every workgroup selects by itself; beyond, a launch before
+// does (16 tokens 22 us against 25, 32 tokens 102 against 98, 64 tokens 96 against 71).
 constexpr int kSelectHere = 16;
 constexpr float kNegInfT = -__builtin_huge_valf();
 
@@ -567,9 +580,8 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
   }
 }
 
-// out[t] = the sum of y over the token's pairs, slot by slot. A thread has four
-// columns of a token; a pair that is not local has no row of y (what is read
-// there is dropped).
+// out[t] = the sum of y over the token's local pairs, slot by slot. A thread has
+// four columns of a token.
 __global__ __launch_bounds__(256) void k_tokens_sum(TokensArgs a) {
   const int t = blockIdx.y;
   const int64_t col = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
@@ -580,16 +592,16 @@ __global__ __launch_bounds__(256) void k_tokens_sum(TokensArgs a) {
   f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int j0 = 0; j0 < a.k; j0 += 8) {
     f32x4 u[8];
-    int id[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int at = min(j0 + j, a.k - 1);
-      id[j] = j0 + j < a.k ? ids[at] : -1;
-      u[j] = *reinterpret_cast<const f32x4*>(y + at * a.K);
+      const int64_t le = (int64_t)ids[at] - a.e0;
+      u[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (j0 + j < a.k && ids[at] >= 0 && le >= 0 && le < a.n_local)
+        u[j] = *reinterpret_cast<const f32x4*>(y + at * a.K);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (id[j] >= 0 && id[j] >= a.e0 && (int64_t)id[j] - a.e0 < a.n_local) v += u[j];
+    for (int j = 0; j < 8; ++j) v += u[j];
   }
   const int64_t at = (int64_t)t * a.K + col;
   if (a.out_bf16)
@@ -599,8 +611,11 @@ __global__ __launch_bounds__(256) void k_tokens_sum(TokensArgs a) {
     *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at) = v;
 }
 
-// Lists of 8 leave the second product room for two chunks of weights in flight,
-// lists of 16 read a busy expert's weights half as often.
+// Lists of 8 pairs leave the second product room for two chunks of weights in
+// flight (7 tokens over 48 experts, one pair an expert, 88 us against 96 with
+// lists of 16; 16 x 8 over 48 86 against 95; 40 x 8 over 48, 6.7 each, 99 against
+// 108). Lists of 16 read a busy expert's weights half as often (64 x 2 over 8, 16
+// each, 36 us against 45; 64 x 8 over 48, 10.7 each, 116 against 128).
 template <bool NV, Kind KIND>
 hipError_t product(const TokensArgs& a, unsigned grid, hipStream_t stream) {
   auto k = a.T * a.k > 7 * a.E ? k_tokens_product<NV, KIND, 16> : k_tokens_product<NV, KIND, 8>;
