@@ -84,7 +84,10 @@ __device__ __forceinline__ uint32_t codes8(const Eight<BF16>& r, float scale) {
   return w;
 }
 
-// A workgroup's wavefronts take runs of 64 U chunks of eight elements.
+// A workgroup's wavefronts take runs of 64 U chunks of eight elements, all loads
+// first. The bytes bound it: 262144 x 2048 bfloat16 205 us (1.36 GB, 6.6 TB/s),
+// 8002 x 1536 float32 of a buffer of 40009 rows 12 us (56 MB, 4.7 TB/s); U = 2
+// (bfloat16) and 1 measured 1 to 3% slower.
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_mxfp4_quantize(const void* __restrict__ x, int64_t chunks,
                                                         int64_t row_chunks,
