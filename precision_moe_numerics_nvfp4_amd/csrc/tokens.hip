@@ -330,6 +330,15 @@ __device__ __forceinline__ void route(const TokensArgs& a, Lists& l, float* gate
   __syncthreads();
 }
 
+typedef __attribute__((address_space(3))) void lds_void;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* p, uint32_t bytes) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uint64_t)hi << 32 | lo), (short)0,
+                                           (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 enum Kind { kUp, kUpGated, kDown };
@@ -344,16 +353,16 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
   constexpr int CH = DOWN && COLS > 8 ? 1 : 2;                 // 128-element chunks of a piece
   constexpr int PL = DOWN ? 2 : 1;                           // parts of the other operand
   constexpr int SB = NV ? 16 : 32;                           // elements of a scale
-  // A wavefront's own LDS. Scales: of its rows, 32 bytes of each at a time (one
-  // by one they would take as many requests as the codes). Columns: a piece of
-  // all of them.
-  constexpr int SStride = 32 + 16, SChunks = 32 * SB / 128, SQ = RS / 2;
+  // A wavefront's own LDS, filled by DMA. Scales: of its rows, 32 bytes of each at
+  // a time (one by one they would take as many requests as the codes). Columns: a
+  // piece of all of them, 16-byte part c of column r at c ^ (r & 7).
+  constexpr int SChunks = 32 * SB / 128, SQ = RS / 2;
   constexpr int SSteps = SChunks / CH;                       // steps that a block of scales lasts
-  constexpr int CBytes = CH * PL * 256, CStride = CBytes + 16, XQ = COLS * CBytes / 1024;
+  constexpr int CBytes = CH * PL * 256, XQ = COLS * CBytes / 1024;
   constexpr int CLanes = CBytes / 16;                        // lanes that hold a column
   struct Own {
-    uint8_t scales[16 + 16 * RS * SStride];
-    uint8_t columns[COLS * CStride];
+    uint8_t scales[RS * 16 * 32];
+    uint8_t columns[COLS * CBytes];
   };
   __shared__ Lists l;
   __shared__ float gates[DOWN ? 1 : kTokensMaxPairs];
@@ -415,13 +424,13 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
       group = u / n;
     }
   };
-  u32x4v w[RS][CH], xq[XQ], sq[SQ];
-  int shift[SQ] = {};                        // of this lane's scales in LDS
+  u32x4v w[RS][CH];
   // The job that loads are for: uniform bases, and 32 bits of offset a lane.
   const uint32_t w_lane = r * (uint32_t)(L / 2) + 16 * g;
   uint32_t x_lane[XQ];
   int64_t row0 = 0;
   int n_next = 0;
+  const uint32_t x_bytes = DOWN ? (uint32_t)(a.T * a.k) * (uint32_t)(4 * L) : (uint32_t)a.T * (uint32_t)(2 * L);
   auto take = [&](int q) {
     int ai, group;
     decode(min(q * jobs_at_once + mine, jobs - 1), ai, group);
@@ -431,32 +440,34 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
 #pragma unroll
     for (int i = 0; i < XQ; ++i) {
       if (i * 64 / CLanes >= n_next) break;
-      const int u = i * 64 + lane, at = first + min(u / CLanes, n_next - 1);
-      x_lane[i] = (uint32_t)(DOWN ? l.pair[at] : l.token[at]) * (uint32_t)(2 * L) + u % 16 * 16;
+      const int u = i * 64 + lane, col = u / CLanes, at = first + min(col, n_next - 1);
+      const int part = (u % CLanes) ^ (col & 7);             // of CH 256-byte runs, or of PL planes of them
+      x_lane[i] = (uint32_t)(DOWN ? l.pair[at] : l.token[at]) * (uint32_t)(2 * L) + part % 16 * 16 +
+                  (DOWN && part / (CH * 16) ? x_bytes / 2 : 0) + (CH > 1 ? part / 16 % CH << 31 : 0);
     }
   };
   // Its piece of step st. The columns and scales before the codes: loads return
   // in order.
   auto load = [&](int st) {
     const int c0 = min(c_first + st * CH, chunks - 1);
+    const auto xr = resource(DOWN ? static_cast<const void*>(hhi) : a.x, x_bytes);
 #pragma unroll
     for (int i = 0; i < XQ; ++i) {
       if (i * 64 / CLanes >= n_next) break;
-      const int u = i * 64 + lane;
-      const uint32_t chunk = CH > 1 ? min(u / 16 % CH, chunks - 1 - c0) * 256 : 0;
-      const uint16_t* from = DOWN ? (u / (CH * 16) % 2 ? hhi : hlo) : static_cast<const uint16_t*>(a.x);
-      xq[i] = *reinterpret_cast<const u32x4v*>(reinterpret_cast<const char*>(from + c0 * 128) + (x_lane[i] + chunk));
+      uint32_t at = x_lane[i] + c0 * 256;
+      if (CH > 1) at = (at & 0x7FFFFFFFu) + (x_lane[i] >> 31 && c0 + 1 < chunks ? 256 : 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(own.columns + i * 1024), 16, at, 0, 0, 0);
     }
     if (st % SSteps == 0) {
-      // 16 bytes a lane; the last rows' may reach past the array and are moved back
+      // 16 bytes a lane; what the last rows' reach past the array is not read
       const int64_t at = row0 * (L / SB) + c0 * (128 / SB);
 #pragma unroll
       for (int u = 0; u < SQ; ++u) {
         const int64_t base = at + (GATED ? u * R : 32 * u) * (L / SB);
-        const int left = (int)min((int64_t)a.n_local * rows_e * (L / SB) - 16 - base, (int64_t)0x7FFFFFFF);
-        const int want = (lane / 2) * (int)(L / SB) + lane % 2 * 16, have = min(want, left);
-        shift[u] = have - want;
-        sq[u] = *reinterpret_cast<const u32x4v_4*>(scales + base + (uint32_t)have);
+        const int64_t left = (int64_t)a.n_local * rows_e * (L / SB) - base;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            resource(scales + base, (uint32_t)min(left, (int64_t)0x7FFFFFFF)), (lds_void*)(own.scales + u * 1024), 16,
+            (lane / 2) * (int)(L / SB) + lane % 2 * 16, 0, 0, 0);
       }
     }
 #pragma unroll
@@ -486,28 +497,32 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
         for (int x = 0; x < CH; ++x) wc[i][x] = w[i][x];
       }
       const int c0 = c_first + st * CH;
-      if (st % SSteps == 0) {
+      // the codes are here, and so is what was asked for before them
 #pragma unroll
-        for (int u = 0; u < SQ; ++u)
-          *reinterpret_cast<u32x4v_4*>(own.scales + 16 + (32 * u + lane / 2) * SStride + lane % 2 * 16 + shift[u]) = sq[u];
-      }
+      for (int i = 0; i < RS; ++i)
 #pragma unroll
-      for (int i = 0; i < XQ; ++i) {
-        if (i * 64 / CLanes >= n) break;
-        const int u = i * 64 + lane;
-        *reinterpret_cast<u32x4v*>(own.columns + u / CLanes * CStride + u % CLanes * 16) = xq[i];
-      }
-      wave_lds_fence();
+        for (int x = 0; x < CH; ++x) asm volatile("" ::"v"(wc[i][x]) : "memory");
+      bf16x8 b[CH][PL][4];                   // columns past the list: some other's, they go nowhere
+      const int col = min(r, n - 1);
+#pragma unroll
+      for (int x = 0; x < CH; ++x)
+#pragma unroll
+        for (int u = 0; u < PL; ++u)
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            b[x][u][m] = *reinterpret_cast<const bf16x8*>(
+                own.columns + col * CBytes + ((((u * CH + x) * 16 + g * 4 + m) ^ (col & 7)) << 4));
       uint32_t sc[RS][CH];
 #pragma unroll
       for (int i = 0; i < RS; ++i) {
 #pragma unroll
         for (int x = 0; x < CH; ++x) {
-          const uint8_t* from = own.scales + 16 + (16 * i + r) * SStride + (st % SSteps * CH + x) * (128 / SB);
+          const uint8_t* from = own.scales + (16 * i + r) * 32 + (st % SSteps * CH + x) * (128 / SB);
           if constexpr (NV) sc[i][x] = *reinterpret_cast<const uint16_t*>(from + 2 * g);
           else sc[i][x] = from[g];
         }
       }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // read: free for the next piece's
       if (st + 1 < steps) {
         load(st + 1);
       } else if (q + (int)gridDim.x < rounds) {
@@ -517,13 +532,6 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
 #pragma unroll
       for (int x = 0; x < CH; ++x) {
         if (c0 + x >= c_end || !real) continue;              // loaded to no use
-        bf16x8 b[PL][4];                     // columns past the list: some other's, they go nowhere
-#pragma unroll
-        for (int u = 0; u < PL; ++u)
-#pragma unroll
-          for (int m = 0; m < 4; ++m)
-            b[u][m] = *reinterpret_cast<const bf16x8*>(own.columns + min(r, n - 1) * CStride +
-                                                       (u * CH + x) * 256 + g * 64 + m * 16);
 #pragma unroll
         for (int i = 0; i < RS; ++i)
 #pragma unroll
@@ -531,10 +539,9 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
             const bf16x8 f = dequant<NV>(wc[i][x], sc[i][x], m);
 #pragma unroll
             for (int u = 0; u < PL; ++u)
-              acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, b[u][m], acc[i], 0, 0, 0);
+              acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, b[x][u][m], acc[i], 0, 0, 0);
           }
       }
-      wave_lds_fence();
     }
 #pragma unroll
     for (int i = 0; i < RS; ++i) red[wave][i][lane] = acc[i];
