@@ -23,20 +23,21 @@
 // wavefront holds one piece, 64 rows of 128 or 256 elements, in registers while
 // the next is on its way, and what else has to be read comes in few requests:
 // the scales 32 bytes of a row at a time, the columns (tokens or h) a line at a
-// time, both through the wavefront's own LDS (a byte of scale and a fragment of
+// time, both by DMA to the wavefront's own LDS (a byte of scale and a fragment of
 // column a lane, straight to registers, took as many requests as the weights: 7
-// tokens gated 143 us instead of 96). Jobs go round a grid of one workgroup per
-// compute unit; a job's contraction is split over as many wavefronts as gives
-// the fewest steps, joined through LDS.
+// tokens gated 143 us; through registers and LDS 89, where the join of a
+// register's two values behind a branch waited for it; by DMA 85.5). Jobs go round
+// a grid of one workgroup per compute unit; a job's contraction is split over as
+// many wavefronts as gives the fewest steps, joined through LDS.
 //
 // Measured (MI355X): one token, 8 of 48 experts, 4096 -> 1536 -> 4096, NVFP4, 57
-// MB: 30 us, of it up 16.4 (1.7 launch, 3 selection and lists), down 13, sum 3.8;
-// 7 tokens, 6 of 48 experts, gated 4096 -> 2 x 2048 -> 4096, MXFP4, 390 MB: 88 us,
-// 4.4 TB/s; 64 tokens, 48 of 384 experts, NVFP4, 240 MB: 72 us, 3.3 TB/s (its
+// MB: 30 us, of it up 16 (1.7 launch, 3 selection and lists), down 12.5, sum 3.8;
+// 7 tokens, 6 of 48 experts, gated 4096 -> 2 x 2048 -> 4096, MXFP4, 390 MB: 85 us,
+// 4.6 TB/s; 64 tokens, 48 of 384 experts, NVFP4, 240 MB: 68 us, 3.5 TB/s (its
 // conversions, four vector instructions to two elements, are busy for half of
-// it, and 5 rounds of jobs are 4.2 rounds' work). Not kept: the last workgroup to
-// finish 64 columns adds their rows in the down launch (64 tokens 127 us, 7
-// tokens 96: every job waits for its rows to reach memory).
+// it, and the rounds of jobs do not come out even). Not kept: the last workgroup
+// to finish 64 columns adds their rows in the down launch (64 tokens 127 us for
+// 72, 7 tokens 96 for 89: every job waits for its rows to reach memory).
 #include "codecs.hpp"
 #include "internal.hpp"
 #include "lanes.hpp"
