@@ -140,9 +140,11 @@ __device__ __forceinline__ void select(const TokensArgs& a, int t, int& id, floa
   float denom = 0.0f;
   if (!a.sigmoid) {
     top = wave_max(top);
+    if (!a.renorm) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) denom += x[i] > kNegInfT ? expf(x[i] - top) : 0.0f;
-    denom = wave_sum(denom);
+      for (int i = 0; i < NE; ++i) denom += x[i] != kNegInfT ? expf(x[i] - top) : 0.0f;
+      denom = wave_sum(denom);
+    }
   }
   id = -1;
   float v = 0.0f;
@@ -189,12 +191,13 @@ __device__ __forceinline__ void select(const TokensArgs& a, int t, int& id, floa
   }
   float s = 0.0f;
   if (id >= 0) {
-    s = a.sigmoid ? 1.0f / (1.0f + expf(-v)) : expf(v - top) / denom;
+    // renormalised, the softmax's own sum cancels
+    s = a.sigmoid ? 1.0f / (1.0f + expf(-v)) : a.renorm ? expf(v - top) : expf(v - top) / denom;
     s = s < 0x1p-126f ? 0.0f : s;
   }
   if (a.renorm) {
     const float total = wave_sum(s);
-    s = total > 0.0f ? s / total : 0.0f;
+    s = total == 0.0f ? 0.0f : s / total;
   }
   gate = a.scale * s;
 }

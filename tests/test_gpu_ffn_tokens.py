@@ -158,6 +158,41 @@ def test_values_of_any_size(nv):
     _check(nv, c, 2, 5, act="none")
 
 
+@pytest.mark.parametrize("lo,hi,mul", [(0, 4, 100), (250, 253, -100), (60, 190, 0)])
+def test_scale_bytes_at_the_ends(nv, lo, hi, mul):
+    """The smallest and the largest MXFP4 scales (252 is the last that holds all codes), inputs that make up for them."""
+    c = _case(6, 3, 2, 4, 4, 256, 128, "mxfp4")
+    rng = np.random.default_rng(2)
+    c["x"] = gen.to_bf16_bits((rng.normal(size=(3, 256)) * 2.0 ** mul).astype(np.float32))
+    c["w1"] = (rng.integers(0, 256, c["w1"][0].shape).astype(np.uint8),
+               rng.integers(lo, hi, c["w1"][1].shape).astype(np.uint8))
+    _check(nv, c, 2, 4, "float32", act="none")
+
+
+def test_gates_of_rows_that_are_not_finite(nv):
+    """Ids are moe_route's in rows with NaN or +inf too; where its gates are NaN, these are, up to 16 tokens and beyond."""
+    import torch
+    for T in (5, 20):
+        lg = torch.randn(T, 24, device="cuda")
+        lg[0, 3], lg[1, 2], lg[1, 7], lg[2, 5] = float("inf"), float("inf"), float("inf"), float("nan")
+        c = _dev(_case(13, T, 4, 24, 24, 128, 128, "mxfp4"))
+        for how in (dict(), dict(renorm=False), dict(score="sigmoid"), dict(score="sigmoid", renorm=False)):
+            o = nv.moe_ffn_tokens(c["x"], lg, 4, c["w1"], c["w2"], **how)
+            r = nv.moe_route(lg, 4, **how)
+            assert torch.equal(o["topk_ids"], r["topk_ids"])
+            assert torch.equal(o["gate"].isnan(), r["gate"].isnan()), how
+
+
+def test_in_place(nv):
+    """The result may take the place of x."""
+    import torch
+    c = _dev(_case(14, 20, 3, 16, 16, 256, 256, "mxfp4"))
+    ref = nv.moe_ffn_tokens(c["x"], c["logits"], 3, c["w1"], c["w2"])["out"]
+    x = c["x"].clone()
+    out = nv.moe_ffn_tokens(x, c["logits"], 3, c["w1"], c["w2"], out=dict(out=x))["out"]
+    assert out is x and torch.equal(x, ref)
+
+
 def test_same_bits_and_two_streams(nv):
     """The same call gives the same bits, on two streams at once with a workspace each."""
     import torch
