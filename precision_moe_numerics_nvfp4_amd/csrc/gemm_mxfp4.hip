@@ -11,13 +11,13 @@
 // matrix unit, and the block sums are added in float32.
 //
 // What bounds it (MI355X). Large groups: the matrix unit, and above some size the
-// card's power: 31596 rows over 48 groups, 4096 -> 1536, 134 us (2.97 PFLOP/s),
+// card's power: 31596 rows over 48 groups, 4096 -> 1536, 133 us (3.1 PFLOP/s),
 // 1536 -> 4096 165 us, one group of 16384, 8192 -> 8192, 505 us (4.36 PFLOP/s; the
 // same on zeros, whose products cost less power, runs at 2.25 GHz instead of
-// 1.76). Few rows to a group: the weights' bytes, 506 rows over 48 groups 48 us for
-// 163 MB (3.4 TB/s; 288 tiles on 256 compute units, a second round of pieces),
+// 1.76). Few rows to a group: the weights' bytes, 506 rows over 48 groups 45 us for
+// 163 MB (3.6 TB/s; 288 tiles on 256 compute units),
 // 1536 -> 4096 40 us (768 tiles, 4.1 TB/s). Short contractions: the output, 8
-// groups of about 1024 rows, 1024 -> 2048, float32, 28 us for 67 MB written after
+// groups of about 1024 rows, 1024 -> 2048, float32, 24 us for 67 MB written after
 // four stages a tile.
 #include <type_traits>
 
@@ -398,14 +398,16 @@ constexpr int kStores = 8 * sizeof(OutT);   // of a wavefront and whole tile: 12
 // ranges, one per XCD (workgroup w runs on XCD w % 8), whose workgroups take
 // theirs a round at a time: those an XCD runs together share rows of both
 // operands in its L2. (Lower tiles last, for an even load, measured slower: the
-// weights are then read twice.) What is left for a last round after at most four
-// whole ones goes by halves or quarters of its rows (by halves of the columns
-// where there are few rows), where that gives no
-// workgroup a second piece: 8 x 1024 rows, 1024 -> 2048, one round and an eighth
-// 29.5 -> 26.2 us, 31000 rows over 48 groups, 4096 -> 1536, three and a half
-// 136.9 -> 134.9 us; after nine rounds, whose ends lie further apart than a
-// tile takes, it lost (1536 -> 4096 164 -> 169 us). The loads of a tile's first
-// stage go out before the rows of the tile before it are written.
+// weights are then read twice.) What does not fill a round goes by halves or
+// quarters of its rows (by halves of the columns where there are few rows), where
+// that gives no workgroup a second piece, and goes first: behind a whole tile its
+// loads would wait for that tile's rows to be written, and at the end of the grid
+// most of the card would be idle (8 x 1024 rows, 1024 -> 2048, one round and an
+// eighth: uncut 29.5, cut and last 27.5, first 24.0 us; 506 rows over 48 groups
+// 48.1 -> 44.8; 16384 x 2, 1024 -> 2048 in float32 86 -> 71; 31000 rows over 48
+// groups, three and a half rounds, 134.8 -> 133; nine rounds 166 -> 163.5). The
+// loads of a tile's first stage go out before the rows of the tile before it are
+// written.
 template <bool OUT_BF16>
 __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lsm[];
@@ -418,16 +420,11 @@ __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
   const int wide = (int)gridDim.x >> 3;     // workgroups on this XCD
   const int first = (int)((int64_t)total * x / 8), n = (int)((int64_t)total * (x + 1) / 8) - first;
   const int whole = n / wide * wide, left = n - whole;
-  const int cut = whole > 4 * wide ? 1 : 4 * left <= wide ? 4 : 2 * left <= wide ? 2 : 1;
-  auto locate = [&](int round, Tile& t) {
-    int at = round * wide + place, piece = 0, pieces = 1;
-    if (at >= whole) {
-      piece = at - whole;
-      if (piece >= left * cut) return false;
-      at = whole + piece / cut;
-      piece %= cut;
-      pieces = cut;
-    }
+  const int cut = 4 * left <= wide ? 4 : 2 * left <= wide ? 2 : 1;
+  // this workgroup's next tile
+  int round = 0;
+  bool part = place < left * cut;
+  auto place_of = [&](int at, int piece, int pieces, Tile& t) {
     at += first;
     t.g = tile_group(pre, p.G, at);
     const int64_t a0 = p.offsets[t.g], a1 = p.offsets[t.g + 1];
@@ -447,9 +444,16 @@ __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
     }
     return t.rows > 0 && t.cols > 0;
   };
-  int round = 0;
+  auto locate = [&](Tile& t) {
+    if (part) {
+      part = false;
+      if (place_of(whole + place / cut, place % cut, cut, t)) return true;
+    }
+    const int at = round++ * wide + place;
+    return at < whole && place_of(at, 0, 1, t);
+  };
   Tile t;
-  if (!locate(round, t)) return;
+  if (!locate(t)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Loads ld;
   ld.init(p, t, threadIdx.x & 63, wave);
@@ -472,7 +476,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
     else products<1>(lsm, p, ld, lane, wave, acc);
     const Tile done = t;
     stored = done.rows == 256 && done.cols == kBN;
-    const bool more = locate(++round, t);
+    const bool more = locate(t);
     if (more) {
       ld.init(p, t, lane, wave);
       ld.first(lsm, p, wave);
