@@ -415,6 +415,7 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
   const int per = (chunks + (1 << lg) - 1) >> lg, steps = (per + CH - 1) / CH;
   const int c_first = (wave & ((1 << lg) - 1)) * per, c_end = min(c_first + per, chunks);
   const int rounds = (jobs + jobs_at_once - 1) / jobs_at_once;
+  const int c_last = c_end > c_first ? c_end - 1 : chunks - 1;     // a step of fewer chunks reads its own again
 
   Own& own = owns[wave];
   // a job's list and rows; the lists of an expert take turns at the same rows
@@ -479,7 +480,7 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
       const uint8_t* row = codes + (row0 + (GATED ? i / RF * R + 16 * (i % RF) : 16 * i)) * (L / 2);
 #pragma unroll
       for (int x = 0; x < CH; ++x)
-        w[i][x] = *reinterpret_cast<const u32x4v*>(row + min(c0 + x, chunks - 1) * 64 + w_lane);
+        w[i][x] = *reinterpret_cast<const u32x4v*>(row + min(c0 + x, c_last) * 64 + w_lane);
     }
   };
   if ((int)blockIdx.x < rounds) {
