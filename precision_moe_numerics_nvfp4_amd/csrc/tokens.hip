@@ -46,12 +46,9 @@ namespace nvfp4moe {
 
 namespace {
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x2v __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
-typedef u32x4v u32x4v_4 __attribute__((aligned(4)));
 
 constexpr int kThreads = 512;
 constexpr int kWavesT = kThreads / 64;
@@ -263,7 +260,8 @@ __device__ __forceinline__ void route(const TokensArgs& a, Lists& l, float* gate
   __shared__ uint32_t members[2][kMaxExperts];               // an expert's tokens, a bit each
   __shared__ int16_t where[kMaxExperts];
   __shared__ int waves[kWavesT];
-  static_assert(2 * kThreads >= kMaxExperts && kThreads >= kTokensMaxPairs && kTokensMaxT <= 64, "one pass of the threads");
+  static_assert(2 * kThreads >= kMaxExperts && kThreads >= kTokensMaxPairs && kTokensMaxT <= 64,
+                "one pass of the threads, a bit for each token");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int i = tid; i < kMaxExperts; i += kThreads) members[0][i] = members[1][i] = 0;
   if (a.T > kSelectHere) {
@@ -338,7 +336,8 @@ typedef __attribute__((address_space(3))) void lds_void;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* p, uint32_t bytes) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uint64_t)hi << 32 | lo), (short)0,
                                            (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000);
 }
