@@ -718,8 +718,7 @@ NVFP4MOE_API size_t nvfp4moe_ffn_tokens_workspace_size(int64_t T, int k, int64_t
  *   h = act(W1[e] x[t]), gated: act(a) * b
  *   out[t] = sum over slots j with a local expert of gate[t, j] * W2[e] h
  * out [T, K] bfloat16 or float32, zero for a token without local experts.
- * Products are exact, sums float32; h, times its gate, is carried in 16
- * significant bits.
+ * Products are exact, sums float32; h, times its gate, is float32.
  * workspace: nvfp4moe_ffn_tokens_workspace_size() bytes, one call's at a time.
  * Requires T <= 64, k <= 16, T * k <= 512, k <= E <= 1024, n_local <= 1024,
  * K % 128 == 0, F % 128 == 0, K, F <= 2^20; x, codes, scales, out and

@@ -97,11 +97,10 @@ def _slope(v, act):
 
 
 def ffn_tokens(x, logits, k, w1, w2, act="silu", gated=False, score="softmax", renorm=True,
-               scale=1.0, bias=None, token_mask=None, e0=0, n_local=1, u=2.0 ** -23, h_bits=2.0 ** -16,
-               gate_rel=0.0):
+               scale=1.0, bias=None, token_mask=None, e0=0, n_local=1, u=2.0 ** -23, gate_rel=0.0):
     """dict(out, topk_ids, gate, bound): float64 results, and how far out may be
-    when sums of n terms lose n u of their magnitude, h is carried to a relative
-    h_bits and gates to gate_rel."""
+    when sums of n terms lose n u of their magnitude, h is a float32 and gates are
+    right to a relative gate_rel."""
     r = R.route(logits, k, score, renorm, scale, bias, token_mask)
     xv = Q._as_f32(x).astype(np.float64)
     W1, W2 = weight(w1), weight(w2)
@@ -123,7 +122,7 @@ def ffn_tokens(x, logits, k, w1, w2, act="silu", gated=False, score="softmax", r
                 dh = dh * np.abs(v[Fw:]) + np.abs(h) * dv[Fw:] + dh * dv[Fw:]
                 h = h * v[Fw:]
             g = r["gate"][t, j]
-            dh = dh + np.abs(h) * (h_bits + gate_rel + 4 * u)
+            dh = dh + np.abs(h) * (gate_rel + 4 * u)
             out[t] += g * (a2 @ h)
             bound[t] += g * (np.abs(a2) @ (dh + (Fw * k + 4) * u * np.abs(h)))
     return dict(out=out, topk_ids=r["topk_ids"], gate=r["gate"], bound=bound)

@@ -9,9 +9,9 @@
 // dequantized element (up to 6 significant bits) is exact in bfloat16, so the
 // products run on v_mfma_f32_16x16x32_bf16 with the weight rows as A and the
 // tokens as B. The activations are not quantized. h (with the gate and W2's outer
-// scale in it) is carried between the products as two bfloat16 parts, value and
-// remainder, 16 bits together, each with products of its own: one part would
-// cost half the output's last bit. y, a row of W2 h per pair, is float32.
+// scale in it) is carried between the products as three bfloat16 parts of eight
+// bits, which together are the float32 value, each with products of its own. y, a
+// row of W2 h per pair, is float32.
 //
 // Launches: past 16 tokens the router's own; up; down; the sum of a token's rows.
 // Up to 16 tokens every workgroup of the first product repeats the selection, a
@@ -57,6 +57,7 @@ constexpr int kMaxExperts = 1024;
 // does (16 tokens 22 us against 25, 32 tokens 102 against 98, 64 tokens 96 against 71).
 constexpr int kSelectHere = 16;
 constexpr float kNegInfT = -__builtin_huge_valf();
+constexpr int kParts = 3;                    // bfloat16 parts of a value of h
 
 // The pairs of the selected local experts in lists of up to COLS, an expert's
 // lists next to each other: in LDS, and in the workspace for the second product.
@@ -354,7 +355,11 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
   constexpr bool DOWN = KIND == kDown, GATED = KIND == kUpGated;
   constexpr int RF = GATED ? RS / 2 : RS;                    // slices of the product
   constexpr int CH = DOWN && COLS > 8 ? 1 : 2;                 // 128-element chunks of a piece
-  constexpr int PL = DOWN ? 2 : 1;                           // parts of the other operand
+  constexpr int PL = DOWN ? kParts : 1;                      // parts of the other operand
+  // Lists of 8 leave half of the matrix unit's 16 columns free: there the first two
+  // parts go side by side, the third beside zeros, and the join adds the halves.
+  constexpr bool FOLD = DOWN && COLS == 8;
+  constexpr int OPS = FOLD ? 2 : PL;                         // operands of a fragment
   constexpr int SB = NV ? 16 : 32;                           // elements of a scale
   // A wavefront's own LDS, filled by DMA. Scales: of its rows, 32 bytes of each at
   // a time (one by one they would take as many requests as the codes). Columns: a
@@ -363,6 +368,7 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
   constexpr int SSteps = SChunks / CH;                       // steps that a block of scales lasts
   constexpr int CBytes = CH * PL * 256, XQ = COLS * CBytes / 1024;
   constexpr int CLanes = CBytes / 16;                        // lanes that hold a column
+  static_assert(CH <= 2 && 64 % (16 * CH) == 0 && CLanes % (16 * CH) == 0, "a lane's chunk is the same in all loads");
   struct Own {
     uint8_t scales[RS * 16 * 32];
     uint8_t columns[COLS * CBytes];
@@ -371,10 +377,12 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
   __shared__ float gates[DOWN ? 1 : kTokensMaxPairs];
   __shared__ __attribute__((aligned(16))) Own owns[kWavesT];
   __shared__ f32x4 red[kWavesT][RS][64];
+  __shared__ __attribute__((aligned(16))) uint8_t zeros[FOLD ? CH * 256 : 16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   constexpr int words = (int)(sizeof(Lists) / 4);
   if constexpr (DOWN) {
+    if (FOLD && tid < CH * 64) reinterpret_cast<int*>(zeros)[tid] = 0;
     for (int i = tid; i < words; i += kThreads)
       reinterpret_cast<int*>(&l)[i] = reinterpret_cast<const int*>(a.ws)[i];
     __syncthreads();
@@ -390,9 +398,9 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
   const int64_t rows_e = GATED ? 2 * R : R;
   const uint8_t* codes = DOWN ? a.w2_codes : a.w1_codes;
   const uint8_t* scales = DOWN ? a.w2_scales : a.w1_scales;
-  uint16_t* hhi = reinterpret_cast<uint16_t*>(a.ws + kListBytes);
-  uint16_t* hlo = hhi + (int64_t)a.T * a.k * a.F;
-  float* y = reinterpret_cast<float*>(hlo + (int64_t)a.T * a.k * a.F);
+  uint16_t* h = reinterpret_cast<uint16_t*>(a.ws + kListBytes);    // a plane [T k, F] for each part
+  const int64_t plane = (int64_t)a.T * a.k * a.F;
+  float* y = reinterpret_cast<float*>(h + kParts * plane);
 
   const int chunks = (int)(L / 128), groups = (int)(R / (16 * RF)), jobs = l.count * groups;
   if (jobs == 0) return;
@@ -434,7 +442,7 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
   uint32_t x_lane[XQ];
   int64_t row0 = 0;
   int n_next = 0;
-  const uint32_t x_bytes = DOWN ? (uint32_t)(a.T * a.k) * (uint32_t)(4 * L) : (uint32_t)a.T * (uint32_t)(2 * L);
+  const uint32_t x_plane = (uint32_t)(DOWN ? a.T * a.k : a.T) * (uint32_t)(2 * L), x_bytes = PL * x_plane;
   auto take = [&](int q) {
     int ai, group;
     decode(min(q * jobs_at_once + mine, jobs - 1), ai, group);
@@ -445,21 +453,22 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
     for (int i = 0; i < XQ; ++i) {
       if (i * 64 / CLanes >= n_next) break;
       const int u = i * 64 + lane, col = u / CLanes, at = first + min(col, n_next - 1);
-      const int part = (u % CLanes) ^ (col & 7);             // of CH 256-byte runs, or of PL planes of them
+      const int part = (u % CLanes) ^ (col & 7);             // of PL planes, in each a run of 256 bytes a chunk
       x_lane[i] = (uint32_t)(DOWN ? l.pair[at] : l.token[at]) * (uint32_t)(2 * L) + part % 16 * 16 +
-                  (DOWN && part / (CH * 16) ? x_bytes / 2 : 0) + (CH > 1 ? part / 16 % CH << 31 : 0);
+                  (uint32_t)(part / (CH * 16)) * x_plane;
     }
   };
   // Its piece of step st. The columns and scales before the codes: loads return
   // in order.
   auto load = [&](int st) {
     const int c0 = min(c_first + st * CH, chunks - 1);
-    const auto xr = resource(DOWN ? static_cast<const void*>(hhi) : a.x, x_bytes);
+    const auto xr = resource(DOWN ? static_cast<const void*>(h) : a.x, x_bytes);
+    // runs of chunks take turns, 16 lanes each; one behind the row's end reads the last again
+    const uint32_t x_at = c0 * 256 + (CH > 1 && lane / 16 % 2 && c0 + 1 < chunks ? 256 : 0);
 #pragma unroll
     for (int i = 0; i < XQ; ++i) {
       if (i * 64 / CLanes >= n_next) break;
-      uint32_t at = x_lane[i] + c0 * 256;
-      if (CH > 1) at = (at & 0x7FFFFFFFu) + (x_lane[i] >> 31 && c0 + 1 < chunks ? 256 : 0);
+      const uint32_t at = x_lane[i] + x_at;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(own.columns + i * 1024), 16, at, 0, 0, 0);
     }
     if (st % SSteps == 0) {
@@ -506,16 +515,21 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
       for (int i = 0; i < RS; ++i)
 #pragma unroll
         for (int x = 0; x < CH; ++x) asm volatile("" ::"v"(wc[i][x]) : "memory");
-      bf16x8 b[CH][PL][4];                   // columns past the list: some other's, they go nowhere
-      const int col = min(r, n - 1);
+      bf16x8 b[CH][OPS][4];                  // columns past the list: some other's, they go nowhere
+      const int col = min(FOLD ? r & 7 : r, n - 1);
 #pragma unroll
       for (int x = 0; x < CH; ++x)
 #pragma unroll
-        for (int u = 0; u < PL; ++u)
+        for (int u = 0; u < OPS; ++u) {
+          const uint8_t* from = own.columns + col * CBytes + u * (CH * 256);
+          if constexpr (FOLD) {
+            if (u == 0) from += r >= 8 ? CH * 256 : 0;
+            else from = r >= 8 ? zeros : own.columns + col * CBytes + 2 * (CH * 256);
+          }
 #pragma unroll
           for (int m = 0; m < 4; ++m)
-            b[x][u][m] = *reinterpret_cast<const bf16x8*>(
-                own.columns + col * CBytes + ((((u * CH + x) * 16 + g * 4 + m) ^ (col & 7)) << 4));
+            b[x][u][m] = *reinterpret_cast<const bf16x8*>(from + (((x * 16 + g * 4 + m) ^ (col & 7)) << 4));
+        }
       uint32_t sc[RS][CH];
 #pragma unroll
       for (int i = 0; i < RS; ++i) {
@@ -542,7 +556,7 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
           for (int m = 0; m < 4; ++m) {
             const bf16x8 f = dequant<NV>(wc[i][x], sc[i][x], m);
 #pragma unroll
-            for (int u = 0; u < PL; ++u)
+            for (int u = 0; u < OPS; ++u)
               acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, b[x][u][m], acc[i], 0, 0, 0);
           }
       }
@@ -562,6 +576,7 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
       f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f}, u = v;
       for (int i = 0; i < 1 << lg; ++i) {
         v += red[(jm << lg) + i][s][li];
+        if constexpr (FOLD) v += red[(jm << lg) + i][s][li + 8];
         if constexpr (GATED) u += red[(jm << lg) + i][RF + s][li];
       }
       const int e = l.expert[aj], p = l.pair[l.first[aj] + col];
@@ -571,20 +586,27 @@ __global__ __launch_bounds__(kThreads) void k_tokens_product(TokensArgs a) {
       } else {
         const float o1 = NV ? a.w1_outer[e] : 1.0f;
         const float go = gates[p] * (NV ? a.w2_outer[e] : 1.0f);
-        float h[4], lo[4];
+        uint32_t part[kParts][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          h[i] = activate(v[i] * o1, a.act);
-          if constexpr (GATED) h[i] *= u[i] * o1;
-          h[i] *= go;
+          float f = activate(v[i] * o1, a.act);
+          if constexpr (GATED) f *= u[i] * o1;
+          f *= go;
+          // the bits cut off are exact in the next part; what is not finite has only a first one
+          const bool finite = fabsf(f) < __builtin_huge_valf();
+          part[0][i] = finite ? f2u(f) : pk_bf16(f, f);
+#pragma unroll
+          for (int j = 1; j < kParts; ++j) {
+            f = finite ? f - u2f(part[j - 1][i] & 0xFFFF0000u) : 0.0f;
+            part[j][i] = f2u(f);
+          }
         }
-        const uint32_t h01 = pk_bf16(h[0], h[1]), h23 = pk_bf16(h[2], h[3]);
-        lo[0] = h[0] - u2f(h01 << 16);
-        lo[1] = h[1] - u2f(h01 & 0xFFFF0000u);
-        lo[2] = h[2] - u2f(h23 << 16);
-        lo[3] = h[3] - u2f(h23 & 0xFFFF0000u);
-        *reinterpret_cast<uint2*>(hhi + at) = make_uint2(h01, h23);
-        *reinterpret_cast<uint2*>(hlo + at) = make_uint2(pk_bf16(lo[0], lo[1]), pk_bf16(lo[2], lo[3]));
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) {
+          const uint32_t* q = part[j];
+          *reinterpret_cast<uint2*>(h + j * plane + at) =
+              make_uint2(q[0] >> 16 | (q[1] & 0xFFFF0000u), q[2] >> 16 | (q[3] & 0xFFFF0000u));
+        }
       }
     }
     __syncthreads();
@@ -597,7 +619,7 @@ __global__ __launch_bounds__(256) void k_tokens_sum(TokensArgs a) {
   const int t = blockIdx.y;
   const int64_t col = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (col >= a.K) return;
-  const float* y = reinterpret_cast<const float*>(a.ws + kListBytes + (int64_t)a.T * a.k * a.F * 4) +
+  const float* y = reinterpret_cast<const float*>(a.ws + kListBytes + (int64_t)a.T * a.k * a.F * (2 * kParts)) +
                    (int64_t)t * a.k * a.K + col;
   const int32_t* ids = a.topk_ids + (int64_t)t * a.k;
   f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -636,9 +658,9 @@ hipError_t product(const TokensArgs& a, unsigned grid, hipStream_t stream) {
 
 }  // namespace
 
-// The lists, h in two bfloat16 parts, y in float32, by pair.
+// The lists, h in bfloat16 parts, y in float32, by pair.
 size_t tokens_workspace_bytes(int64_t T, int k, int64_t K, int64_t F) {
-  return kListBytes + (size_t)(T * k * (K + F)) * 4;
+  return kListBytes + (size_t)(T * k) * (size_t)(4 * K + 2 * kParts * F);
 }
 
 hipError_t launch_ffn_tokens(const TokensArgs& a, hipStream_t stream) {
