@@ -102,7 +102,7 @@ __device__ __forceinline__ uint64_t order_key(double v) {
 }
 __device__ __forceinline__ uint32_t order_key(float v) {
   if (!(v > kNegInfT)) return 0;
-  const uint32_t b = f2u(v);
+  const uint32_t b = f2u(v + 0.0f);        // + 0: -0 is +0, as comparisons have it
   return b >> 31 ? ~b : b | 0x80000000u;
 }
 
