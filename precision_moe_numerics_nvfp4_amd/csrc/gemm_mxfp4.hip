@@ -223,8 +223,8 @@ struct Loads {
 #pragma unroll
     for (int i = 0; i < 4; ++i) b(lsm, p, 0, wave, i);
   }
-  // The scales of stages 2 b and 2 b + 1 (those behind the row's end belong to
-  // codes of zero).
+  // The scales of stages 2 b and 2 b + 1 (those behind the row's end are another
+  // row's, and are not used).
   __device__ __forceinline__ void scales(uint8_t* lsm, const Gemm& p, int b, int wave) const {
     const bool real = b * 512 < p.K;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -323,11 +323,14 @@ __device__ __forceinline__ void products(uint8_t* lsm, const Gemm& p, const Load
   auto stage = [&](int b, auto at) {
     constexpr int Q = decltype(at)::value;
     const int s = 2 * b + Q;
+    // The scales of half a stage; of a second half behind the row's end 2^-127: the
+    // bytes there may be any, and 255 (NaN) times the codes' zeros would be NaN.
     auto shift = [&](int d) {
+      const uint32_t real = d % 2 == 0 || 512 * b + 128 * d < (int)p.K ? ~0u : 0u;
 #pragma unroll
-      for (int i = 0; i < TM; ++i) ca[i] = sA[i][d] >> (8 * half);
+      for (int i = 0; i < TM; ++i) ca[i] = (sA[i][d] >> (8 * half)) & real;
 #pragma unroll
-      for (int j = 0; j < TN; ++j) cb[j] = sB[j][d] >> (8 * half);
+      for (int j = 0; j < TN; ++j) cb[j] = (sB[j][d] >> (8 * half)) & real;
     };
     shift(2 * Q);
     step(std::integral_constant<int, 0>{}, s, -1, [&](int i) {
