@@ -228,7 +228,7 @@ __device__ __forceinline__ bf16x8 dequant(const u32x4v w, uint32_t s, int m) {
 __device__ __forceinline__ float activate(float v, int act) {
   if (act == 2) return v / (1.0f + expf(-v));
   if (act == 1) {
-    v = fmaxf(v, 0.0f);
+    v = v < 0.0f ? 0.0f : v;                 // NaN stays
     return v * v;
   }
   return v;

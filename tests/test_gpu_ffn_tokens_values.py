@@ -89,3 +89,34 @@ def test_h_next_to_the_largest_float32(nv, T, E):
     big = np.finfo(np.float32).max
     want = np.where(np.arange(T)[:, None] % 2 == 0, -big, big) * np.ones((1, 128))
     assert np.array_equal(got, want.astype(np.float32))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", ["none", "relu2", "silu"])
+@pytest.mark.parametrize("T,E", SIZES)
+def test_nan_reaches_its_token_and_no_other(nv, T, E, act, gated, fmt):
+    """A NaN in x, or in an expert's outer scale, is NaN in the output of the tokens that meet it; the others keep
+    their bits."""
+    rng = np.random.default_rng(T + E)
+    cols = lambda n, rows: [rng.choice(n, 3, replace=False) for _ in range(rows)]
+    w1 = _picking(cols(256, 256 if gated else 128), 256 if gated else 128, 256, fmt, E)
+    w2 = _picking(cols(128, 256), 256, 128, fmt, E)
+    x = rng.integers(-8, 9, (T, 256)).astype(np.float64)
+    clean = _run(nv, x, w1, w2, E, act=act, gated=gated)
+    assert np.isfinite(clean).all()
+    bad = np.arange(T) % 3 == 0
+    x[bad, rng.integers(0, 256, bad.sum())] = np.nan
+    got = _run(nv, x, w1, w2, E, act=act, gated=gated)
+    assert np.isnan(got[bad]).all() and np.array_equal(got[~bad], clean[~bad])
+    if fmt == "nvfp4":
+        x[bad] = 1.0
+        clean = _run(nv, x, w1, w2, E, act=act, gated=gated)
+        lg = np.random.default_rng(3).normal(size=(T, E)).astype(np.float32)
+        met = lg.argmax(axis=1) == lg[0].argmax()
+        for i in (0, 1):
+            w = [list(w1), list(w2)]
+            w[i][2] = w[i][2].copy()
+            w[i][2][lg[0].argmax()] = np.nan
+            got = _run(nv, x, *map(tuple, w), E, act=act, gated=gated)
+            assert np.isnan(got[met]).all() and np.array_equal(got[~met], clean[~met])
