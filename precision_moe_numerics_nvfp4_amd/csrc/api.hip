@@ -59,7 +59,8 @@ int grad_list_status(const void* const* grads, void* const* outs, const int* dty
 }
 
 // A launch holds less than 2^32 threads: the quantizers take 16 elements a
-// thread at least, the tiled kernels 256 threads a tile.
+// thread at least (the way back to values goes in pieces), the tiled kernels 256
+// threads a tile.
 constexpr int64_t kMaxElems = (int64_t)1 << 35;
 constexpr int64_t kMaxTiles = (int64_t)1 << 23;
 // Widths of the few-token layer.

@@ -1,0 +1,41 @@
+"""The MXFP4 calls at the largest sizes that their contract names."""
+
+import numpy as np
+import pytest
+
+from helpers import ensure_built, from_dev, to_dev
+from oracle import mxfp4 as M4
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def nv():
+    ensure_built()
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import precision_moe_numerics_nvfp4_amd as nv
+    yield nv
+    torch.cuda.empty_cache()
+
+
+def test_dequantize_the_largest_size(nv):
+    """2^35 - 32 float32 values: rows at both ends, and at every 2^31 values between."""
+    import torch
+    rows = (1 << 30) - 1
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 160 << 30:
+        pytest.skip("needs 160 GiB of free device memory")
+    codes = torch.zeros(rows, 16, dtype=torch.uint8, device="cuda")
+    scales = torch.full((rows, 1), 127, dtype=torch.uint8, device="cuda")
+    at = np.unique(np.clip(np.arange(0, 17)[:, None] * (1 << 26) + np.arange(-2, 3), 0, rows - 1))
+    rng = np.random.default_rng(1)
+    c, s = rng.integers(0, 256, (len(at), 16)).astype(np.uint8), rng.integers(100, 150, (len(at), 1)).astype(np.uint8)
+    codes[to_dev(at)], scales[to_dev(at)] = to_dev(c), to_dev(s)
+    out = torch.full((rows, 32), -7.0, device="cuda")
+    nv.mxfp4_dequantize(codes, scales, out=out)
+    got = from_dev(out[to_dev(at)])
+    assert np.array_equal(got, M4.dequantize(c, s).astype(np.float32))
+    out[to_dev(at)] = 0.0
+    step = 1 << 25
+    assert all(not out[i:i + step].any() for i in range(0, rows, step))     # every other value is zero
