@@ -679,7 +679,9 @@ NVFP4MOE_API int moe_group(const int32_t* topk_ids, int64_t T, int k, int e0, in
  *   float32 or bfloat16 (round to nearest even). Products and the sums of a
  *   block of 32 are exact, the blocks are added in float32. Rows >= offsets[G]
  *   untouched. Requires N % 128 == 0, K % 128 == 0, K < 2^23, G <= 4000,
- *   m_cap < 2^31, a_rows < 2^31, scales 4-byte aligned.
+ *   m_cap < 2^31, a_rows < 2^31, scales 4-byte aligned, and
+ *   (N + 255) / 256 < 2^31 / (m_cap / 256 + G + 1); where rows are gathered from
+ *   2 GiB of codes and more, N / 128 < 2^23 / (m_cap / 32 + G + 1).
  */
 NVFP4MOE_API int moe_fwd_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a_rows,
                                const int32_t* row_token, const uint8_t* b_codes,
@@ -694,7 +696,7 @@ NVFP4MOE_API int moe_fwd_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_
  * {0, rows_per_group, ...}), both as mxfp8_requant_sr writes them.
  * row_token int32 or NULL (activations only): the row of codes/scales that
  * grouped row r reads; entries outside [0, rows) are taken as rows of zeros.
- * Requires cols % 128 == 0, P % 32 == 0.
+ * Requires cols % 128 == 0, P % 32 == 0, P / 128 + 1 < 2^23 / (cols / 128).
  */
 NVFP4MOE_API int mxfp8_requant_sr_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows,
                            int64_t cols, const int32_t* row_token, int64_t rows_per_group,

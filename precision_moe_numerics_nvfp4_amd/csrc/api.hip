@@ -606,7 +606,10 @@ int moe_fwd_grouped_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, 
   REQUIRE(row_token || a_rows >= m_cap, NVFP4MOE_EINVAL);
   REQUIRE(N % 128 == 0 && K % 128 == 0 && K > 0 && K < (int64_t)1 << 23, NVFP4MOE_EUNSUPPORTED);
   REQUIRE(G <= 4000 && m_cap < (int64_t)1 << 31 && a_rows < (int64_t)1 << 31, NVFP4MOE_EUNSUPPORTED);
-  REQUIRE(N / 128 < kMaxTiles / (m_cap / 32 + G + 1), NVFP4MOE_EUNSUPPORTED);
+  if (fwd_mxfp4_wide(row_token != nullptr, a_rows, K))       // a workgroup to each 32 x 128
+    REQUIRE(N / 128 < kMaxTiles / (m_cap / 32 + G + 1), NVFP4MOE_EUNSUPPORTED);
+  else                                                        // tiles of 256 x 256, counted in an int
+    REQUIRE((N + 255) / 256 < ((int64_t)1 << 31) / (m_cap / 256 + G + 1), NVFP4MOE_EUNSUPPORTED);
   REQUIRE(aligned16(a_codes) && aligned16(b_codes) && aligned16(y) && aligned(a_scales, 4) &&
               aligned(b_scales, 4) && aligned(row_token, 4) && aligned(offsets, 8),
           NVFP4MOE_EUNSUPPORTED);

@@ -519,12 +519,16 @@ hipError_t tiles(const Gemm& p, int64_t most, hipStream_t stream) {
 
 }  // namespace
 
+// The tiles address the rows they gather by 32 bits, in place a tile's own rows.
+bool fwd_mxfp4_wide(bool gathers, int64_t a_rows, int64_t K) {
+  return (gathers ? a_rows : 256) * (K / 2) >= (int64_t)1 << 31;
+}
+
 hipError_t launch_fwd_mxfp4(const uint8_t* ac, const uint8_t* as, int64_t a_rows,
                             const int32_t* row_token, const uint8_t* bc, const uint8_t* bs,
                             const int64_t* offsets, int G, int64_t m_cap, int64_t N, int64_t K,
                             void* y, bool y_bf16, hipStream_t stream) {
-  const int64_t a_bytes = (row_token ? a_rows : 256) * (K / 2);
-  if (a_bytes < (int64_t)1 << 31) {
+  if (!fwd_mxfp4_wide(row_token != nullptr, a_rows, K)) {
     const Gemm p{ac, as, bc, bs, row_token, offsets, a_rows, N, K, y, G};
     const int64_t most = ((m_cap + 255) / 256 + G) * ((N + kBN - 1) / kBN);
     return y_bf16 ? tiles<true>(p, most, stream) : tiles<false>(p, most, stream);

@@ -137,6 +137,7 @@ hipError_t launch_fwd_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scal
                                    int64_t K, void* y, bool y_bf16, hipStream_t stream);
 
 // gemm_mxfp4.hip
+bool fwd_mxfp4_wide(bool gathers, int64_t a_rows, int64_t K);   // which of its two kernels
 hipError_t launch_fwd_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a_rows,
                             const int32_t* row_token, const uint8_t* b_codes,
                             const uint8_t* b_scales, const int64_t* offsets, int G, int64_t m_cap,

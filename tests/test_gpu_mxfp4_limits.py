@@ -39,3 +39,25 @@ def test_dequantize_the_largest_size(nv):
     out[to_dev(at)] = 0.0
     step = 1 << 25
     assert all(not out[i:i + step].any() for i in range(0, rows, step))     # every other value is zero
+
+
+def test_product_of_many_possible_tiles(nv):
+    """A capacity of 2^20 rows and 32768 columns, of which the groups fill a few rows."""
+    import torch
+    cap, N, K, G = 1 << 20, 32768, 128, 2
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GiB of free device memory")
+    rng = np.random.default_rng(2)
+    a = M4.quantize(rng.normal(size=(40, K)).astype(np.float32))
+    b = M4.quantize((rng.normal(size=(G * N, K)) * 0.02).astype(np.float32))
+    off = np.array([0, 70, 300])
+    tok = torch.zeros(cap, dtype=torch.int32, device="cuda")
+    m = rng.integers(0, 40, 300).astype(np.int32)
+    tok[:300] = to_dev(m)
+    y = torch.empty(cap, N, dtype=torch.bfloat16, device="cuda")
+    y[300:400] = -7.0
+    nv.moe_fwd_grouped_gemm_mxfp4(*map(to_dev, a), *map(to_dev, b), to_dev(off), row_token=tok, y=y)
+    ref, mag = M4.fwd_grouped(a, b, off, N, m)
+    bound = (K / 32 + 1) * 2.0 ** -23 * mag + 2.0 ** -8 * np.abs(ref)
+    assert (np.abs(y[:300].double().cpu().numpy() - ref) <= bound).all() and (y[300:400] == -7.0).all()
