@@ -13,10 +13,9 @@
 // bits, which together are the float32 value, each with products of its own. y, a
 // row of W2 h per pair, is float32.
 //
-// Launches: past 16 tokens the router's own; up; down; the sum of a token's rows.
-// Up to 16 tokens every workgroup of the first product repeats the selection, a
-// wavefront to a token (16 tokens x 8 experts: 22.6 us the layer against 25.1
-// with the router's launch; 32 x 48: 102 against 98).
+// Launches: the router's own; up; down; the sum of a token's rows. For a few tokens
+// of few experts every workgroup of the first product repeats the selection
+// instead, a wavefront to a token.
 //
 // What bounds it is the weights' bytes in flight: each selected expert's weights
 // are read once (a list of pairs at a time), the operations are few. So a
@@ -53,9 +52,19 @@ typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 512;
 constexpr int kWavesT = kThreads / 64;
 constexpr int kMaxExperts = 1024;
-// Up to so many tokens every workgroup selects by itself; beyond, a launch before
-// does (16 tokens 22 us against 25, 32 tokens 102 against 98, 64 tokens 96 against 71).
-constexpr int kSelectHere = 16;
+// Where every workgroup of the first product selects by itself; else a launch
+// before it does. By itself it saves the launch and pays for rows and experts. The
+// layer (1024 -> 512 -> 1024) in a graph, by itself against with the launch: an
+// expert a lane, 1 to 8 tokens of 48 experts 19.6 to 20.7 us against 21.5 to 22.4, 16
+// tokens 23.2 against 23.0 (with a bias 25.6 against 24.4; of 8 experts, called one
+// by one, 20.6 against 21.8), 32 tokens of a larger layer 102 against 98. Six
+// experts a lane (384), 1 to 8 tokens 20.6 to 21.8 against 20.5 to 22.4 (called one
+// by one 21.0 to 22.2 against 21.8 to 22.8), 12 tokens 24.0 against 21.8, 16 24.5
+// against 21.6; with a bias, whose keys take 64 bits, 21.8 to 29.9 against 21.0 to
+// 21.9. Sixteen a lane (1024) 21.9 to 30.0 against 21.2 to 22.6.
+__host__ __device__ inline bool selects_here(const TokensArgs& a) {
+  return a.E <= 64 ? a.T <= 16 : a.E <= 384 && !a.bias && a.T <= 8;
+}
 constexpr float kNegInfT = -__builtin_huge_valf();
 constexpr int kParts = 3;                    // bfloat16 parts of a value of h
 
@@ -265,19 +274,17 @@ __device__ __forceinline__ void route(const TokensArgs& a, Lists& l, float* gate
                 "one pass of the threads, a bit for each token");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int i = tid; i < kMaxExperts; i += kThreads) members[0][i] = members[1][i] = 0;
-  if (a.T > kSelectHere) {
+  if (!selects_here(a)) {
     if (tid < a.T * a.k) {
       ids[tid] = a.topk_ids[tid];
       gates[tid] = a.gate[tid];
     }
   } else if (a.bias) {
-    if (a.E <= 64) select_all<1, true>(a, ids, gates);
-    else if (a.E <= 384) select_all<6, true>(a, ids, gates);
-    else select_all<16, true>(a, ids, gates);
+    select_all<1, true>(a, ids, gates);
+  } else if (a.E <= 64) {
+    select_all<1, false>(a, ids, gates);
   } else {
-    if (a.E <= 64) select_all<1, false>(a, ids, gates);
-    else if (a.E <= 384) select_all<6, false>(a, ids, gates);
-    else select_all<16, false>(a, ids, gates);
+    select_all<6, false>(a, ids, gates);
   }
   __syncthreads();
   // A token selects an expert at most once: a pair's place in its expert's lists
@@ -666,7 +673,7 @@ size_t tokens_workspace_bytes(int64_t T, int k, int64_t K, int64_t F) {
 hipError_t launch_ffn_tokens(const TokensArgs& a, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
   hipError_t e = hipSuccess;
-  if (a.T > kSelectHere)
+  if (!selects_here(a))
     e = launch_route(a.logits, a.logits_bf16, a.T, a.E, a.k, a.sigmoid, a.renorm, a.scale, a.bias,
                      a.token_mask, a.topk_ids, a.gate, nullptr, nullptr, nullptr, stream);
   if (e != hipSuccess) return e;
