@@ -10,14 +10,18 @@
 // values are multiples of 1/4 up to 36, so a block's sum is exact in the
 // matrix unit, and the block sums are added in float32.
 //
-// What bounds it (MI355X). Large groups: the matrix unit, and above some size the
-// card's power: 31596 rows over 48 groups, 4096 -> 1536, 133 us (3.1 PFLOP/s),
-// 1536 -> 4096 165 us, one group of 16384, 8192 -> 8192, 505 us (4.36 PFLOP/s; the
-// same on zeros, whose products cost less power, runs at 2.25 GHz instead of
-// 1.76). Few rows to a group: the weights' bytes, 506 rows over 48 groups 45 us for
-// 163 MB (3.6 TB/s; 288 tiles on 256 compute units),
-// 1536 -> 4096 40 us (768 tiles, 4.1 TB/s). Short contractions: the output, 8
-// groups of about 1024 rows, 1024 -> 2048, float32, 24 us for 67 MB written after
+// What bounds it (MI355X). Large groups: the wait for a stage, of which one at most
+// is on its way. Tiles of 256 x 256 on all compute units take 1.72 us a stage (5.0
+// PFLOP/s) and 6.3 us each from one to the next (whole rounds of them, contractions
+// of 1024 to 8192). One group of 16384, 8192 -> 8192: 500 us (4.4 PFLOP/s), the
+// matrix unit busy 71% of the cycles, at 1.76 GHz for the card's power (on zeros,
+// whose products cost less, 2.25 GHz and the same cycles). 31596 rows over 48
+// groups, 4096 -> 1536: 133 us (2.99 PFLOP/s), busy 42 to 50%: 27.5 us of stages a
+// tile beside those 6.3, three and a half rounds in the time of four, the tiles'
+// rows filled to 84%; 1536 -> 4096 165 us. Few rows to a group: the weights' bytes,
+// 506 rows over 48 groups 45 us for 163 MB (3.6 TB/s; 288 tiles on 256 compute
+// units), 1536 -> 4096 40 us (768 tiles, 4.1 TB/s). Short contractions: the output,
+// 8 groups of about 1024 rows, 1024 -> 2048, float32, 24 us for 67 MB written after
 // four stages a tile.
 #include <type_traits>
 
@@ -38,9 +42,10 @@ __device__ __forceinline__ i32x8 frag(const uint4 v) {
 
 // Gathered activations of 2 GiB and more, past the 32-bit offsets of the tiles
 // below: 32 rows x 128 columns per workgroup, a wavefront to 32 columns,
-// fragments straight from global memory. (For all else the tiles are faster, a
-// few rows to a group included: 506 rows over 48 groups, 4096 -> 1536, 49.7 us
-// against 78.)
+// fragments straight from global memory. Each fragment waits for its loads: rows
+// gathered from 1050000 tokens (2.0 GiB) against tiles and 1040000, 4096 -> 1536: 506
+// rows over 48 groups 57 us against 34, 8192 over 8 269 against 32, 31596 over 48
+// 1088 against 131. So the tiles take all else.
 template <bool OUT_BF16>
 __global__ __launch_bounds__(256) void k_mxfp4_wide(
     const uint8_t* __restrict__ ac, const uint8_t* __restrict__ as, int64_t a_rows,
@@ -409,8 +414,9 @@ constexpr int kStores = 8 * sizeof(OutT);   // of a wavefront and whole tile: 12
 // eighth: uncut 29.5, cut and last 27.5, first 24.0 us; 506 rows over 48 groups
 // 48.1 -> 44.8; 16384 x 2, 1024 -> 2048 in float32 86 -> 71; 31000 rows over 48
 // groups, three and a half rounds, 134.8 -> 133; nine rounds 166 -> 163.5). The
-// loads of a tile's first stage go out before the rows of the tile before it are
-// written.
+// loads of a tile's first stage are asked for before the rows of the tile before it
+// are written, which then wait for them: the compiler cannot tell the rows' staging
+// from the loads' place in LDS.
 template <bool OUT_BF16>
 __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lsm[];
@@ -468,7 +474,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void k_mxfp4_tiles(Gemm p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) ld.a(lsm, 1, wave, i);
     // the first stage: all but these loads, and the stores between them (of a
-    // whole tile; of a partial one some may not have been issued)
+    // whole tile; of a partial one some may not have been issued), which go on
     if (stored) wait_barrier<4 + kStores<OutT>>();
     else wait_barrier<4>();
     f32x16 acc[4][kTN];

@@ -19,8 +19,11 @@
 //
 // What bounds it is the weights' bytes in flight: each selected expert's weights
 // are read once (a list of pairs at a time), the operations are few. So a
-// wavefront holds one piece, 64 rows of 128 or 256 elements, in registers while
-// the next is on its way, and what else has to be read comes in few requests:
+// wavefront holds one piece of its job, 64 rows of 128 or 256 elements, in registers
+// while the job's next is on its way (the first piece of its next job is asked for
+// with the last of this one, but the join of the sums waits for it: the registers
+// are loaded under branches, and what joins behind a branch is copied there), and
+// what else has to be read comes in few requests:
 // the scales 32 bytes of a row at a time, the columns (tokens or h) a line at a
 // time, both by DMA to the wavefront's own LDS (a byte of scale and a fragment of
 // column a lane, straight to registers, took as many requests as the weights: 7
@@ -30,11 +33,15 @@
 // many wavefronts as gives the fewest steps, joined through LDS.
 //
 // Measured (MI355X): one token, 8 of 48 experts, 4096 -> 1536 -> 4096, NVFP4, 57
-// MB: 30 us, of it up 16 (1.7 launch, 3 selection and lists), down 12.5, sum 3.8;
-// 7 tokens, 6 of 48 experts, gated 4096 -> 2 x 2048 -> 4096, MXFP4, 390 MB: 85 us,
-// 4.6 TB/s; 64 tokens, 48 of 384 experts, NVFP4, 240 MB: 68 us, 3.5 TB/s (its
-// conversions, four vector instructions to two elements, are busy for half of
-// it, and the rounds of jobs do not come out even). Not kept: the last workgroup
+// MB: 31 us, of it up 16.5 (1.7 launch, 3 selection and lists), down 12.8 (the lists
+// come a dword a lane, four times one after the other), sum 3.9; 7 tokens, 6 of 48
+// experts, gated 4096 -> 2 x 2048 -> 4096, MXFP4, 390 MB: 87 us, 4.5 TB/s; 64 tokens,
+// 48 of 384 experts, NVFP4, 240 MB: 69.5 us, 3.5 TB/s (its conversions, four vector
+// instructions to two elements, are busy for half of it, the joins of jobs wait for
+// the next one's weights, and the rounds of jobs do not come out even); 64 tokens x
+// 8 on 48 experts (lists of 16), MXFP4, 118 us, 2.7 TB/s. h in two parts, 16 bits of
+// it, measured 30.1, 85.5, 68.2 and 110 us and left float32 results 2.5e-6 from 64
+// bits; with three 2.1e-7. Not kept: the last workgroup
 // to finish 64 columns adds their rows in the down launch (64 tokens 127 us for
 // 72, 7 tokens 96 for 89: every job waits for its rows to reach memory).
 #include "codecs.hpp"
@@ -652,10 +659,10 @@ __global__ __launch_bounds__(256) void k_tokens_sum(TokensArgs a) {
 }
 
 // Lists of 8 pairs leave the second product room for two chunks of weights in
-// flight (7 tokens over 48 experts, one pair an expert, 88 us against 96 with
-// lists of 16; 16 x 8 over 48 86 against 95; 40 x 8 over 48, 6.7 each, 99 against
-// 108). Lists of 16 read a busy expert's weights half as often (64 x 2 over 8, 16
-// each, 36 us against 45; 64 x 8 over 48, 10.7 each, 116 against 128).
+// flight (7 tokens over 48 experts, one pair an expert, 87 us against 91 with
+// lists of 16; 16 x 8 over 48 85 against 90; 40 x 8 over 48, 6.7 each, 100 against
+// 107). Lists of 16 read a busy expert's weights half as often (64 x 2 over 8, 16
+// each, 36 us against 44; 64 x 8 over 48, 10.7 each, 118 against 129).
 template <bool NV, Kind KIND>
 hipError_t product(const TokensArgs& a, unsigned grid, hipStream_t stream) {
   auto k = a.T * a.k > 7 * a.E ? k_tokens_product<NV, KIND, 16> : k_tokens_product<NV, KIND, 8>;
