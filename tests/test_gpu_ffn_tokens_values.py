@@ -120,3 +120,29 @@ def test_nan_reaches_its_token_and_no_other(nv, T, E, act, gated, fmt):
             w[i][2][lg[0].argmax()] = np.nan
             got = _run(nv, x, *map(tuple, w), E, act=act, gated=gated)
             assert np.isnan(got[met]).all() and np.array_equal(got[~met], clean[~met])
+
+
+@pytest.mark.parametrize("E", [8, 80])
+def test_the_largest_h(nv, E):
+    """512 pairs of 2^20 values: the parts of h end past 3 GiB. Lists of 16 and of 8."""
+    import torch
+    T, k, K, Fw, local = 64, 8, 128, 1 << 20, 7
+    rng = np.random.default_rng(E)
+    x = rng.choice([-1.0, 1.0], (T, K)) * rng.integers(1, 257, (T, K))
+    lg = np.full((T, E), -20.0, np.float32)
+    lg[:, :k] = 4.0                                      # slot j is expert j, its gate 1/8; one of them is local
+    w1c = np.zeros((Fw, K // 2), np.uint8)
+    j = np.arange(Fw)
+    col = (j * 37 + j // K) % K                          # h[j] = x[col[j]]
+    w1c[j, col // 2] = np.where(col % 2, ONE << 4, ONE)
+    w2c = np.zeros((K, Fw // 2), np.uint8)
+    pick = np.concatenate([rng.integers(0, Fw, (K, 4)), Fw - 1 - np.arange(K)[:, None], np.arange(K)[:, None]], axis=1)
+    for r in range(K):
+        for c in set(pick[r].tolist()):
+            w2c[r, c // 2] |= ONE << 4 if c % 2 else ONE
+    ones = lambda rows, cols: torch.full((rows, cols // 32), 127, dtype=torch.uint8, device="cuda")
+    o = nv.moe_ffn_tokens(to_dev(gen.to_bf16_bits(x.astype(np.float32))), to_dev(lg), k, (to_dev(w1c), ones(Fw, K)),
+                          (to_dev(w2c), ones(K, Fw)), act="none", e0=local, out_dtype=torch.float32)
+    assert (from_dev(o["topk_ids"]) == np.arange(k)).all() and (from_dev(o["gate"]) == 0.125).all()
+    want = np.stack([x[:, col[sorted(set(pick[r].tolist()))]].sum(axis=1) for r in range(K)], axis=1) / 8
+    assert np.array_equal(from_dev(o["out"]), want.astype(np.float32))
